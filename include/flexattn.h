@@ -65,7 +65,10 @@ enum {
 /* ----------------------------------------------------------------------- */
 enum {
   FA_DTYPE_BF16 = 0, /* bfloat16 storage, fp32 arithmetic and accumulation  */
-  FA_DTYPE_F32 = 1   /* fp32 storage and arithmetic                         */
+  FA_DTYPE_F32 = 1,  /* fp32 storage and arithmetic                         */
+  FA_DTYPE_E4M3 = 2  /* 8-bit floats (4 exponent, 3 mantissa bits, no infinity) under a
+                        scale per block of tokens and head: caches only (fa_kv_cache,
+                        flexattn_forward_fp8)                                */
 };
 
 /* ----------------------------------------------------------------------- */
@@ -403,6 +406,169 @@ int flexattn_backward(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v
                       const fa_tensor* dv, float scale, int32_t enable_gqa, const fa_score_mod* score_mod,
                       const fa_mask_mod* mask_mod, const fa_block_mask* block_mask,
                       const fa_block_mask_q* block_mask_q, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ----------------------------------------------------------------------- */
+/* Query / key preparation: a norm per head and the position rotation       */
+/* ----------------------------------------------------------------------- */
+
+/* Root-mean-square norm of one head's row x (D elements):
+ *   u = x * r * w,  r = (mean(x^2) + eps)^(-1/2). */
+typedef struct fa_head_norm {
+  const void* weight;    /* device [D], contiguous, or NULL for w = 1                     */
+  int32_t weight_dtype;  /* FA_DTYPE_BF16 or FA_DTYPE_F32                                 */
+  float eps;             /* finite, >= 0                                                  */
+} fa_head_norm;
+
+/* Rotation of the first rot_dim elements of a row in pairs (a, b) by the angle
+ * t_i = pos * inv_freq[i], i < rot_dim / 2:
+ *   a' = a cos t_i - b sin t_i,   b' = b cos t_i + a sin t_i;
+ * the elements from rot_dim on pass through.  The product pos * inv_freq[i] is
+ * formed and reduced to one turn in 64 bits, so far positions keep their angle. */
+typedef struct fa_rope {
+  const float* inv_freq; /* device fp32 [rot_dim / 2], radians per position               */
+  const int32_t* pos;    /* device int32 [pos_batch, N] positions, or NULL: token n of the
+                            call is at n (flexattn_qk_norm_rope) or at
+                            cache_len[b] + n (flexattn_cache_append)                      */
+  int32_t rot_dim;       /* even, 2..D                                                    */
+  int32_t interleaved;   /* 0: the pair is (i, i + rot_dim / 2); 1: it is (2 i, 2 i + 1)  */
+  int32_t pos_batch;     /* with pos: 1 (broadcast) or B                                  */
+  int32_t reserved;      /* must be 0                                                     */
+} fa_rope;
+
+/* Norm (optional) and rotation (optional) of queries and keys in one pass:
+ * every row of q and k is read once and written once.
+ *   q (B, Hq, N, D) and q_out of the same shape, k (B, Hkv, N, D) and k_out:
+ *       bf16 or fp32 each, 1 <= D <= 128; the pair q, q_out or the pair
+ *       k, k_out may be NULL.  Any strides with a contiguous last dimension:
+ *       slices of a fused projection are read in place (rows of a multiple of
+ *       8 elements on 16-byte boundaries take 16-byte accesses).
+ *   q_norm, k_norm: NULL for no norm.  rope: NULL for no rotation.  At least
+ *       one of the three is given.
+ * An output may be its own input (same base, strides and type); other overlaps
+ * are not supported.  The arithmetic is fp32; the result is rounded once, to
+ * the output's type.
+ * Errors: FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_BATCH, FA_ERR_DTYPE,
+ * FA_ERR_HEADDIM, FA_ERR_ALIGN, FA_ERR_PARAM, FA_ERR_CUDA. */
+int flexattn_qk_norm_rope(const fa_tensor* q, const fa_tensor* k, const fa_tensor* q_out, const fa_tensor* k_out,
+                          const fa_head_norm* q_norm, const fa_head_norm* k_norm, const fa_rope* rope, void* stream);
+
+/* Bytes of device workspace flexattn_qk_norm_rope_backward needs (partial sums
+ * of the weight gradients; 0 when neither is asked for). */
+int flexattn_qk_norm_rope_backward_workspace_size(int32_t D, int32_t weight_grads, size_t* bytes);
+
+/* Gradients of sum(q_out * dq_out) + sum(k_out * dk_out) for
+ * flexattn_qk_norm_rope with the same arguments.  With g = R(-t) dy, the
+ * output gradient turned back,
+ *   dw = sum over batch, heads and tokens of g x r,
+ *   dx = r (g w - x r^2 mean(g w x))          (dx = g without a norm).
+ *   q, k: the forward's inputs (read again; r is recomputed).  They may be
+ *       NULL where the side has no norm.  dq_out, dk_out, dq, dk: bf16 or fp32
+ *       each; dq may be dq_out or q itself (same base, strides and type), and
+ *       likewise for k.
+ *   dq_weight, dk_weight: optional device fp32 [D] (NULL: not computed),
+ *       written in full; given only where the side has a norm (with a NULL
+ *       weight: the gradient at w = 1).
+ *   workspace: flexattn_qk_norm_rope_backward_workspace_size() bytes, 16-byte
+ *       aligned; not used by other work in flight during the call.
+ * The sums run in a fixed order: equal calls give equal bits.
+ * Errors: those of flexattn_qk_norm_rope, and FA_ERR_WORKSPACE. */
+int flexattn_qk_norm_rope_backward(const fa_tensor* q, const fa_tensor* k, const fa_tensor* dq_out,
+                                   const fa_tensor* dk_out, const fa_tensor* dq, const fa_tensor* dk,
+                                   float* dq_weight, float* dk_weight, const fa_head_norm* q_norm,
+                                   const fa_head_norm* k_norm, const fa_rope* rope, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* ----------------------------------------------------------------------- */
+/* Writing a KV cache                                                       */
+/* ----------------------------------------------------------------------- */
+
+/* A cache that flexattn_cache_append writes.  Logical token j of sequence b is
+ * slot j of row b of a dense cache, or slot j % page_size of page
+ * page_table[b * pages_per_seq + j / page_size] of a paged pool (as in
+ * fa_forward_options).
+ *
+ * An e4m3 cache holds codes c with value c * scale, one fp32 scale for every
+ * scale_block consecutive slots of a page (or of a dense row) and head.
+ * Appending writes scale = 2^ceil(log2(amax / 448)), amax the largest finite
+ * magnitude among the block's values (0 for a block of zeros, 2^-126 at
+ * least), and codes rounded to nearest even.  A power of two costs e4m3
+ * nothing in relative precision and makes every value exact in bf16.  Where a
+ * block already holds older tokens its scale only grows: the codes are then
+ * rounded again, as old code * (old scale / new scale).  Infinities become
+ * +-448 * scale and NaN stays NaN. */
+typedef struct fa_kv_cache {
+  fa_tensor k, v;            /* paged: (num_pages, Hkv, page_size, E / Ev); dense: (B, Hkv, S, E / Ev).
+                                One dtype for both: bf16, fp32 or e4m3                     */
+  const int32_t* page_table; /* device int32 [B, pages_per_seq], row-major; NULL: dense      */
+  const int32_t* cache_len;  /* device int32 [B]: tokens that sequence b holds before the call */
+  const int32_t* new_len;    /* device int32 [B] in 0..N: tokens of the call that belong to
+                                sequence b (the others are padding); NULL: all N           */
+  float* k_scale;            /* e4m3: device fp32 [num_pages or B, Hkv, ceil(size / scale_block)],
+                                contiguous, size = page_size or S; NULL otherwise           */
+  float* v_scale;            /* likewise                                                     */
+  int32_t pages_per_seq;     /* paged: columns of page_table                                 */
+  int32_t scale_block;       /* e4m3: tokens per scale, a power of two in 1..128 that divides
+                                page_size (any such power for a dense cache)                */
+} fa_kv_cache;
+
+/* Append N tokens a sequence to a cache, in one launch: k normed and rotated on
+ * the way (k_norm, rope: NULL leaves it out), v as it is.  With q, the queries
+ * of the same tokens are normed and rotated into q_out in the same launch (all
+ * N rows of every sequence).
+ *   k (B, Hkv, N, E), v (B, Hkv, N, Ev), q and q_out (B, Hq, N, E): bf16 or
+ *       fp32 each, any strides with a contiguous last dimension, E, Ev <= 128.
+ * Token n of sequence b goes to logical slot cache_len[b] + n.  Slots that the
+ * call does not name keep their bits, but for older tokens of a block whose
+ * scale grows (above).  cache_len and new_len are read, not changed.
+ * Nothing outside the cache is written: a token past the cache's end, a page id
+ * outside the pool, a negative cache_len or a new_len outside 0..N records
+ * FA_ERR_PARAM in the device status word, and the tokens concerned are left
+ * out (new_len is clamped).  Two sequences of one call must not share the
+ * pages they write to.
+ * Errors: FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_HEADS, FA_ERR_BATCH, FA_ERR_DTYPE,
+ * FA_ERR_HEADDIM, FA_ERR_ALIGN, FA_ERR_PARAM, FA_ERR_CUDA. */
+int flexattn_cache_append(const fa_tensor* k, const fa_tensor* v, const fa_kv_cache* cache,
+                          const fa_head_norm* k_norm, const fa_rope* rope, const fa_tensor* q,
+                          const fa_tensor* q_out, const fa_head_norm* q_norm, void* stream);
+
+/* ----------------------------------------------------------------------- */
+/* Attention over an e4m3 cache                                             */
+/* ----------------------------------------------------------------------- */
+
+typedef struct fa_kv_quant {
+  const float* k_scale;  /* device fp32 [num_pages or B, Hkv, ceil(size / scale_block)], as in
+                            fa_kv_cache; any finite values >= 0 (not only powers of two)     */
+  const float* v_scale;
+  int32_t scale_block;   /* as in fa_kv_cache                                                */
+  int32_t reserved;      /* must be 0                                                        */
+} fa_kv_quant;
+
+/* Bytes of device workspace flexattn_forward_fp8 needs for these arguments. */
+int flexattn_forward_fp8_workspace_size(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v,
+                                        const fa_kv_quant* quant, const fa_block_mask* block_mask, int32_t split_kv,
+                                        const fa_forward_options* options, size_t* bytes);
+
+/* flexattn_forward over an e4m3 cache: the same definition, block masks, rules,
+ * options and outputs, with k_j = code * scale and v_j = code * scale.
+ *   q: bf16 or fp32; k, v: e4m3, dense (B, Hkv, S, E / Ev) or page pools
+ *       (options->page_table).
+ *   Short queries (bf16 q, one query tile, 128-key tiles, E and Ev multiples of
+ *       16, 16-byte aligned codes and strides, pages of a multiple of 8 keys)
+ *       run on the 8-bit decode kernel, which reads every code once and keeps
+ *       q exactly (two e4m3 terms a value); the softmax weights are rounded to
+ *       two e4m3 terms, at most 2^-8 of each.  Other calls restore
+ *       the visible part of the cache to q's type in the workspace (exact in
+ *       bf16 for power-of-two scales, else rounded, 2^-8 of each value at
+ *       most) and run flexattn_forward on it.
+ *   Slots at or beyond kv_len[b] are not read as numbers (NaN there is
+ *       harmless), nor are page ids past the last page in use.
+ *   split_kv: as in flexattn_forward, for the decode kernel.
+ * Errors: those of flexattn_forward. */
+int flexattn_forward_fp8(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const fa_kv_quant* quant,
+                         const fa_tensor* out, float* lse, float scale, int32_t enable_gqa,
+                         const fa_score_mod* score_mod, const fa_mask_mod* mask_mod, const fa_block_mask* block_mask,
+                         int32_t split_kv, const fa_forward_options* options, void* workspace,
+                         size_t workspace_bytes, void* stream);
 
 /* Wait for `stream`, then read and clear the device status word that the
  * kernels set when a bounded wait runs out (FA_ERR_TIMEOUT) or an index check

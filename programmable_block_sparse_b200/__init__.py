@@ -19,6 +19,15 @@ Specification dicts (the menu of include/flexattn.h):
   goes on the outermost rule.
 * score_mod: ``{"kind": "none" | "softcap" | "alibi" | "cap_then_bias",
   "cap": c, "slope_heads": H, "pos": int32 tensor (B or 1, S) or None}``
+
+and, for the calls that prepare queries and keys and write caches:
+
+* norm: ``{"weight": bf16 or fp32 tensor (D,) or None, "eps": e}`` (1e-6 when absent)
+* rope: ``{"inv_freq": fp32 tensor (rot_dim / 2,), "interleaved": bool,
+  "pos": int32 tensor (B or 1, N) or None}``
+* cache: ``{"k": pool, "v": pool, "cache_len": int32 (B,), "new_len": int32 (B,) or None,
+  "page_table": int32 (B, pages_per_seq) or None}``, and for an e4m3 cache
+  ``"k_scale", "v_scale": fp32 (pages or B, Hkv, ceil(slots / scale_block)), "scale_block": n``
 """
 
 from __future__ import annotations
@@ -35,6 +44,8 @@ __all__ = [
     "flexattn_version", "flexattn_last_error", "flexattn_block_mask_dims", "flexattn_build_block_mask",
     "flexattn_forward_workspace_size", "flexattn_forward", "flexattn_forward_decode_noalloc",
     "flexattn_poll_device_status", "BlockMaskQ", "flexattn_transpose_block_mask", "flexattn_backward",
+    "flexattn_qk_norm_rope", "flexattn_qk_norm_rope_backward", "flexattn_cache_append",
+    "flexattn_forward_fp8_workspace_size", "flexattn_forward_fp8",
 ]
 
 _LIB = None
@@ -440,3 +451,273 @@ def flexattn_backward(q, k, v, out, dout, lse, block_mask, q_side=None, score_mo
         C.byref(gv), C.c_float(sc), int(bool(enable_gqa)), C.byref(sm), C.byref(mm), C.byref(bm), C.byref(qsd),
         _ptr(workspace), C.c_size_t(workspace.numel()), _stream_handle(stream)))
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------
+# Query / key preparation, cache writes and attention over an e4m3 cache
+# ---------------------------------------------------------------------------
+_DTYPES = {}
+
+
+def _dtype_codes():
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: _abi.FA_DTYPE_BF16, torch.float32: _abi.FA_DTYPE_F32,
+                        torch.float8_e4m3fn: _abi.FA_DTYPE_E4M3})
+    return _DTYPES
+
+
+def _device_tensor(t, name, device=None):
+    """``t`` as an fa_tensor, on ``device`` when given."""
+    code = _dtype_codes().get(t.dtype)
+    if code is None:
+        raise FlexAttnError(6, f"{name}: unsupported dtype {t.dtype}")
+    if t.dim() != 4:
+        raise FlexAttnError(2, f"{name}: expected a 4-D tensor, got shape {tuple(t.shape)}")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise FlexAttnError(9, f"{name} is on {t.device}, expected {device or 'a CUDA device'}")
+    return _abi.fa_tensor(t.data_ptr(), code, 0, tuple(t.shape), t.stride())
+
+
+def _device_array(t, name, dtype, shape, device):
+    """Address of a contiguous ``dtype`` tensor of the given shape on ``device``
+    (the library reads it without knowing its extent)."""
+    if t.dtype != dtype:
+        raise FlexAttnError(6, f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise FlexAttnError(2, f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise FlexAttnError(9, f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise FlexAttnError(8, f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _norm_struct(spec, name, D, device):
+    if spec is None:
+        return None
+    n = _abi.fa_head_norm(None, _abi.FA_DTYPE_F32, float(spec.get("eps", 1e-6)))
+    w = spec.get("weight")
+    if w is not None:
+        code = _dtype_codes().get(w.dtype, -1)
+        n.weight = _device_array(w, f"{name} weight", w.dtype, (D,), device)
+        n.weight_dtype = code
+    return n
+
+
+def _rope_struct(spec, B, N, device):
+    import torch
+    if spec is None:
+        return None
+    f = spec["inv_freq"]
+    r = _abi.fa_rope(_device_array(f, "inv_freq", torch.float32, (f.numel(),), device), None, 2 * f.numel(),
+                     1 if spec.get("interleaved") else 0, 0, 0)
+    pos = spec.get("pos")
+    if pos is not None:
+        rows = pos.shape[0] if pos.dim() == 2 else 1
+        if rows not in (1, B):
+            raise FlexAttnError(4, f"rope pos: {rows} rows, expected 1 or {B}")
+        r.pos = _device_array(pos, "rope pos", torch.int32, (rows, N) if pos.dim() == 2 else (N,), device)
+        r.pos_batch = rows
+    return r
+
+
+def _ref(s):
+    return None if s is None else C.byref(s)
+
+
+def _call(device, stream, fn, *args):
+    """``fn(*args, stream)`` with ``device`` current; ``stream`` None is that device's current stream."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        handle = _stream_handle(stream)
+        _check(fn(*args, handle))
+        return
+    with torch.cuda.device(device):
+        handle = _stream_handle(stream)
+        _check(fn(*args, handle))
+
+
+def flexattn_qk_norm_rope(q, k, q_norm=None, k_norm=None, rope=None, q_out=None, k_out=None, stream=None):
+    """Norm (per head) and rotation of queries (B, Hq, N, D) and keys
+    (B, Hkv, N, D) in one pass; returns ``(q_out, k_out)``.  Either of q, k
+    may be None; the outputs may be preallocated, or the inputs themselves."""
+    import torch
+    x = q if q is not None else k
+    if x is None:
+        raise FlexAttnError(1, "q and k are both None")
+    dev = x.device
+    qs = ks = qo = ko = None
+    if q is not None:
+        qs = _device_tensor(q, "q", dev)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        qo = _device_tensor(q_out, "q_out", dev)
+    if k is not None:
+        ks = _device_tensor(k, "k", dev)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        ko = _device_tensor(k_out, "k_out", dev)
+    B, _, N, D = x.shape
+    qn, kn = _norm_struct(q_norm, "q_norm", D, dev), _norm_struct(k_norm, "k_norm", D, dev)
+    rp = _rope_struct(rope, B, N, dev)
+    _call(dev, stream, load_library().flexattn_qk_norm_rope, _ref(qs), _ref(ks), _ref(qo), _ref(ko), _ref(qn),
+          _ref(kn), _ref(rp))
+    return q_out, k_out
+
+
+def flexattn_qk_norm_rope_backward(q, k, dq_out, dk_out, q_norm=None, k_norm=None, rope=None, dq=None, dk=None,
+                                   grad_dtype=None, weight_grads=True, workspace=None, stream=None):
+    """Gradients ``(dq, dk, dq_weight, dk_weight)`` of
+    :func:`flexattn_qk_norm_rope` with the same arguments; q and k are its
+    inputs (needed where that side has a norm).  The weight gradients are fp32
+    (D,) tensors, None without a norm or with ``weight_grads=False``; dq and dk
+    are allocated in ``grad_dtype`` (default: the output gradient's type)."""
+    import torch
+    g = dq_out if dq_out is not None else dk_out
+    if g is None:
+        raise FlexAttnError(1, "dq_out and dk_out are both None")
+    dev = g.device
+    B, _, N, D = g.shape
+
+    def side(x, dy, dx, norm, name):
+        xs = None if x is None or norm is None else _device_tensor(x, name, dev)
+        if dy is None:
+            return xs, None, None, None, None
+        if dx is None:
+            dx = torch.empty(dy.shape, dtype=grad_dtype or dy.dtype, device=dev)
+        dw = torch.empty(D, dtype=torch.float32, device=dev) if norm is not None and weight_grads else None
+        return xs, _device_tensor(dy, f"d{name}_out", dev), _device_tensor(dx, f"d{name}", dev), dx, dw
+
+    qs, gq, oq, dq, dqw = side(q, dq_out, dq, q_norm, "q")
+    ks, gk, ok, dk, dkw = side(k, dk_out, dk, k_norm, "k")
+    qn, kn = _norm_struct(q_norm, "q_norm", D, dev), _norm_struct(k_norm, "k_norm", D, dev)
+    rp = _rope_struct(rope, B, N, dev)
+    lib = load_library()
+    if workspace is None and (dqw is not None or dkw is not None):
+        n = C.c_size_t()
+        _check(lib.flexattn_qk_norm_rope_backward_workspace_size(D, 1, C.byref(n)))
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+    _call(dev, stream, lib.flexattn_qk_norm_rope_backward, _ref(qs), _ref(ks), _ref(gq), _ref(gk), _ref(oq), _ref(ok),
+          _ptr(dqw), _ptr(dkw), _ref(qn), _ref(kn), _ref(rp), _ptr(workspace),
+          C.c_size_t(workspace.numel() * workspace.element_size() if workspace is not None else 0))
+    return dq, dk, dqw, dkw
+
+
+def _scale_shape(pool, scale_block):
+    return (pool.shape[0], pool.shape[1], -(-pool.shape[2] // max(1, scale_block)))
+
+
+def flexattn_cache_append(k, v, cache, k_norm=None, rope=None, q=None, q_norm=None, q_out=None, stream=None):
+    """Append the tokens of k (B, Hkv, N, E) and v (B, Hkv, N, Ev) to ``cache``
+    (updated in place), keys normed and rotated on the way; with ``q``, the
+    queries of the same tokens go the same way into ``q_out``, which is
+    returned (None without q)."""
+    import torch
+    dev = k.device
+    ks, vs = _device_tensor(k, "k", dev), _device_tensor(v, "v", dev)
+    B, _, N, E = k.shape
+    kp, vp = cache["k"], cache["v"]
+    c = _abi.fa_kv_cache()
+    c.k, c.v = _device_tensor(kp, "cache k", dev), _device_tensor(vp, "cache v", dev)
+    c.cache_len = _device_array(cache["cache_len"], "cache_len", torch.int32, (B,), dev)
+    if cache.get("new_len") is not None:
+        c.new_len = _device_array(cache["new_len"], "new_len", torch.int32, (B,), dev)
+    table = cache.get("page_table")
+    if table is not None:
+        c.page_table = _device_array(table, "page_table", torch.int32, (B, table.shape[-1]), dev)
+        c.pages_per_seq = table.shape[-1]
+    if cache.get("k_scale") is not None or cache.get("v_scale") is not None:
+        n = int(cache.get("scale_block", 0))
+        c.scale_block = n
+        for name, pool in (("k_scale", kp), ("v_scale", vp)):
+            if cache.get(name) is not None:
+                setattr(c, name, _device_array(cache[name], name, torch.float32, _scale_shape(pool, n), dev))
+    qs = qo = None
+    if q is not None:
+        qs = _device_tensor(q, "q", dev)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        qo = _device_tensor(q_out, "q_out", dev)
+    kn = _norm_struct(k_norm, "k_norm", E, dev)
+    qn = _norm_struct(q_norm, "q_norm", E, dev)
+    rp = _rope_struct(rope, B, N, dev)
+    _call(dev, stream, load_library().flexattn_cache_append, C.byref(ks), C.byref(vs), C.byref(c), _ref(kn), _ref(rp),
+          _ref(qs), _ref(qo), _ref(qn))
+    return q_out
+
+
+def _quant_struct(quant, k, v, device):
+    import torch
+    n = int(quant["scale_block"])
+    return _abi.fa_kv_quant(
+        _device_array(quant["k_scale"], "k_scale", torch.float32, _scale_shape(k, n), device),
+        _device_array(quant["v_scale"], "v_scale", torch.float32, _scale_shape(v, n), device), n, 0)
+
+
+def _paged_checked(paged, B, device):
+    import torch
+    if paged is not None:
+        t = paged["page_table"]
+        _device_array(t, "page_table", torch.int32, (B, t.shape[-1]), device)
+    return paged
+
+
+def flexattn_forward_fp8_workspace_size(q, k, v, block_mask, quant, split_kv=0, paged=None):
+    """Workspace bytes of :func:`flexattn_forward_fp8` for these arguments."""
+    dev = q.device
+    qs, ks, vs = _device_tensor(q, "q", dev), _device_tensor(k, "k", dev), _device_tensor(v, "v", dev)
+    qt, bm = _quant_struct(quant, k, v, dev), block_mask.as_struct()
+    opts = _options_struct(None, False, 0, _paged_checked(paged, q.shape[0], dev))
+    n = C.c_size_t()
+    _check(load_library().flexattn_forward_fp8_workspace_size(C.byref(qs), C.byref(ks), C.byref(vs), C.byref(qt),
+                                                              C.byref(bm), int(split_kv), _ref(opts), C.byref(n)))
+    return n.value
+
+
+def flexattn_forward_fp8(q, k, v, block_mask, quant, score_mod=None, mask_mod=None, scale=None, enable_gqa=False,
+                         out=None, lse=True, split_kv=0, workspace=None, stream=None, out_dtype=None,
+                         max_scores=None, rows_guaranteed_safe=False, wait_cycles=0, paged=None):
+    """:func:`flexattn_forward` over an e4m3 cache: k and v are
+    ``torch.float8_e4m3fn`` codes, dense (B, Hkv, S, D) or page pools, and
+    ``quant`` is ``{"k_scale", "v_scale": fp32 (pages or B, Hkv,
+    ceil(slots / scale_block)), "scale_block": n}``.  Returns ``(out, lse)``,
+    or ``(out, lse, max_scores)`` when those are requested."""
+    import torch
+    dev = q.device
+    qs, ks, vs = _device_tensor(q, "q", dev), _device_tensor(k, "k", dev), _device_tensor(v, "v", dev)
+    B, Hq, L, _ = q.shape
+    if out is None:
+        out = torch.empty((B, Hq, L, v.shape[3]), dtype=out_dtype or q.dtype, device=dev)
+    os_ = _device_tensor(out, "out", dev)
+    if lse is True:
+        lse = torch.empty((B, Hq, L), dtype=torch.float32, device=dev)
+    elif lse is False or lse is None:
+        lse = None
+    else:
+        _device_array(lse, "lse", torch.float32, (B, Hq, L), dev)
+    want_max = max_scores is not None and max_scores is not False
+    if max_scores is True:
+        max_scores = torch.empty((B, Hq, L), dtype=torch.float32, device=dev)
+    elif not want_max:
+        max_scores = None
+    else:
+        _device_array(max_scores, "max_scores", torch.float32, (B, Hq, L), dev)
+    qt, bm = _quant_struct(quant, k, v, dev), block_mask.as_struct()
+    opts = _options_struct(max_scores, rows_guaranteed_safe, wait_cycles, _paged_checked(paged, B, dev))
+    sm, mm = _score_struct(score_mod), _mask_struct(mask_mod)
+    sc = 0.0 if scale is None or math.isnan(float(scale)) else float(scale)
+    lib = load_library()
+    if workspace is None:
+        n = C.c_size_t()
+        _check(lib.flexattn_forward_fp8_workspace_size(C.byref(qs), C.byref(ks), C.byref(vs), C.byref(qt), C.byref(bm),
+                                                       int(split_kv), _ref(opts), C.byref(n)))
+        if n.value > 0:
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+    _call(dev, stream, lib.flexattn_forward_fp8, C.byref(qs), C.byref(ks), C.byref(vs), C.byref(qt), C.byref(os_),
+          _ptr(lse), C.c_float(sc), int(bool(enable_gqa)), C.byref(sm), C.byref(mm), C.byref(bm), int(split_kv),
+          _ref(opts), _ptr(workspace),
+          C.c_size_t(workspace.numel() * workspace.element_size() if workspace is not None else 0))
+    if want_max:
+        return out, lse, max_scores
+    return out, lse

@@ -14,6 +14,7 @@ FA_ERR_TIMEOUT = 13
 
 FA_DTYPE_BF16 = 0
 FA_DTYPE_F32 = 1
+FA_DTYPE_E4M3 = 2
 
 FA_FLAG_ROWS_GUARANTEED_SAFE = 1
 
@@ -78,6 +79,29 @@ class fa_block_mask_q(C.Structure):
     ]
 
 
+class fa_head_norm(C.Structure):
+    _fields_ = [("weight", C.c_void_p), ("weight_dtype", C.c_int32), ("eps", C.c_float)]
+
+
+class fa_rope(C.Structure):
+    _fields_ = [
+        ("inv_freq", C.c_void_p), ("pos", C.c_void_p), ("rot_dim", C.c_int32), ("interleaved", C.c_int32),
+        ("pos_batch", C.c_int32), ("reserved", C.c_int32),
+    ]
+
+
+class fa_kv_cache(C.Structure):
+    _fields_ = [
+        ("k", fa_tensor), ("v", fa_tensor), ("page_table", C.c_void_p), ("cache_len", C.c_void_p),
+        ("new_len", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p), ("pages_per_seq", C.c_int32),
+        ("scale_block", C.c_int32),
+    ]
+
+
+class fa_kv_quant(C.Structure):
+    _fields_ = [("k_scale", C.c_void_p), ("v_scale", C.c_void_p), ("scale_block", C.c_int32), ("reserved", C.c_int32)]
+
+
 # (name, restype, argtypes) for every exported entry point.
 PROTOTYPES = [
     ("flexattn_version", C.c_int, []),
@@ -103,6 +127,24 @@ PROTOTYPES = [
       C.c_void_p, C.POINTER(fa_tensor), C.POINTER(fa_tensor), C.POINTER(fa_tensor), C.c_float, C.c_int32,
       C.POINTER(fa_score_mod), C.POINTER(fa_mask_mod), C.POINTER(fa_block_mask), C.POINTER(fa_block_mask_q),
       C.c_void_p, C.c_size_t, C.c_void_p]),
+    ("flexattn_qk_norm_rope", C.c_int,
+     [C.POINTER(fa_tensor), C.POINTER(fa_tensor), C.POINTER(fa_tensor), C.POINTER(fa_tensor), C.POINTER(fa_head_norm),
+      C.POINTER(fa_head_norm), C.POINTER(fa_rope), C.c_void_p]),
+    ("flexattn_qk_norm_rope_backward_workspace_size", C.c_int, [C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
+    ("flexattn_qk_norm_rope_backward", C.c_int,
+     [C.POINTER(fa_tensor), C.POINTER(fa_tensor), C.POINTER(fa_tensor), C.POINTER(fa_tensor), C.POINTER(fa_tensor),
+      C.POINTER(fa_tensor), C.c_void_p, C.c_void_p, C.POINTER(fa_head_norm), C.POINTER(fa_head_norm),
+      C.POINTER(fa_rope), C.c_void_p, C.c_size_t, C.c_void_p]),
+    ("flexattn_cache_append", C.c_int,
+     [C.POINTER(fa_tensor), C.POINTER(fa_tensor), C.POINTER(fa_kv_cache), C.POINTER(fa_head_norm), C.POINTER(fa_rope),
+      C.POINTER(fa_tensor), C.POINTER(fa_tensor), C.POINTER(fa_head_norm), C.c_void_p]),
+    ("flexattn_forward_fp8_workspace_size", C.c_int,
+     [C.POINTER(fa_tensor), C.POINTER(fa_tensor), C.POINTER(fa_tensor), C.POINTER(fa_kv_quant),
+      C.POINTER(fa_block_mask), C.c_int32, C.POINTER(fa_forward_options), C.POINTER(C.c_size_t)]),
+    ("flexattn_forward_fp8", C.c_int,
+     [C.POINTER(fa_tensor), C.POINTER(fa_tensor), C.POINTER(fa_tensor), C.POINTER(fa_kv_quant), C.POINTER(fa_tensor),
+      C.c_void_p, C.c_float, C.c_int32, C.POINTER(fa_score_mod), C.POINTER(fa_mask_mod), C.POINTER(fa_block_mask),
+      C.c_int32, C.POINTER(fa_forward_options), C.c_void_p, C.c_size_t, C.c_void_p]),
     ("flexattn_poll_device_status", C.c_int, [C.c_void_p, C.POINTER(C.c_int32)]),
 ]
 

@@ -530,6 +530,208 @@ int prepare(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const fa
   return FA_OK;
 }
 
+// ----------------------------------------------------------------------------
+// Query / key preparation and cache writes
+// ----------------------------------------------------------------------------
+constexpr int64_t kMaxTokens = 1 << 30;  // tokens of one call, slots of one sequence
+
+// A tensor that a call writes: no two elements in one place.
+int check_written(const fa_tensor* t, const char* name) {
+  for (int i = 0; i < 3; ++i)
+    if (t->size[i] > 1 && t->stride[i] == 0)
+      return fail(FA_ERR_ALIGN, "%s: written, so dimension %d must not be broadcast (stride 0)", name, i);
+  return FA_OK;
+}
+
+// Rows that take 16-byte accesses of 8 bf16 or 4 fp32 elements.
+bool vector_rows(const fa_tensor* t) { return t->size[3] % 8 == 0 && aligned16(t); }
+
+RowsIn rows_in(const fa_tensor* t) {
+  RowsIn r{};
+  if (t) r = RowsIn{t->data, t->dtype == FA_DTYPE_F32, (int)t->size[1], {t->stride[0], t->stride[1], t->stride[2]}};
+  return r;
+}
+RowsOut rows_out(const fa_tensor* t) {
+  RowsOut r{};
+  if (t) r = RowsOut{t->data, t->dtype == FA_DTYPE_F32, {t->stride[0], t->stride[1], t->stride[2]}};
+  return r;
+}
+
+int norm_to_device(const fa_head_norm* n, const char* name, NormArgs* out) {
+  *out = NormArgs{};
+  if (n == nullptr) return FA_OK;
+  if (!(n->eps >= 0.0f) || isinf(n->eps)) return fail(FA_ERR_PARAM, "%s: eps must be finite and >= 0 (got %g)", name, n->eps);
+  if (n->weight && n->weight_dtype != FA_DTYPE_BF16 && n->weight_dtype != FA_DTYPE_F32)
+    return fail(FA_ERR_DTYPE, "%s: weights are bf16 or fp32 (got dtype %d)", name, n->weight_dtype);
+  if (n->weight && reinterpret_cast<uintptr_t>(n->weight) % (n->weight_dtype == FA_DTYPE_F32 ? 4 : 2))
+    return fail(FA_ERR_ALIGN, "%s: weight is not aligned to its type", name);
+  *out = NormArgs{1, n->weight, n->weight_dtype == FA_DTYPE_F32, n->eps};
+  return FA_OK;
+}
+
+int rope_to_device(const fa_rope* r, int64_t D, int64_t B, RopeArgs* out) {
+  *out = RopeArgs{};
+  if (r == nullptr) return FA_OK;
+  if (r->inv_freq == nullptr) return fail(FA_ERR_NULL, "rope: inv_freq is NULL");
+  if (r->reserved != 0) return fail(FA_ERR_PARAM, "rope: reserved field must be 0");
+  if (r->rot_dim < 2 || r->rot_dim % 2 || r->rot_dim > D)
+    return fail(FA_ERR_PARAM, "rope: rot_dim must be even and in 2..%lld (got %d)", (long long)D, r->rot_dim);
+  if (r->interleaved != 0 && r->interleaved != 1) return fail(FA_ERR_PARAM, "rope: interleaved is 0 or 1");
+  if (r->pos && r->pos_batch != 1 && r->pos_batch != B)
+    return fail(FA_ERR_BATCH, "rope: pos_batch must be 1 or %lld (got %d)", (long long)B, r->pos_batch);
+  if (reinterpret_cast<uintptr_t>(r->inv_freq) % 4 || reinterpret_cast<uintptr_t>(r->pos) % 4)
+    return fail(FA_ERR_ALIGN, "rope: inv_freq and pos are 4-byte aligned");
+  *out = RopeArgs{r->rot_dim, r->interleaved, r->inv_freq, r->pos, r->pos_batch};
+  return FA_OK;
+}
+
+// One side (q or k) of a preparation call: an input and an output of one
+// shape, agreeing with the other side's batch, tokens and head dimension.
+int check_side(const fa_tensor* x, const fa_tensor* y, const char* xn, const char* yn, const fa_tensor** first) {
+  if ((x == nullptr) != (y == nullptr)) return fail(FA_ERR_NULL, "%s and %s go together", xn, yn);
+  if (x == nullptr) return FA_OK;
+  int rc;
+  if ((rc = check_tensor(x, xn)) || (rc = check_tensor(y, yn)) || (rc = check_written(y, yn))) return rc;
+  for (int i = 0; i < 4; ++i)
+    if (x->size[i] != y->size[i]) return fail(FA_ERR_SHAPE, "%s must have the shape of %s", yn, xn);
+  if (x->size[3] > 128) return fail(FA_ERR_HEADDIM, "head dims above 128 are not supported (got %lld)", (long long)x->size[3]);
+  if (x->size[0] > 65535 || x->size[1] > 32767 || x->size[2] > kMaxTokens)
+    return fail(FA_ERR_SHAPE, "%s: at most 65535 sequences, 32767 heads and 2^30 tokens", xn);
+  if (*first == nullptr) {
+    *first = x;
+  } else {
+    const fa_tensor* f = *first;
+    if (f->size[0] != x->size[0]) return fail(FA_ERR_BATCH, "q and k must have the same batch size");
+    if (f->size[2] != x->size[2] || f->size[3] != x->size[3])
+      return fail(FA_ERR_SHAPE, "q and k must have the same tokens and head dimension");
+  }
+  return FA_OK;
+}
+
+int check_quant_block(int32_t scale_block, bool paged, int64_t page_size) {
+  if (scale_block < 1 || scale_block > 128 || (scale_block & (scale_block - 1)))
+    return fail(FA_ERR_PARAM, "scale_block must be a power of two in 1..128 (got %d)", scale_block);
+  if (paged && page_size % scale_block)
+    return fail(FA_ERR_PARAM, "scale_block (%d) must divide the page size (%lld)", scale_block, (long long)page_size);
+  return FA_OK;
+}
+
+// Codes of an e4m3 cache: check_tensor for the 8-bit type.
+int check_codes(const fa_tensor* t, const char* name) {
+  if (t == nullptr) return fail(FA_ERR_NULL, "%s is NULL", name);
+  if (t->dtype != FA_DTYPE_E4M3) return fail(FA_ERR_DTYPE, "%s must be e4m3 (got dtype %d)", name, t->dtype);
+  fa_tensor as = *t;
+  as.dtype = FA_DTYPE_BF16;  // the remaining checks do not depend on the element type
+  return check_tensor(&as, name);
+}
+
+// (outer, H, N, D) codes -> 4-D byte map with a 128 x box_rows box, 128 B swizzle.
+int encode_byte_map(CUtensorMap* map, const fa_tensor* t, int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return fail(FA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(t->size[3]), static_cast<cuuint64_t>(t->size[2]),
+                        static_cast<cuuint64_t>(t->size[1]), static_cast<cuuint64_t>(t->size[0])};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(t->stride[2]), static_cast<cuuint64_t>(t->stride[1]),
+                           static_cast<cuuint64_t>(t->stride[0])};
+  cuuint32_t box[4] = {128, static_cast<cuuint32_t>(box_rows), 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, t->data, dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(FA_ERR_ALIGN, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return FA_OK;
+}
+
+bool codes_aligned16(const fa_tensor* t) {
+  return reinterpret_cast<uintptr_t>(t->data) % 16 == 0 && t->stride[0] % 16 == 0 && t->stride[1] % 16 == 0 &&
+         t->stride[2] % 16 == 0 && t->size[3] % 16 == 0;
+}
+
+// How a call of flexattn_forward_fp8 runs.
+struct Fp8Call {
+  FwdArgs a;
+  QuantArgs qa;
+  bool decode;        // the 8-bit decode kernel; else restore, then flexattn_forward
+  Fp8Plan plan;       // decode
+  int box;            // decode: slots per TMA box
+  fa_tensor kd, vd;   // restore: the dense tensors (data: workspace offsets)
+  size_t restored;    // restore: their bytes
+  size_t bytes;       // workspace
+};
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Up to this many 16-row chunks per KV head the decode kernel is taken: each
+// chunk reads the cache again (mostly from L2), where restoring reads it once,
+// writes it in q's type and reads that.
+constexpr int kFp8MaxRowChunks = 16;
+
+int prepare_fp8(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const fa_kv_quant* quant,
+                const fa_tensor* out, float scale, int32_t enable_gqa, const fa_score_mod* score,
+                const fa_mask_mod* mask, const fa_block_mask* bm, int32_t split_kv, const fa_forward_options* opt,
+                Fp8Call* c) {
+  int rc;
+  if ((rc = check_tensor(q, "q")) || (rc = check_codes(k, "k")) || (rc = check_codes(v, "v"))) return rc;
+  if (!quant || !quant->k_scale || !quant->v_scale) return fail(FA_ERR_NULL, "quant and its scales must not be NULL");
+  if (quant->reserved != 0) return fail(FA_ERR_PARAM, "quant: reserved field must be 0");
+  if (split_kv < 0) return fail(FA_ERR_PARAM, "split_kv must be >= 0");
+  const bool paged = opt != nullptr && opt->page_table != nullptr;
+  if ((rc = check_quant_block(quant->scale_block, paged, k->size[2]))) return rc;
+  if (reinterpret_cast<uintptr_t>(quant->k_scale) % 4 || reinterpret_cast<uintptr_t>(quant->v_scale) % 4)
+    return fail(FA_ERR_ALIGN, "scales are 4-byte aligned");
+  // the shape, head, mask and rule checks of flexattn_forward: k and v as
+  // tensors of q's type (split_kv 1: whichever kernel, none is run here)
+  fa_tensor kt = *k, vt = *v;
+  kt.dtype = vt.dtype = q->dtype;
+  Path path;
+  if ((rc = prepare(q, &kt, &vt, out, scale, enable_gqa, score, mask, bm, 1, opt, &c->a, &path))) return rc;
+  if (c->a.S > kMaxTokens) return fail(FA_ERR_SHAPE, "at most 2^30 keys");
+  const FwdArgs& a = c->a;
+  int block_log = 0;
+  while ((1 << block_log) < quant->scale_block) ++block_log;
+  const int64_t slots = k->size[2];
+  c->qa = QuantArgs{quant->k_scale, quant->v_scale, block_log,
+                    static_cast<int>((slots + quant->scale_block - 1) / quant->scale_block)};
+  c->box = 128;
+  if (paged)
+    while (opt->page_size % c->box) c->box /= 2;
+  plan_decode_fp8(a, split_kv, sm_count(), &c->plan);
+  c->decode = q->dtype == FA_DTYPE_BF16 && bm->Mb == 1 && bm->BN == 128 && c->box >= 8 && aligned16(q) &&
+              codes_aligned16(k) && codes_aligned16(v) && c->plan.row_chunks <= kFp8MaxRowChunks &&
+              static_cast<int64_t>(a.Hkv) * c->plan.row_chunks * a.B < (int64_t{1} << 30);
+  if (c->decode) {
+    c->bytes = c->plan.workspace_bytes;
+    return FA_OK;
+  }
+  if (2 * static_cast<int64_t>(a.Hkv) > 65535) return fail(FA_ERR_SHAPE, "at most 32767 KV heads");
+  // the dense tensors that the cache is restored to
+  const size_t es = q->dtype == FA_DTYPE_BF16 ? 2 : 4;
+  fa_tensor* dst[2] = {&c->kd, &c->vd};
+  const int dims[2] = {a.E, a.Ev};
+  size_t at = 0;
+  for (int i = 0; i < 2; ++i) {
+    fa_tensor& t = *dst[i];
+    t = fa_tensor{};
+    t.dtype = q->dtype;
+    const int64_t size[4] = {a.B, a.Hkv, a.S, dims[i]};
+    for (int d = 3; d >= 0; --d) {
+      t.size[d] = size[d];
+      t.stride[d] = d == 3 ? 1 : t.stride[d + 1] * size[d + 1];
+    }
+    t.data = reinterpret_cast<void*>(256 + at);  // an aligned stand-in until the workspace is known
+    at += round256(static_cast<size_t>(t.stride[0]) * size[0] * es);
+  }
+  c->restored = at;
+  size_t inner = 0;
+  fa_forward_options dense{};
+  if (opt) dense = *opt;
+  dense.page_table = nullptr;
+  dense.page_size = dense.pages_per_seq = 0;
+  if ((rc = flexattn_forward_workspace_size(q, &c->kd, &c->vd, bm, split_kv, &dense, &inner))) return rc;
+  c->bytes = at + inner;
+  return FA_OK;
+}
+
 }  // namespace
 }  // namespace fa
 
@@ -804,6 +1006,260 @@ int flexattn_backward(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v
   cudaError_t e = launch_bwd(a, maps, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "backward launch");
   return FA_OK;
+}
+
+int flexattn_qk_norm_rope(const fa_tensor* q, const fa_tensor* k, const fa_tensor* q_out, const fa_tensor* k_out,
+                          const fa_head_norm* q_norm, const fa_head_norm* k_norm, const fa_rope* rope, void* stream) {
+  if (!q && !k) return fail(FA_ERR_NULL, "q and k are both NULL");
+  if (!q_norm && !k_norm && !rope) return fail(FA_ERR_NULL, "q_norm, k_norm and rope are all NULL");
+  const fa_tensor* first = nullptr;
+  int rc;
+  if ((rc = check_side(q, q_out, "q", "q_out", &first)) || (rc = check_side(k, k_out, "k", "k_out", &first))) return rc;
+  PrepArgs a{};
+  if ((rc = norm_to_device(q_norm, "q_norm", &a.norm[0])) || (rc = norm_to_device(k_norm, "k_norm", &a.norm[1])) ||
+      (rc = rope_to_device(rope, first->size[3], first->size[0], &a.rope)))
+    return rc;
+  a.x[0] = rows_in(q);
+  a.x[1] = rows_in(k);
+  a.y[0] = rows_out(q_out);
+  a.y[1] = rows_out(k_out);
+  a.B = (int)first->size[0];
+  a.N = (int)first->size[2];
+  a.D = (int)first->size[3];
+  a.vec = 1;
+  for (const fa_tensor* t : {q, k, q_out, k_out})
+    if (t && !vector_rows(t)) a.vec = 0;
+  cudaError_t e = launch_prep(a, sm_count(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "query/key preparation launch");
+  return FA_OK;
+}
+
+int flexattn_qk_norm_rope_backward_workspace_size(int32_t D, int32_t weight_grads, size_t* bytes) {
+  if (!bytes) return fail(FA_ERR_NULL, "bytes must not be NULL");
+  if (D < 1) return fail(FA_ERR_SHAPE, "D must be >= 1");
+  if (D > 128) return fail(FA_ERR_HEADDIM, "head dims above 128 are not supported (got %d)", D);
+  *bytes = weight_grads ? static_cast<size_t>(kPrepBwdMaxCtas) * 2 * D * sizeof(float) : 0;
+  return FA_OK;
+}
+
+int flexattn_qk_norm_rope_backward(const fa_tensor* q, const fa_tensor* k, const fa_tensor* dq_out,
+                                   const fa_tensor* dk_out, const fa_tensor* dq, const fa_tensor* dk,
+                                   float* dq_weight, float* dk_weight, const fa_head_norm* q_norm,
+                                   const fa_head_norm* k_norm, const fa_rope* rope, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  if (!dq_out && !dk_out) return fail(FA_ERR_NULL, "dq_out and dk_out are both NULL");
+  if (!q_norm && !k_norm && !rope) return fail(FA_ERR_NULL, "q_norm, k_norm and rope are all NULL");
+  const fa_tensor* first = nullptr;
+  int rc;
+  if ((rc = check_side(dq_out, dq, "dq_out", "dq", &first)) || (rc = check_side(dk_out, dk, "dk_out", "dk", &first)))
+    return rc;
+  PrepBwdArgs a{};
+  if ((rc = norm_to_device(q_norm, "q_norm", &a.norm[0])) || (rc = norm_to_device(k_norm, "k_norm", &a.norm[1])) ||
+      (rc = rope_to_device(rope, first->size[3], first->size[0], &a.rope)))
+    return rc;
+  const fa_tensor* x[2] = {q, k};
+  const fa_tensor* dy[2] = {dq_out, dk_out};
+  const fa_tensor* dx[2] = {dq, dk};
+  float* dw[2] = {dq_weight, dk_weight};
+  const char* names[2] = {"q", "k"};
+  a.vec = 1;
+  for (int i = 0; i < 2; ++i) {
+    if (dw[i] && (!dy[i] || !a.norm[i].on))
+      return fail(FA_ERR_PARAM, "d%s_weight needs the gradient and the norm of %s", names[i], names[i]);
+    if (reinterpret_cast<uintptr_t>(dw[i]) % 4) return fail(FA_ERR_ALIGN, "d%s_weight is not 4-byte aligned", names[i]);
+    if (!dy[i]) continue;
+    if (a.norm[i].on) {
+      if ((rc = check_tensor(x[i], names[i]))) return rc;
+      for (int d = 0; d < 4; ++d)
+        if (x[i]->size[d] != dy[i]->size[d]) return fail(FA_ERR_SHAPE, "d%s_out must have the shape of %s", names[i], names[i]);
+      a.x[i] = rows_in(x[i]);
+      if (!vector_rows(x[i])) a.vec = 0;
+    }
+    a.dy[i] = rows_in(dy[i]);
+    a.dx[i] = rows_out(dx[i]);
+    a.dw[i] = dw[i];
+    if (!vector_rows(dy[i]) || !vector_rows(dx[i])) a.vec = 0;
+  }
+  a.B = (int)first->size[0];
+  a.N = (int)first->size[2];
+  a.D = (int)first->size[3];
+  size_t need = 0;
+  if ((rc = flexattn_qk_norm_rope_backward_workspace_size(a.D, dq_weight || dk_weight, &need))) return rc;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+    return fail(FA_ERR_WORKSPACE, "the weight gradients need %zu bytes of workspace (got %zu)", need,
+                workspace ? workspace_bytes : static_cast<size_t>(0));
+  if (need > 0 && reinterpret_cast<uintptr_t>(workspace) % 16) return fail(FA_ERR_ALIGN, "workspace must be 16-byte aligned");
+  a.partial = static_cast<float*>(workspace);
+  cudaError_t e = launch_prep_bwd(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "query/key preparation backward launch");
+  return FA_OK;
+}
+
+int flexattn_cache_append(const fa_tensor* k, const fa_tensor* v, const fa_kv_cache* cache,
+                          const fa_head_norm* k_norm, const fa_rope* rope, const fa_tensor* q,
+                          const fa_tensor* q_out, const fa_head_norm* q_norm, void* stream) {
+  if (!cache) return fail(FA_ERR_NULL, "cache is NULL");
+  int rc;
+  if ((rc = check_tensor(k, "k")) || (rc = check_tensor(v, "v"))) return rc;
+  const int64_t B = k->size[0], H = k->size[1], N = k->size[2], E = k->size[3], Ev = v->size[3];
+  if (v->size[0] != B) return fail(FA_ERR_BATCH, "k and v must have the same batch size");
+  if (v->size[1] != H || v->size[2] != N) return fail(FA_ERR_SHAPE, "v must be (B, Hkv, N, Ev) like k");
+  if (E > 128 || Ev > 128) return fail(FA_ERR_HEADDIM, "head dims above 128 are not supported (E=%lld, Ev=%lld)", (long long)E, (long long)Ev);
+  const fa_tensor* first = nullptr;
+  if ((rc = check_side(q, q_out, "q", "q_out", &first))) return rc;
+  if (q && q->size[0] != B) return fail(FA_ERR_BATCH, "q and k must have the same batch size");
+  if (q && (q->size[2] != N || q->size[3] != E)) return fail(FA_ERR_SHAPE, "q must have the tokens and head dimension of k");
+  const int64_t Hq = q ? q->size[1] : 0;
+  if (B > 65535 || N > kMaxTokens || 2 * H + Hq > 65535)
+    return fail(FA_ERR_SHAPE, "at most 65535 sequences, 2^30 tokens and 2 Hkv + Hq = 65535 heads");
+  const bool paged = cache->page_table != nullptr;
+  const fa_tensor* pools[2] = {&cache->k, &cache->v};
+  const char* names[2] = {"cache.k", "cache.v"};
+  const int64_t dims[2] = {E, Ev};
+  const int32_t dtype = cache->k.dtype;
+  if (cache->v.dtype != dtype) return fail(FA_ERR_DTYPE, "cache.k and cache.v must share one dtype");
+  for (int i = 0; i < 2; ++i) {
+    const fa_tensor* t = pools[i];
+    if ((rc = dtype == FA_DTYPE_E4M3 ? check_codes(t, names[i]) : check_tensor(t, names[i])) ||
+        (rc = check_written(t, names[i])))
+      return rc;
+    if (t->size[1] != H) return fail(FA_ERR_HEADS, "%s has %lld heads, k and v %lld", names[i], (long long)t->size[1], (long long)H);
+    if (t->size[3] != dims[i]) return fail(FA_ERR_SHAPE, "%s has head dim %lld, the new rows %lld", names[i], (long long)t->size[3], (long long)dims[i]);
+    if (t->size[0] != pools[0]->size[0] || t->size[2] != pools[0]->size[2])
+      return fail(FA_ERR_SHAPE, "cache.k and cache.v must have the same pages (or batch and slots)");
+  }
+  const int64_t slots = cache->k.size[2];
+  if (paged) {
+    if (cache->pages_per_seq < 1) return fail(FA_ERR_PARAM, "paged cache: pages_per_seq must be >= 1 (got %d)", cache->pages_per_seq);
+    if (slots * cache->pages_per_seq > kMaxTokens) return fail(FA_ERR_SHAPE, "at most 2^30 slots a sequence");
+  } else {
+    if (cache->k.size[0] != B) return fail(FA_ERR_BATCH, "a dense cache must have the batch size of k");
+    if (slots > kMaxTokens) return fail(FA_ERR_SHAPE, "at most 2^30 slots a sequence");
+  }
+  if (!cache->cache_len) return fail(FA_ERR_NULL, "cache_len is NULL");
+  if (dtype == FA_DTYPE_E4M3) {
+    if (!cache->k_scale || !cache->v_scale) return fail(FA_ERR_NULL, "an e4m3 cache needs k_scale and v_scale");
+    if ((rc = check_quant_block(cache->scale_block, paged, slots))) return rc;
+    if (reinterpret_cast<uintptr_t>(cache->k_scale) % 4 || reinterpret_cast<uintptr_t>(cache->v_scale) % 4)
+      return fail(FA_ERR_ALIGN, "scales are 4-byte aligned");
+  } else if (cache->k_scale || cache->v_scale) {
+    return fail(FA_ERR_PARAM, "scales belong to an e4m3 cache");
+  }
+  AppendArgs a{};
+  if ((rc = norm_to_device(k_norm, "k_norm", &a.k_norm)) || (rc = norm_to_device(q_norm, "q_norm", &a.q_norm)) ||
+      (rc = rope_to_device(rope, E, B, &a.rope)))
+    return rc;
+  int serr = 0;
+  a.status = status_word(&serr);
+  if (serr) return fail(FA_ERR_CUDA, "cannot locate the device status word");
+  a.k = rows_in(k);
+  a.v = rows_in(v);
+  a.q = rows_in(q);
+  a.q_out = rows_out(q_out);
+  a.B = (int)B;
+  a.N = (int)N;
+  a.E = (int)E;
+  a.Ev = (int)Ev;
+  a.k_vec = vector_rows(k);
+  a.v_vec = vector_rows(v);
+  a.q_vec = q && vector_rows(q) && vector_rows(q_out);
+  a.kc = cache->k.data;
+  a.vc = cache->v.data;
+  int vec[2];
+  for (int i = 0; i < 2; ++i) {
+    const fa_tensor* t = pools[i];
+    vec[i] = dtype != FA_DTYPE_E4M3 ? vector_rows(t)
+                                    : t->size[3] % 8 == 0 && reinterpret_cast<uintptr_t>(t->data) % 8 == 0 &&
+                                          t->stride[0] % 8 == 0 && t->stride[1] % 8 == 0 && t->stride[2] % 8 == 0;
+    for (int d = 0; d < 3; ++d) (i ? a.vc_stride : a.kc_stride)[d] = t->stride[d];
+  }
+  a.kc_vec = vec[0];
+  a.vc_vec = vec[1];
+  a.dtype = dtype;
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.scale_block = dtype == FA_DTYPE_E4M3 ? cache->scale_block : 1;
+  a.scales_per_outer = static_cast<int>((slots + a.scale_block - 1) / a.scale_block);
+  a.page_table = cache->page_table;
+  a.cache_len = cache->cache_len;
+  a.new_len = cache->new_len;
+  a.page_size = static_cast<int>(slots);
+  a.pages_per_seq = paged ? cache->pages_per_seq : 1;
+  a.num_outer = static_cast<int>(cache->k.size[0]);
+  cudaError_t e = launch_append(a, sm_count(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache append launch");
+  return FA_OK;
+}
+
+int flexattn_forward_fp8_workspace_size(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v,
+                                        const fa_kv_quant* quant, const fa_block_mask* block_mask, int32_t split_kv,
+                                        const fa_forward_options* options, size_t* bytes) {
+  if (!bytes) return fail(FA_ERR_NULL, "bytes must not be NULL");
+  fa_score_mod none_score{FA_SCORE_NONE, 0.0f, 0, 0, nullptr};
+  fa_mask_mod none_mask{};
+  none_mask.kind = FA_MASK_NONE;
+  Fp8Call c;
+  int rc = prepare_fp8(q, k, v, quant, nullptr, 0.0f, 1, &none_score, &none_mask, block_mask, split_kv, options, &c);
+  if (rc) return rc;
+  *bytes = c.bytes;
+  return FA_OK;
+}
+
+int flexattn_forward_fp8(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const fa_kv_quant* quant,
+                         const fa_tensor* out, float* lse, float scale, int32_t enable_gqa,
+                         const fa_score_mod* score_mod, const fa_mask_mod* mask_mod, const fa_block_mask* block_mask,
+                         int32_t split_kv, const fa_forward_options* options, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  if (!out) return fail(FA_ERR_NULL, "out is NULL");
+  Fp8Call c;
+  int rc = prepare_fp8(q, k, v, quant, out, scale, enable_gqa, score_mod, mask_mod, block_mask, split_kv, options, &c);
+  if (rc) return rc;
+  if ((rc = apply_options(options, &c.a)) || (rc = check_written(out, "out"))) return rc;
+  if (c.bytes > 0 && (workspace == nullptr || workspace_bytes < c.bytes))
+    return fail(FA_ERR_WORKSPACE, "this call needs %zu bytes of workspace (got %zu)", c.bytes,
+                workspace ? workspace_bytes : static_cast<size_t>(0));
+  if (c.bytes > 0 && reinterpret_cast<uintptr_t>(workspace) % 16) return fail(FA_ERR_ALIGN, "workspace must be 16-byte aligned");
+  int serr = 0;
+  c.a.status = status_word(&serr);
+  if (serr) return fail(FA_ERR_CUDA, "cannot locate the device status word");
+  c.a.lse = lse;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (c.decode) {
+    CUtensorMap map_k, map_v;
+    if ((rc = encode_byte_map(&map_k, k, c.box)) || (rc = encode_byte_map(&map_v, v, c.box))) return rc;
+    cudaError_t e = launch_decode_fp8(c.a, c.qa, c.plan, map_k, map_v, c.box, workspace, st);
+    if (e != cudaSuccess) return cuda_fail(e, "8-bit decode launch");
+    return FA_OK;
+  }
+  // restore the cache's visible part, then the forward pass on it; its checks
+  // come first, so that nothing is enqueued on an error
+  char* ws = static_cast<char*>(workspace);
+  for (fa_tensor* t : {&c.kd, &c.vd}) t->data = ws + (reinterpret_cast<uintptr_t>(t->data) - 256);
+  fa_forward_options dense{};
+  if (options) dense = *options;
+  dense.page_table = nullptr;
+  dense.page_size = dense.pages_per_seq = 0;
+  FwdArgs checked;
+  Path path;
+  if ((rc = prepare(q, &c.kd, &c.vd, out, scale, enable_gqa, score_mod, mask_mod, block_mask, split_kv, &dense,
+                    &checked, &path)))
+    return rc;
+  RestoreArgs rk{}, rv{};
+  const fa_tensor* src[2] = {k, v};
+  const fa_tensor* dst[2] = {&c.kd, &c.vd};
+  RestoreArgs* r[2] = {&rk, &rv};
+  for (int i = 0; i < 2; ++i)
+    *r[i] = RestoreArgs{static_cast<const uint8_t*>(src[i]->data),
+                        {src[i]->stride[0], src[i]->stride[1], src[i]->stride[2]},
+                        i ? quant->v_scale : quant->k_scale,
+                        dst[i]->data,
+                        (int)src[i]->size[3],
+                        q->dtype == FA_DTYPE_F32,
+                        codes_aligned16(src[i])};
+  cudaError_t e = launch_restore(c.a, c.qa, rk, rv, st);
+  if (e != cudaSuccess) return cuda_fail(e, "cache restore launch");
+  return flexattn_forward(q, &c.kd, &c.vd, out, lse, scale, enable_gqa, score_mod, mask_mod, block_mask, split_kv,
+                          &dense, ws + c.restored, workspace_bytes - c.restored, stream);
 }
 
 int flexattn_poll_device_status(void* stream, int32_t* status) {

@@ -1,0 +1,318 @@
+// Appending new keys and values to a dense or paged KV cache in bf16, fp32 or
+// e4m3 with a scale per block of tokens and head; keys (and the queries of the
+// same tokens) are normed and rotated on the way.  Contract and the rule for
+// the scales: include/flexattn.h.
+//
+// A CTA owns an aligned chunk of one sequence's slots (32, or one scale block
+// where that is longer) and a run of heads of k, of v or of q.  A scale block
+// never spans two chunks, so its largest magnitude is found inside the CTA: the
+// rows stay in registers between the pass that finds it and the pass that
+// rounds, and each new value is read once.  The maximum goes through shared
+// memory atomics on the bits of non-negative floats, which gives the same
+// result in every order.  Angles are computed once per token of the chunk and
+// shared by the CTA's heads.
+#include "headprep.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kAppThreads = 256;
+constexpr int kMaxChunk = 128;
+
+// 2^ceil(log2(amax / 448)) from the bits of a finite amax >= 0; 0 for 0.
+// 448 = 1.75 * 2^8: the exponent of amax less 8, and one more past 1.75.
+__device__ __forceinline__ float pow2_scale(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  if (u == 0u) return 0.0f;
+  int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = max(e, -126);
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// 8 floats as e4m3 codes (round to nearest even, +-448 at most, NaN kept).
+__device__ __forceinline__ uint2 e4m3x8(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code & 0xffu), __NV_E4M3);
+  return __half2float(__half(h));
+}
+
+// Where one sequence's new tokens go.
+struct Span {
+  int start, count;  // first slot, tokens
+  bool bad;          // something was refused
+};
+__device__ __forceinline__ Span append_span(const AppendArgs& a, int b) {
+  Span s;
+  s.start = __ldg(a.cache_len + b);
+  s.count = a.new_len ? __ldg(a.new_len + b) : a.N;
+  s.bad = s.count < 0 || s.count > a.N;
+  s.count = min(max(s.count, 0), a.N);
+  const int cap = a.page_table ? a.page_size * a.pages_per_seq : a.page_size;
+  if (s.start < 0 || s.start > cap) {
+    s.bad = s.bad || s.start < 0 || s.count > 0;
+    s.count = 0;
+    s.start = 0;
+  } else if (s.count > cap - s.start) {
+    s.bad = true;
+    s.count = cap - s.start;
+  }
+  return s;
+}
+
+template <int T, Pair kPair, bool kVec, int kIters>
+__global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int kGroups = kAppThreads / T;
+  extern __shared__ float tables[];  // cosines, then sines, of the chunk's tokens
+  __shared__ int s_outer[kMaxChunk];
+  __shared__ uint32_t s_amax[32];
+  __shared__ float s_scale[32], s_old[32];
+  const int b = blockIdx.z, t = threadIdx.x % T, grp = threadIdx.x / T, e0 = 8 * t;
+  const int rot = a.rope.rot, h2 = rot >> 1;
+  float* cos_t = tables;
+  float* sin_t = tables + a.chunk * h2;
+  const int kv_runs = (a.k.H + a.k_heads - 1) / a.k_heads;
+  const Span sp = append_span(a, b);
+  if (sp.bad && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) record_error(a.status, FA_ERR_PARAM);
+  const int* pos_row =
+      a.rope.pos ? a.rope.pos + static_cast<int64_t>(a.rope.pos_batch > 1 ? b : 0) * a.N : nullptr;
+  const int pos0 = __ldg(a.cache_len + b);
+  auto position = [&](int n) {
+    return pos_row ? __ldg(pos_row + n) : static_cast<int>(static_cast<uint32_t>(pos0) + static_cast<uint32_t>(n));
+  };
+
+  if (static_cast<int>(blockIdx.y) >= 2 * kv_runs) {
+    // ------------------------------------------------------------- queries
+    const int n0 = blockIdx.x * a.chunk, ntok = min(a.chunk, a.N - n0);
+    if (ntok <= 0) return;
+    const int hq0 = (blockIdx.y - 2 * kv_runs) * a.q_heads, nh = min(a.q_heads, a.q.H - hq0);
+    if (rot) {
+      for (int i = threadIdx.x; i < ntok * h2; i += kAppThreads)
+        angle(position(n0 + i / h2), __ldg(a.rope.inv_freq + i % h2), cos_t + i, sin_t + i);
+      __syncthreads();
+    }
+    float w[8];
+    if (a.q_norm.on) load_weight8(a.q_norm, e0, a.E, w);
+    const int rows = ntok * nh;
+    for (int r0 = 0; r0 < rows; r0 += kGroups) {
+      const int r = r0 + grp;
+      const bool ok = r < rows;
+      const int tk = ok ? r % ntok : 0, h = hq0 + (ok ? r / ntok : 0), n = n0 + tk;
+      float x[8], y[8];
+      load8<kVec>(row_ptr(a.q.p, a.q.f32, b * a.q.stride[0] + h * a.q.stride[1] + n * a.q.stride[2]), a.q.f32, e0, a.E,
+                  x);
+      if (a.q_norm.on) norm8<T>(x, w, a.q_norm.eps, 1.0f / static_cast<float>(a.E));
+      if (rot) {
+        float c[8], s[8];
+        lane_angles<kPair>(cos_t + tk * h2, sin_t + tk * h2, e0, rot, c, s);
+        rotate8<T, kPair>(x, c, s, 1.0f, t, rot, y);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = x[i];
+      }
+      if (ok)
+        store8<kVec>(row_ptr(a.q_out.p, a.q_out.f32,
+                             b * a.q_out.stride[0] + h * a.q_out.stride[1] + n * a.q_out.stride[2]),
+                     a.q_out.f32, e0, a.E, y);
+    }
+    return;
+  }
+
+  // ------------------------------------------------------- keys or values
+  const bool is_k = static_cast<int>(blockIdx.y) < kv_runs;
+  const int run = is_k ? blockIdx.y : blockIdx.y - kv_runs;
+  const int slot0 = (sp.start / a.chunk + static_cast<int>(blockIdx.x)) * a.chunk;
+  const int end = sp.start + sp.count;  // past the last new slot
+  if (sp.count == 0 || slot0 >= end) return;
+  const int D = is_k ? a.E : a.Ev;
+  const RowsIn& in = is_k ? a.k : a.v;
+  const bool turn = is_k && rot, norm = is_k && a.k_norm.on;
+  // page (or sequence) of each slot of the chunk that the call touches; -1: none
+  for (int i = threadIdx.x; i < a.chunk; i += kAppThreads) {
+    const int slot = slot0 + i;
+    int outer = -1;
+    if (slot < end) {
+      if (!a.page_table) {
+        outer = b;
+      } else {
+        outer = __ldg(a.page_table + static_cast<int64_t>(b) * a.pages_per_seq + slot / a.page_size);
+        if (outer < 0 || outer >= a.num_outer) {
+          // an id outside the pool is an error only where a new token needs it
+          if (slot >= sp.start) record_error(a.status, FA_ERR_PARAM);
+          outer = -1;
+        }
+      }
+    }
+    s_outer[i] = outer;
+  }
+  if (turn) {
+    for (int i = threadIdx.x; i < a.chunk * h2; i += kAppThreads) {
+      const int n = slot0 + i / h2 - sp.start;
+      if (n >= 0 && n < sp.count) angle(position(n), __ldg(a.rope.inv_freq + i % h2), cos_t + i, sin_t + i);
+    }
+  }
+  float w[8];
+  if (norm) load_weight8(a.k_norm, e0, D, w);
+  const int e4m3 = a.dtype == FA_DTYPE_E4M3;
+  const int sb_log = e4m3 ? __ffs(a.scale_block) - 1 : 5;
+  float* scales = is_k ? a.k_scale : a.v_scale;
+  char* cache = static_cast<char*>(is_k ? a.kc : a.vc);
+  const int64_t* cs = is_k ? a.kc_stride : a.vc_stride;
+  const bool cvec = is_k ? a.kc_vec : a.vc_vec;
+  __syncthreads();
+
+  for (int h = run * a.k_heads; h < min((run + 1) * a.k_heads, in.H); ++h) {
+    if (e4m3) {
+      if (threadIdx.x < 32) s_amax[threadIdx.x] = 0u;
+      __syncthreads();
+    }
+    float x[kIters][8];
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) {
+      const int n = slot0 + it * kGroups + grp - sp.start;
+      if (n >= 0 && n < sp.count) {
+        load8<kVec>(row_ptr(in.p, in.f32, b * in.stride[0] + h * in.stride[1] + n * in.stride[2]), in.f32, e0, D,
+                    x[it]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[it][i] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) {
+      const int row = it * kGroups + grp;
+      if (norm) norm8<T>(x[it], w, a.k_norm.eps, 1.0f / static_cast<float>(D));
+      if (turn) {
+        float c[8], s[8], y[8];
+        lane_angles<kPair>(cos_t + row * h2, sin_t + row * h2, e0, rot, c, s);
+        rotate8<T, kPair>(x[it], c, s, 1.0f, t, rot, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[it][i] = y[i];
+      }
+      if (e4m3) {
+        float m = 0.0f;  // of this row's finite magnitudes (rows without a new token: 0)
+        const int n = slot0 + row - sp.start;
+        if (n >= 0 && n < sp.count) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[it][i]) < INFINITY ? fabsf(x[it][i]) : 0.0f);
+        }
+#pragma unroll
+        for (int o = T / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (t == 0 && m > 0.0f) atomicMax(&s_amax[row >> sb_log], __float_as_uint(m));
+      }
+    }
+    if (e4m3) {
+      __syncthreads();
+      const int blk = threadIdx.x;
+      if (blk < (a.chunk >> sb_log)) {
+        const int bs = slot0 + (blk << sb_log), first = max(bs, sp.start);
+        // touched by a new token, and that token's page is in the pool
+        if (first < min(bs + a.scale_block, end) && s_outer[first - slot0] >= 0) {
+          float* sc = scales + (static_cast<int64_t>(s_outer[first - slot0]) * in.H + h) * a.scales_per_outer +
+                      (bs % a.page_size) / a.scale_block;
+          const float fresh = pow2_scale(__uint_as_float(s_amax[blk]));
+          const bool had = bs < sp.start;
+          const float old = had ? *sc : 0.0f, now = had ? fmaxf(old, fresh) : fresh;
+          s_old[blk] = old;
+          s_scale[blk] = now;
+          if (!had || now != old) *sc = now;
+        } else {
+          s_old[blk] = s_scale[blk] = 0.0f;
+        }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) {
+      const int row = it * kGroups + grp, slot = slot0 + row, outer = s_outer[row];
+      if (outer < 0 || e0 >= D) continue;
+      const int64_t off = outer * cs[0] + h * cs[1] + static_cast<int64_t>(slot % a.page_size) * cs[2];
+      if (!e4m3) {
+        if (slot < sp.start) continue;
+        const int f32 = a.dtype == FA_DTYPE_F32;
+        if (cvec)
+          store8<true>(row_ptr(static_cast<void*>(cache), f32, off), f32, e0, D, x[it]);
+        else
+          store8<false>(row_ptr(static_cast<void*>(cache), f32, off), f32, e0, D, x[it]);
+        continue;
+      }
+      const float now = s_scale[row >> sb_log], inv = now > 0.0f ? 1.0f / now : 0.0f;
+      uint8_t* dst = reinterpret_cast<uint8_t*>(cache) + off + e0;
+      float y[8];
+      if (slot >= sp.start) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = x[it][i] * inv;
+      } else {
+        // an older token of a block: rounded again where its scale grew
+        const float old = s_old[row >> sb_log];
+        if (!(now > old)) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = e0 + i < D ? e4m3_value(dst[i]) * (old * inv) : 0.0f;
+      }
+      const uint2 code = e4m3x8(y);
+      if (cvec) {
+        *reinterpret_cast<uint2*>(dst) = code;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (e0 + i < D) dst[i] = static_cast<uint8_t>((i < 4 ? code.x : code.y) >> (8 * (i & 3)));
+      }
+    }
+    // the next head's maxima are cleared only after this head's scales were read
+    if (e4m3) __syncthreads();
+  }
+}
+
+template <int T, Pair kPair, bool kVec>
+cudaError_t launch_append_i(const AppendArgs& a, dim3 grid, size_t smem, cudaStream_t st) {
+  constexpr int kUnit = T / 8;  // turns of the CTA's groups over 32 slots
+  auto kern = a.chunk == 32   ? append_kernel<T, kPair, kVec, kUnit>
+              : a.chunk == 64 ? append_kernel<T, kPair, kVec, 2 * kUnit>
+                              : append_kernel<T, kPair, kVec, 4 * kUnit>;
+  if (smem > 40 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<grid, kAppThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <int T>
+cudaError_t launch_append_t(const AppendArgs& a, bool vec, dim3 grid, size_t smem, cudaStream_t st) {
+  if (a.rope.rot == 0 || a.rope.interleaved)
+    return vec ? launch_append_i<T, Pair::kNext, true>(a, grid, smem, st)
+               : launch_append_i<T, Pair::kNext, false>(a, grid, smem, st);
+  if (!vec) return launch_append_i<T, Pair::kHalfAny, false>(a, grid, smem, st);
+  return (a.rope.rot / 2) % 8 == 0 ? launch_append_i<T, Pair::kHalf, true>(a, grid, smem, st)
+                                   : launch_append_i<T, Pair::kHalfAny, true>(a, grid, smem, st);
+}
+
+}  // namespace
+
+cudaError_t launch_append(AppendArgs a, int num_sms, cudaStream_t st) {
+  const bool small = a.E <= 64 && a.Ev <= 64;
+  const int groups = kAppThreads / (small ? 8 : 16);
+  a.chunk = a.dtype == FA_DTYPE_E4M3 && a.scale_block > 32 ? a.scale_block : 32;
+  // N tokens that start anywhere in a chunk touch this many chunks at most
+  const int chunks = static_cast<int>((static_cast<int64_t>(a.N) + a.chunk - 2) / a.chunk) + 1;
+  // Heads of k share the chunk's angles: as many a CTA as leave the GPU four
+  // CTAs an SM.
+  const int64_t per_head = static_cast<int64_t>(chunks) * a.B;
+  a.k_heads = 1;
+  while (2 * a.k_heads <= a.k.H && per_head * (a.k.H / (2 * a.k_heads)) >= 4 * num_sms) a.k_heads *= 2;
+  const int ntok = a.N < a.chunk ? a.N : a.chunk;
+  a.q_heads = ntok < groups ? (groups + ntok - 1) / ntok : 8;
+  const int kv_runs = (a.k.H + a.k_heads - 1) / a.k_heads;
+  const int q_runs = a.q.p ? (a.q.H + a.q_heads - 1) / a.q_heads : 0;
+  const dim3 grid(chunks, 2 * kv_runs + q_runs, a.B);
+  const size_t smem = static_cast<size_t>(a.chunk) * (a.rope.rot / 2) * 2 * sizeof(float);
+  const bool vec = a.k_vec && a.v_vec && (!a.q.p || a.q_vec);
+  return small ? launch_append_t<8>(a, vec, grid, smem, st) : launch_append_t<16>(a, vec, grid, smem, st);
+}
+
+}  // namespace fa

@@ -1,0 +1,837 @@
+// Split-KV decode over an e4m3 cache: codes under one fp32 scale per block of
+// slots and head (definition: include/flexattn.h, flexattn_forward_fp8).
+//
+// A step streams every code of the visible cache once, so HBM is the bound and
+// the codes must reach the tensor cores without a conversion pass over them
+// (at this rate an SM has 23 bytes a clock to take; widening every code and
+// writing it back to shared memory would cost more issue slots than the whole
+// softmax).  So the products run on e4m3 operands (tcgen05 kind::f8f6f4) and
+// the other operands are made to fit exactly or nearly so:
+//
+//   * a bf16 query value has 8 significant bits.  Divided by a power of two s_r
+//     that brings its row below 448, it is the sum of two e4m3 terms: hi, its
+//     rounding to 4 bits, and lo / 16, what is left, a multiple of its last
+//     place of at most 4 bits.  The sum is exact for values down to 2^-14 of
+//     the row's largest, and off by 2^-22 of that one at most below.
+//   * a softmax weight w is likewise hi + lo / 16, rounded: at most 2^-8 w, as
+//     a rounding to bf16, and a third of that in the mean square.
+//
+// hi and lo are neighbouring columns of the small N side: 16 query rows make
+// N = 32, which costs the tensor core what N = 16 does.  With s^k_j, s^v_j the
+// scales of key j, c_j the codes, in log2 units:
+//   t_rj  = rule(s_r s^k_j scale (hi_r + lo_r / 16) . c^k_j)
+//   w_rj  = 2^(t_rj + log2 s^v_j - m_r + 6),  m_r the running maximum of
+//           t + log2 s^v, moved when some key passes it by more than 2, so
+//           that w <= 2^8 stays inside e4m3
+//   O_r   = sum_j w_rj c^v_j,   l_r = sum_j w_rj / s^v_j,   out = O_r / l_r.
+// Carrying the value scale inside the weight keeps it out of the codes and
+// bounds the weights' rounding against the largest contribution to the output.
+//
+// Layout: the 128 keys of a tile are the M side of both products (S^T = K Q^T,
+// O^T = V^T W^T with V read MN-major), as in decode.cu: a softmax thread owns
+// one key, its TMEM lane, and the 16 rows' scores.  Rows of 128 bytes with a
+// 128-byte swizzle; a head dim below 128 is padded with zeros by TMA.
+//   warp 0      TMA: one box per page piece, a lane each.
+//   warp 1      TMEM allocation; one thread issues the MMAs, whichever product
+//               is ready first.
+//   warps 2-5   softmax (warp % 4 is the TMEM lane quadrant), epilogue.
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include "common.cuh"
+#include "fastmath.cuh"
+#include "launch.h"
+#include "mods.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 192;
+constexpr int kKeys = 128;        // keys per tile: the M side
+constexpr int kRows = 16;         // query rows per CTA
+constexpr int kCols = 2 * kRows;  // hi and lo columns: the N side
+constexpr int kTmemCols = 128;    // S^T buffers at 0 and 32, O^T at 64
+constexpr int kRing = 6;          // K or V tiles of 16 KB in flight
+constexpr int kTileBytes = kKeys * 128;
+constexpr int kQBytes = kCols * 128;
+constexpr int kPBytes = kCols * 128;
+constexpr int kSmemBytes = kRing * kTileBytes + kQBytes + 2 * kPBytes + 1024;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// Start of the running maximum: finite and below any real score.
+constexpr float kNoKeyMax = -1.0e30f;
+// The maximum moves when a key passes it by more than kSlack; weights carry
+// 2^kShift, so they stay below 2^(kSlack + kShift) = 256 < 448.
+constexpr float kSlack = 2.0f;
+constexpr float kShift = 6.0f;
+
+// kind::f8f6f4 instruction descriptor: e4m3 A and B, fp32 accumulator.
+constexpr uint32_t idesc_e4m3(int M, int N, int a_mn_major) {
+  return (1u << 4) | (static_cast<uint32_t>(a_mn_major) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::
+          "r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+
+// Two values as (hi, lo) e4m3 pairs: v = hi + lo / 16.
+__device__ __forceinline__ void split_e4m3(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+  hi = __nv_cvt_float2_to_fp8x2(make_float2(v0, v1), __NV_SATFINITE, __NV_E4M3);
+  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3);
+  const float2 h = __half22float2(__half2(r));
+  lo = __nv_cvt_float2_to_fp8x2(make_float2((v0 - h.x) * 16.0f, (v1 - h.y) * 16.0f), __NV_SATFINITE, __NV_E4M3);
+}
+
+struct Bars {
+  uint64_t full[kRing], empty[kRing];
+  uint64_t s_full[2], s_free[2], p_full[2], p_free[2], o_final;
+  uint32_t tmem_base;
+  int abort;
+};
+
+__device__ __forceinline__ int listed_tile(const FwdArgs& a, int64_t brow, int nfull, int j) {
+  return j < nfull ? __ldg(a.bm.full_kv_indices + brow * a.bm.Nb + j)
+                   : __ldg(a.bm.kv_indices + brow * a.bm.Nb + (j - nfull));
+}
+
+// Reduce-scatter of 16 values per lane over a warp: lane l gets the reduction
+// over all lanes of value (l >> 1) & 15, in sixteen shuffles.
+template <bool kMax>
+__device__ __forceinline__ float reduce_rows(const float (&v)[16], int lane) {
+  auto op = [](float x, float y) { return kMax ? fmaxf(x, y) : x + y; };
+  float a[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a[i] = v[i];
+#pragma unroll
+  for (int w = 8; w >= 1; w >>= 1) {
+    const bool up = lane & (2 * w);
+#pragma unroll
+    for (int i = 0; i < w; ++i)
+      a[i] = op(up ? a[w + i] : a[i], __shfl_xor_sync(0xffffffffu, up ? a[i] : a[w + i], 2 * w));
+  }
+  return op(a[0], __shfl_xor_sync(0xffffffffu, a[0], 1));
+}
+
+// The sequence of the given rank by length of its list of tiles, longest first
+// (ties by index), for up to 32 sequences with lists of their own; else the
+// batch order.  Called by every lane of a warp.
+__device__ __forceinline__ int ranked_sequence(const FwdArgs& a, int rank) {
+  if (a.B > 32 || a.bm.B == 1) return rank;
+  const int lane = threadIdx.x & 31;
+  int cnt = -1;
+  if (lane < a.B) {
+    const int64_t row = static_cast<int64_t>(lane) * a.bm.H * a.bm.Mb;
+    cnt = __ldg(a.bm.full_kv_num_blocks + row) + __ldg(a.bm.kv_num_blocks + row);
+  }
+  int r = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const int cj = __shfl_sync(0xffffffffu, cnt, j);
+    r += (cj > cnt || (cj == cnt && j < lane)) ? 1 : 0;
+  }
+  const unsigned hit = __ballot_sync(0xffffffffu, lane < a.B && r == rank);
+  return hit ? __ffs(hit) - 1 : rank;
+}
+
+// tanh of a score under a cap: the odd series for small arguments, else
+// 1 - 2 / (1 + e^(2 |y|)), whose absolute error of about 2^-22 is below 2^-20
+// of the result there.
+__device__ __forceinline__ float tanh_large(float y) {
+  const float e = ex2_approx(2.0f * kLog2e * fabsf(y));
+  return copysignf(1.0f - __fdividef(2.0f, 1.0f + e), y);
+}
+
+template <int SCORE>
+__global__ void __launch_bounds__(kThreads, 2)
+    decode_fp8_kernel(const __grid_constant__ FwdArgs a, const __grid_constant__ QuantArgs qa, const Fp8Plan p,
+                      const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, int box,
+                      float* ws_o, float* ws_lse, float* ws_max) {
+  constexpr int R = kRing;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Bars bars;
+  __shared__ float s_red[2][4][kRows];
+  __shared__ int s_qpos[kRows], s_head[kRows], s_row[kRows], s_pq[kRows];
+  __shared__ float s_slope[kRows], s_unit[kRows];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sKV = smem;
+  uint8_t* sQ = smem + R * kTileBytes;
+  uint8_t* sP = sQ + kQBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // grid (KV head x row chunk, split, rank): the longest sequences start first
+  const int split = blockIdx.y;
+  const int hk = blockIdx.x / p.row_chunks, rc = blockIdx.x % p.row_chunks;
+  const int b = ranked_sequence(a, static_cast<int>(blockIdx.z));
+  const int S_b = seq_len_b(a.mask, b, a.S);
+  // Rows of the chunk: 16 consecutive ones of the group's G x L (head, position)
+  // pairs; with per-head lists, of one head's L positions.
+  const int per_head = a.bm.H > 1 ? (a.L + kRows - 1) / kRows : 0;
+  const int g0 = per_head ? rc / per_head : 0;
+  const int rho0 = (per_head ? rc % per_head : rc) * kRows;
+  const int rho_end = per_head ? a.L : a.G * a.L;
+  const int bmb = a.bm.B > 1 ? b : 0;
+  const int bmh = per_head ? hk * a.G + g0 : 0;
+  const int64_t brow = (static_cast<int64_t>(bmb) * a.bm.H + bmh) * a.bm.Mb;
+  const int nfull = __ldg(a.bm.full_kv_num_blocks + brow);
+  const int ntiles = nfull + __ldg(a.bm.kv_num_blocks + brow);
+  const int chunk = (ntiles + p.splits - 1) / p.splits;
+  const int t0 = split * chunk;
+  const int t1 = min(ntiles, t0 + chunk);
+  const int nsub = t1 > t0 ? t1 - t0 : 0;
+  volatile int* abort = &bars.abort;
+  const bool has_pos = SCORE == FA_SCORE_CAP_THEN_BIAS && a.score.pos != nullptr;
+
+  // Row and outer coordinate (batch, or page) of this lane's box of tile j.
+  // Slots at or past the sequence's end are not read: a row past the tensor's
+  // end makes TMA fill the box with zeros.
+  const int nbox = kKeys / box;
+  auto box_addr = [&](int j, int& row, int& outer) {
+    const int kv = listed_tile(a, brow, nfull, t0 + j) * kKeys + lane * box;
+    row = kv;
+    outer = b;
+    if (kv >= S_b) {
+      row = a.page_table ? a.page_size : a.S;
+      outer = 0;
+    } else if (a.page_table) {
+      outer = cache_page(a.page_table, a.pages_per_seq, a.page_size, a.num_pages, a.status, b, kv);
+      row = kv % a.page_size;
+    }
+  };
+  int row_c = 0, outer_c = 0, row_n = 0, outer_n = 0;  // this tile's box, and the next tile's
+  // K (u even) or V (u odd) of tile u / 2 into ring entry u % R; all lanes of warp 0
+  auto issue_load = [&](int u) {
+    if (lane < nbox) {
+      if (u == 0) {
+        box_addr(0, row_c, outer_c);
+        if (nsub > 1) box_addr(1, row_n, outer_n);
+      } else if ((u & 1) == 0) {
+        row_c = row_n;
+        outer_c = outer_n;
+        if ((u >> 1) + 1 < nsub) box_addr((u >> 1) + 1, row_n, outer_n);
+      }
+    }
+    const int e = u % R;
+    if (lane == 0) mbar_expect_tx(&bars.full[e], kTileBytes);
+    __syncwarp();
+    if (lane < nbox)
+      tma_load_4d(sKV + e * kTileBytes + lane * box * 128, (u & 1) ? &map_v : &map_k, &bars.full[e], 0, row_c, hk,
+                  outer_c);
+  };
+
+  const int first_loads = min(R, 2 * nsub);
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int s = 0; s < R; ++s) {
+        mbar_init(&bars.full[s], 1);
+        mbar_init(&bars.empty[s], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bars.s_full[i], 1);
+        mbar_init(&bars.s_free[i], 4);
+        mbar_init(&bars.p_full[i], 4);
+        mbar_init(&bars.p_free[i], 1);
+      }
+      mbar_init(&bars.o_final, 1);
+      bars.abort = 0;
+      mbar_fence_init();
+      if (nsub > 0) {
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+      }
+    }
+    __syncwarp();
+    for (int u = 0; u < first_loads; ++u) issue_load(u);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars.tmem_base, kTmemCols);
+    if (lane < kRows) {
+      const int rho = rho0 + lane;
+      const bool ok = rho < rho_end;
+      const int head = hk * a.G + (per_head ? g0 : min(rho / a.L, a.G - 1)), i = per_head ? rho : rho % a.L;
+      const int Hs = a.score.slope_heads > 0 ? a.score.slope_heads : a.Hq;
+      s_qpos[lane] = query_pos(i, a.L, S_b);
+      s_head[lane] = ok ? head : -1;
+      s_row[lane] = ok ? i : 0;
+      s_slope[lane] = distance_slope(head, Hs);
+      s_pq[lane] = has_pos ? pos_at(a.score, b, s_qpos[lane], a.S) : 0;
+    }
+  }
+  if (warp >= 2) {
+    // Query rows as hi (rows 0-15) and lo (16-31) terms, 128-byte swizzled;
+    // 8 threads a row, 16 values each.
+    const int r = (threadIdx.x - 64) >> 3, seg = threadIdx.x & 7;
+    const int rho = rho0 + r;
+    float q[16];
+    float amax = 0.0f;
+    bool finite = true;
+    const bool ok = rho < rho_end;
+    const int head = hk * a.G + (per_head ? g0 : min(rho / a.L, a.G - 1)), i = per_head ? rho : rho % a.L;
+    const __nv_bfloat16* src =
+        static_cast<const __nv_bfloat16*>(a.q) + b * a.q_stride[0] + head * a.q_stride[1] + i * a.q_stride[2];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) q[e] = 0.0f;
+    if (ok && seg * 16 < a.E) {  // E is a multiple of 16
+      const uint4 v0 = *reinterpret_cast<const uint4*>(src + seg * 16);
+      const uint4 v1 = *reinterpret_cast<const uint4*>(src + seg * 16 + 8);
+      const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        q[2 * e] = __uint_as_float(w[e] << 16);
+        q[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      finite = finite && fabsf(q[e]) < INFINITY;
+      amax = fmaxf(amax, fabsf(q[e]));
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      finite = __shfl_xor_sync(0xffffffffu, static_cast<int>(finite), o) && finite;
+    }
+    // 2^x with amax / 2^x in (224, 448]
+    const uint32_t ab = __float_as_uint(amax);
+    int x = static_cast<int>(ab >> 23) - 127 - 8 + ((ab & 0x7fffffu) > 0x600000u ? 1 : 0);
+    x = min(max(x, -126), 126);
+    if (!finite || amax == 0.0f) x = 0;
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - x) << 23);
+    // a row with an infinity or a NaN: every score, and so the output, is NaN
+    if (seg == 0) s_unit[r] = finite ? __uint_as_float(static_cast<uint32_t>(127 + x) << 23) : NAN;
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t h0, h1, l0, l1;
+      split_e4m3(q[4 * c] * inv, q[4 * c + 1] * inv, h0, l0);
+      split_e4m3(q[4 * c + 2] * inv, q[4 * c + 3] * inv, h1, l1);
+      hi[c] = h0 | (h1 << 16);
+      lo[c] = l0 | (l1 << 16);
+    }
+    const int off = (r >> 3) * 1024 + (r & 7) * 128 + ((seg ^ (r & 7)) << 4);
+    *reinterpret_cast<uint4*>(sQ + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(sQ + kRows * 128 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = bars.tmem_base;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA
+    if (nsub > 0) {
+      int issued = first_loads;
+      for (int u = first_loads; u < 2 * nsub; ++u) {
+        const bool ok = !*abort && mbar_wait(&bars.empty[u % R], ((u / R) - 1) & 1, abort, a.status, a.wait_cycles);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        issue_load(u);
+        issued = u + 1;
+      }
+      // every copy issued lands before this warp leaves (only the last R can
+      // be pending: earlier entries were waited free before their reuse)
+      volatile int never = 0;
+      for (int u = (issued > R ? issued - R : 0); u < issued; ++u)
+        mbar_wait(&bars.full[u % R], (u / R) & 1, &never, nullptr);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_e4m3(kKeys, kCols, 0);
+      constexpr uint32_t idesc_o = idesc_e4m3(kKeys, kCols, 1);
+      const uint64_t dk0 = umma_desc_sw128(smem_u32(sKV), 16, 1024);
+      // V^T: M runs along a row of V, one 128-byte block wide; 8 keys a group
+      const uint64_t dv0 = umma_desc_sw128(smem_u32(sKV), kTileBytes, 1024);
+      const uint64_t dq0 = umma_desc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t dp0 = umma_desc_sw128(smem_u32(sP), 16, 1024);
+      const int ksteps = (a.E + 31) / 32;  // Q and K are zero past E
+      auto issue_qk = [&](int j) {
+        const int e = (2 * j) % R, sb = j & 1;
+        tc_fence_after();
+        for (int kk = 0; kk < ksteps; ++kk)
+          umma_e4m3(tbase + kCols * sb, dk0 + ((e * kTileBytes + kk * 32) >> 4), dq0 + ((kk * 32) >> 4), idesc_s,
+                    kk > 0 ? 1u : 0u);
+        umma_commit(&bars.s_full[sb]);
+        umma_commit(&bars.empty[e]);
+      };
+      auto issue_pv = [&](int j) {
+        const int e = (2 * j + 1) % R, pb = j & 1;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 32; ++kk)
+          umma_e4m3(tbase + 2 * kCols, dv0 + ((e * kTileBytes + kk * 32 * 128) >> 4),
+                    dp0 + ((pb * kPBytes + kk * 32) >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(&bars.p_free[pb]);
+        umma_commit(&bars.empty[e]);
+      };
+      // Whichever product is ready first.  Tile jq's K entry last held K of
+      // tile jq - R / 2, whose QK was issued before, and likewise for V: a
+      // tested barrier is never two phases behind.
+      int jq = 0, jp = 0;
+      long long idle_from = clock64();
+      while (jp < nsub) {
+        bool progressed = false;
+        if (jq < nsub && mbar_test(&bars.full[(2 * jq) % R], ((2 * jq) / R) & 1) &&
+            (jq < 2 || mbar_test(&bars.s_free[jq & 1], ((jq - 2) >> 1) & 1))) {
+          issue_qk(jq++);
+          progressed = true;
+        }
+        if (jp < jq && mbar_test(&bars.p_full[jp & 1], (jp >> 1) & 1) &&
+            mbar_test(&bars.full[(2 * jp + 1) % R], ((2 * jp + 1) / R) & 1)) {
+          issue_pv(jp++);
+          progressed = true;
+        }
+        if (progressed) {
+          idle_from = clock64();
+        } else if (*abort) {
+          break;
+        } else if (clock64() - idle_from > a.wait_cycles) {
+          record_error(a.status, FA_ERR_TIMEOUT);
+          *abort = 1;
+          break;
+        }
+      }
+      // every MMA issued above completes before the epilogue or TMEM release
+      umma_commit(&bars.o_final);
+      volatile int never = 0;
+      mbar_wait(&bars.o_final, 0, &never, nullptr);
+    }
+  } else {
+    // -------------------------------------------------------------- softmax
+    const int qd = warp & 3;
+    const int kk = qd * 32 + lane;  // this thread's key of a tile; its TMEM lane
+    const uint32_t lane_base = static_cast<uint32_t>(qd * 32) << 16;
+    constexpr bool kCapped = SCORE == FA_SCORE_SOFTCAP || SCORE == FA_SCORE_CAP_THEN_BIAS;
+    const float c_in = kCapped ? a.scale / a.score.cap : a.scale * kLog2e;
+    const float c_out = kCapped ? a.score.cap * kLog2e : 1.0f;
+    const bool want_max = a.max_scores != nullptr;
+    float m_run[kRows], l_part[kRows], tm[kRows], unit[kRows];
+    float sl2[kRows], sq2[kRows];  // distance bias in log2 units: slope, slope * q
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      m_run[r] = kNoKeyMax;
+      l_part[r] = 0.0f;
+      tm[r] = -INFINITY;
+      unit[r] = s_unit[r] * c_in;
+      sl2[r] = s_slope[r] * kLog2e;
+      sq2[r] = sl2[r] * static_cast<float>(s_qpos[r]);
+    }
+    // This key's scales, loaded a tile ahead, its page two tiles ahead (the
+    // two loads depend on one another).
+    auto key_of = [&](int j) { return listed_tile(a, brow, nfull, t0 + j) * kKeys + kk; };
+    auto page_of = [&](int j) {  // -1 past the sequence's end
+      if (j >= nsub) return -1;
+      const int kv = key_of(j);
+      if (kv >= S_b) return -1;
+      if (!a.page_table) return b;
+      const int pg = __ldg(a.page_table + static_cast<int64_t>(b) * a.pages_per_seq + kv / a.page_size);
+      return min(max(pg, 0), a.num_pages - 1);  // warp 0 records an id outside the pool
+    };
+    auto scales_of = [&](int j, int pg, float& ks, float& vs) {
+      ks = vs = 1.0f;
+      if (pg < 0) return;
+      const int kv = key_of(j), at = a.page_table ? kv % a.page_size : kv;
+      const int64_t i = (static_cast<int64_t>(pg) * a.Hkv + hk) * qa.scales_per_outer + (at >> qa.block_log);
+      ks = __ldg(qa.k_scale + i);
+      vs = __ldg(qa.v_scale + i);
+    };
+    float ks_n, vs_n;
+    scales_of(0, page_of(0), ks_n, vs_n);
+    int pg_n = page_of(1);
+    bool alive = true;
+    for (int j = 0; j < nsub; ++j) {
+      const int sb = j & 1;
+      const int jt = t0 + j;
+      const int kv0 = listed_tile(a, brow, nfull, jt) * kKeys, kv = kv0 + kk;
+      const float ks = ks_n, vs = fmaxf(vs_n, 7.888609052210118e-31f);  // 2^-100: a block of zeros has scale 0
+      scales_of(j + 1, pg_n, ks_n, vs_n);
+      pg_n = page_of(j + 2);
+      const float lv = log2f(vs), ivs = 1.0f / vs;
+      bool ok = alive && __all_sync(0xffffffffu, mbar_wait(&bars.s_full[sb], (j >> 1) & 1, abort, a.status,
+                                                           a.wait_cycles));
+      float t[kRows];  // score + log2 of the value scale
+      bool grow = false;
+      if (ok) {
+        uint32_t sh[kRows], sl[kRows];
+        tc_fence_after();
+        tmem_ld16(tbase + lane_base + kCols * sb, sh);
+        tmem_ld16(tbase + lane_base + kCols * sb + kRows, sl);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.s_free[sb]);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+          t[r] = fmaf(__uint_as_float(sl[r]), 0.0625f, __uint_as_float(sh[r])) * (unit[r] * ks);
+        if constexpr (kCapped) {
+          float th[kRows];
+          bool big = false;
+#pragma unroll
+          for (int i = 0; i < kRows / 2; ++i) {
+            float2 u2;
+            const float2 v2 = tanh_poly2(make_float2(t[2 * i], t[2 * i + 1]), u2);
+            th[2 * i] = v2.x;
+            th[2 * i + 1] = v2.y;
+            big |= !(fmaxf(u2.x, u2.y) <= kTanhPolyMax * kTanhPolyMax);
+          }
+          if (__any_sync(0xffffffffu, big)) {
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+              if (!(fabsf(t[r]) <= kTanhPolyMax)) th[r] = tanh_large(t[r]);
+          }
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) t[r] = th[r] * c_out;
+        }
+        if constexpr (SCORE == FA_SCORE_ALIBI) {
+          const float kvf = static_cast<float>(kv);
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) t[r] += fmaf(sl2[r], kvf, -sq2[r]);
+        }
+        if constexpr (SCORE == FA_SCORE_CAP_THEN_BIAS) {
+          const int pk = has_pos ? pos_at(a.score, b, kv, a.S) : kv;
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) {
+            const int d = has_pos ? pk - s_pq[r] : kv - s_qpos[r];
+            t[r] = fmaf(sl2[r], static_cast<float>(d), t[r]);
+          }
+        }
+        // element mask on listed-partial tiles and at the end of the sequence
+        if (jt >= nfull || kv0 + kKeys > S_b) {
+#pragma unroll
+          for (int r = 0; r < kRows; ++r)
+            if (s_head[r] < 0 || !mask_visible(a.mask, b, s_head[r], s_qpos[r], kv, S_b, a.S)) t[r] = -INFINITY;
+        }
+        if (want_max) {
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) tm[r] = fmaxf(tm[r], t[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          t[r] += lv;
+          grow |= t[r] > m_run[r] + kSlack;
+        }
+      }
+      // one vote per tile: as usual, or a wait gave up, or a maximum moves
+      if (named_bar_or(1, 128, !ok || grow)) {
+        if (named_bar_or(1, 128, !ok)) {
+          alive = false;
+          break;
+        }
+        const float v = reduce_rows<true>(t, lane);
+        if ((lane & 1) == 0) s_red[0][qd][(lane >> 1) & 15] = v;
+        named_bar_sync(1, 128);
+        float alpha[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          const float tmax = fmaxf(fmaxf(s_red[0][0][r], s_red[0][1][r]), fmaxf(s_red[0][2][r], s_red[0][3][r]));
+          const float mn = fmaxf(m_run[r], tmax);
+          alpha[r] = ex2_approx(m_run[r] - mn);
+          m_run[r] = mn;
+          l_part[r] *= alpha[r];
+        }
+        named_bar_sync(1, 128);  // s_red is read by all before its next use
+        if (j > 0) {
+          // O^T holds tiles 0 .. j-1: once the last of them is in, rescale
+          const int jp = j - 1;
+          alive = __all_sync(0xffffffffu, mbar_wait(&bars.p_free[jp & 1], (jp >> 1) & 1, abort, a.status,
+                                                    a.wait_cycles));
+          if (alive) {
+            tc_fence_after();
+            uint32_t o[kRows], o2[kRows];
+            tmem_ld16(tbase + lane_base + 2 * kCols, o);
+            tmem_ld16(tbase + lane_base + 2 * kCols + kRows, o2);
+            tmem_wait_ld();
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+              o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r]);
+              o2[r] = __float_as_uint(__uint_as_float(o2[r]) * alpha[r]);
+            }
+            tmem_st16(tbase + lane_base + 2 * kCols, o);
+            tmem_st16(tbase + lane_base + 2 * kCols + kRows, o2);
+            tmem_wait_st();
+          }
+        }
+      }
+      // weights of this tile into buffer j & 1, free once PV of tile j - 2 is done
+      if (alive && j >= 2)
+        alive = __all_sync(0xffffffffu, mbar_wait(&bars.p_free[sb], ((j - 2) >> 1) & 1, abort, a.status,
+                                                  a.wait_cycles));
+      // Values past the sequence's end may hold anything (0 * NaN is NaN):
+      // their rows are cleared before the product reads them.
+      if (alive && kv0 + kKeys > S_b) {
+        const int u = 2 * j + 1;
+        alive = __all_sync(0xffffffffu, mbar_wait(&bars.full[u % R], (u / R) & 1, abort, a.status, a.wait_cycles));
+        if (alive && kv >= S_b) {
+          uint4* vrow = reinterpret_cast<uint4*>(sKV + (u % R) * kTileBytes + kk * 128);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) vrow[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      if (alive) {
+        uint8_t* pbuf = sP + sb * kPBytes + (kk & 15);
+        const int ch = kk >> 4;
+#pragma unroll
+        for (int r = 0; r < kRows; r += 2) {
+          const float w0 = ex2_approx(t[r] - (m_run[r] - kShift)), w1 = ex2_approx(t[r + 1] - (m_run[r + 1] - kShift));
+          l_part[r] = fmaf(w0, ivs, l_part[r]);
+          l_part[r + 1] = fmaf(w1, ivs, l_part[r + 1]);
+          uint32_t hi, lo;
+          split_e4m3(w0, w1, hi, lo);
+          uint8_t* p0 = pbuf + (r >> 3) * 1024 + (r & 7) * 128 + ((ch ^ (r & 7)) << 4);
+          uint8_t* p1 = pbuf + (r >> 3) * 1024 + ((r + 1) & 7) * 128 + ((ch ^ ((r + 1) & 7)) << 4);
+          p0[0] = static_cast<uint8_t>(hi);
+          p1[0] = static_cast<uint8_t>(hi >> 8);
+          p0[kRows * 128] = static_cast<uint8_t>(lo);
+          p1[kRows * 128] = static_cast<uint8_t>(lo >> 8);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[sb]);
+      }
+    }
+    // every softmax thread arrives here together (the loop is left only
+    // through the vote, or at its end)
+    bool fin = alive;
+    if (fin && nsub > 0) fin = mbar_wait(&bars.o_final, 0, abort, a.status, a.wait_cycles);
+    fin = named_bar_and(1, 128, fin && !*abort);
+    if (fin) {
+      tc_fence_after();
+      uint32_t o[kRows], o2[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) o[r] = o2[r] = 0u;
+      if (nsub > 0) {
+        tmem_ld16(tbase + lane_base + 2 * kCols, o);
+        tmem_ld16(tbase + lane_base + 2 * kCols + kRows, o2);
+        tmem_wait_ld();
+      }
+      const float ls = reduce_rows<false>(l_part, lane);
+      const float lm = reduce_rows<true>(tm, lane);
+      if ((lane & 1) == 0) {
+        s_red[0][qd][(lane >> 1) & 15] = ls;
+        s_red[1][qd][(lane >> 1) & 15] = lm;
+      }
+      named_bar_sync(1, 128);
+      const int ev = kk;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const int hq = s_head[r];
+        if (hq < 0) continue;
+        const float l = (s_red[0][0][r] + s_red[0][1][r]) + (s_red[0][2][r] + s_red[0][3][r]);
+        const float top = fmaxf(fmaxf(s_red[1][0][r], s_red[1][1][r]), fmaxf(s_red[1][2][r], s_red[1][3][r]));
+        // a row without a visible key (in this split) has l = 0: out 0 and lse
+        // -inf, unless the caller promised there is none and there is one
+        // split; NaN stays NaN
+        const bool live = (a.rows_safe && p.splits == 1) || !(l == 0.0f);
+        const float inv = live ? 1.0f / l : 0.0f;
+        const float lse = live ? ((m_run[r] - kShift) + log2f(l)) * kLn2 : -INFINITY;
+        const int64_t row_id = (static_cast<int64_t>(b) * a.Hq + hq) * a.L + s_row[r];
+        const float val = fmaf(__uint_as_float(o2[r]), 0.0625f, __uint_as_float(o[r])) * inv;
+        if (p.splits == 1) {
+          if (ev < a.Ev) {
+            const int64_t off = b * a.o_stride[0] + hq * a.o_stride[1] + s_row[r] * a.o_stride[2] + ev;
+            if (a.out_f32)
+              static_cast<float*>(a.out)[off] = val;
+            else
+              static_cast<__nv_bfloat16*>(a.out)[off] = __float2bfloat16_rn(val);
+          }
+          if (ev == 0 && a.lse) a.lse[row_id] = lse;
+          if (ev == 0 && a.max_scores) a.max_scores[row_id] = top * kLn2;
+        } else {
+          if (ev < a.Ev) ws_o[(row_id * p.splits + split) * a.Ev + ev] = val;
+          if (ev == 0) ws_lse[row_id * p.splits + split] = lse;
+          if (ev == 0) ws_max[row_id * p.splits + split] = top;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tbase, kTmemCols);
+}
+
+// One CTA per query row: merge the splits' (o_s, lse_s, max_s), with
+// lse = ln sum e^(lse_s), o = sum e^(lse_s - lse) o_s.
+__global__ void __launch_bounds__(128) combine_fp8_kernel(const __grid_constant__ FwdArgs a, int splits,
+                                                          const float* ws_o, const float* ws_lse, const float* ws_max) {
+  __shared__ float s_w[kFp8MaxSplits];
+  __shared__ float s_m[4], s_t[4], s_sum[4];
+  const int64_t row_id = blockIdx.x;
+  const int i = static_cast<int>(row_id % a.L), h = static_cast<int>((row_id / a.L) % a.Hq);
+  const int b = static_cast<int>(row_id / (static_cast<int64_t>(a.L) * a.Hq));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float m = -INFINITY, top = -INFINITY;
+  bool nan = false;
+  for (int s = threadIdx.x; s < splits; s += 128) {
+    const float v = ws_lse[row_id * splits + s];
+    s_w[s] = v;
+    nan = nan || v != v;
+    m = fmaxf(m, v);
+    top = fmaxf(top, ws_max[row_id * splits + s]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  }
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_t[warp] = top;
+  }
+  nan = __syncthreads_or(nan);
+  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  top = fmaxf(fmaxf(s_t[0], s_t[1]), fmaxf(s_t[2], s_t[3]));
+  const bool live = a.rows_safe || nan || m != -INFINITY;
+  float sum = 0.0f;
+  for (int s = threadIdx.x; s < splits; s += 128) {
+    const float w = live ? expf(s_w[s] - m) : 0.0f;
+    s_w[s] = w;
+    sum += w;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  sum = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+  const int ev = threadIdx.x;
+  if (ev < a.Ev) {
+    const float* src = ws_o + row_id * splits * a.Ev + ev;
+    float acc = 0.0f;
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) acc = fmaf(s_w[s], src[static_cast<int64_t>(s) * a.Ev], acc);
+    const float val = live ? acc / sum : 0.0f;
+    const int64_t off = b * a.o_stride[0] + h * a.o_stride[1] + i * a.o_stride[2] + ev;
+    if (a.out_f32)
+      static_cast<float*>(a.out)[off] = val;
+    else
+      static_cast<__nv_bfloat16*>(a.out)[off] = __float2bfloat16_rn(val);
+  }
+  if (threadIdx.x == 0 && a.lse) a.lse[row_id] = live ? m + logf(sum) : -INFINITY;
+  if (threadIdx.x == 0 && a.max_scores) a.max_scores[row_id] = top * kLn2;
+}
+
+// Codes times scales as bf16 or fp32, 16 codes a thread, for the slots below
+// the sequence's end; the slots up to a tile past it become 0 (kernels load
+// whole tiles), the rest is not written.
+template <bool kVec>
+__global__ void __launch_bounds__(256) restore_kernel(const __grid_constant__ FwdArgs a, const QuantArgs qa,
+                                                      const __grid_constant__ RestoreArgs k,
+                                                      const __grid_constant__ RestoreArgs v) {
+  const bool is_v = blockIdx.y >= static_cast<unsigned>(a.Hkv);
+  const RestoreArgs& r = is_v ? v : k;
+  const int hk = is_v ? blockIdx.y - a.Hkv : blockIdx.y, b = blockIdx.z;
+  const int S_b = seq_len_b(a.mask, b, a.S);
+  const int end = min(S_b + 128, a.S);
+  const int pieces = (r.D + 15) / 16;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < static_cast<int64_t>(end) * pieces;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int kv = static_cast<int>(i / pieces), e0 = static_cast<int>(i % pieces) * 16;
+    float scale = 0.0f;
+    const uint8_t* src = nullptr;
+    if (kv < S_b) {
+      int outer = b, at = kv;
+      if (a.page_table) {
+        outer = cache_page(a.page_table, a.pages_per_seq, a.page_size, a.num_pages, a.status, b, kv);
+        at = kv % a.page_size;
+      }
+      scale = __ldg(r.scale + (static_cast<int64_t>(outer) * a.Hkv + hk) * qa.scales_per_outer + (at >> qa.block_log));
+      src = r.codes + outer * r.stride[0] + hk * r.stride[1] + at * r.stride[2] + e0;
+    }
+    float x[16];
+    if (kVec && src) {
+      const uint4 c = *reinterpret_cast<const uint4*>(src);
+      const uint32_t u[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+            static_cast<__nv_fp8x2_storage_t>(u[w >> 1] >> (16 * (w & 1))), __NV_E4M3);
+        const float2 f = __half22float2(__half2(h));
+        x[2 * w] = f.x * scale;
+        x[2 * w + 1] = f.y * scale;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        x[e] = 0.0f;
+        if (src && e0 + e < r.D)
+          x[e] = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(src[e]), __NV_E4M3))) * scale;
+      }
+    }
+    const int64_t off = ((static_cast<int64_t>(b) * a.Hkv + hk) * a.S + kv) * r.D + e0;
+    if (kVec) {
+      if (r.f32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(r.out) + off);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) o[w] = make_float4(x[4 * w], x[4 * w + 1], x[4 * w + 2], x[4 * w + 3]);
+      } else {
+        uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(r.out) + off);
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          o[w] = make_uint4(pack_bf16x2(x[8 * w], x[8 * w + 1]), pack_bf16x2(x[8 * w + 2], x[8 * w + 3]),
+                            pack_bf16x2(x[8 * w + 4], x[8 * w + 5]), pack_bf16x2(x[8 * w + 6], x[8 * w + 7]));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (e0 + e < r.D) {
+          if (r.f32)
+            static_cast<float*>(r.out)[off + e] = x[e];
+          else
+            static_cast<__nv_bfloat16*>(r.out)[off + e] = __float2bfloat16_rn(x[e]);
+        }
+    }
+  }
+}
+
+}  // namespace
+
+void plan_decode_fp8(const FwdArgs& a, int split_kv, int num_sms, Fp8Plan* p) {
+  p->row_chunks = a.bm.H > 1 ? a.G * ((a.L + kRows - 1) / kRows) : (a.G * a.L + kRows - 1) / kRows;
+  const int64_t units = static_cast<int64_t>(a.B) * a.Hkv * p->row_chunks;
+  int64_t splits = split_kv;
+  if (split_kv == 0) splits = (5 * num_sms + units - 1) / units;  // about 2.5 rounds of two CTAs an SM
+  splits = splits < 1 ? 1 : (splits > a.bm.Nb ? a.bm.Nb : splits);
+  splits = splits > kFp8MaxSplits ? kFp8MaxSplits : splits;
+  const int per = static_cast<int>((a.bm.Nb + splits - 1) / splits);
+  p->splits = (a.bm.Nb + per - 1) / per;
+  p->workspace_bytes =
+      p->splits > 1 ? static_cast<size_t>(a.B) * a.Hq * a.L * p->splits * (a.Ev + 2) * sizeof(float) : 0;
+}
+
+cudaError_t launch_decode_fp8(const FwdArgs& a, const QuantArgs& qa, const Fp8Plan& p, const CUtensorMap& map_k,
+                              const CUtensorMap& map_v, int box, void* workspace, cudaStream_t stream) {
+  float* ws_o = static_cast<float*>(workspace);
+  const int64_t rows = static_cast<int64_t>(a.B) * a.Hq * a.L;
+  float* ws_lse = ws_o ? ws_o + rows * p.splits * a.Ev : nullptr;
+  float* ws_max = ws_o ? ws_lse + rows * p.splits : nullptr;
+  auto kern = a.score.kind == FA_SCORE_NONE      ? decode_fp8_kernel<FA_SCORE_NONE>
+              : a.score.kind == FA_SCORE_SOFTCAP ? decode_fp8_kernel<FA_SCORE_SOFTCAP>
+              : a.score.kind == FA_SCORE_ALIBI   ? decode_fp8_kernel<FA_SCORE_ALIBI>
+                                                 : decode_fp8_kernel<FA_SCORE_CAP_THEN_BIAS>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3(a.Hkv * p.row_chunks, p.splits, a.B), kThreads, kSmemBytes, stream>>>(a, qa, p, map_k, map_v, box, ws_o,
+                                                                                 ws_lse, ws_max);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.splits == 1) return e;
+  combine_fp8_kernel<<<static_cast<unsigned>(rows), 128, 0, stream>>>(a, p.splits, ws_o, ws_lse, ws_max);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_restore(const FwdArgs& a, const QuantArgs& qa, const RestoreArgs& k, const RestoreArgs& v,
+                           cudaStream_t stream) {
+  const int64_t pieces = static_cast<int64_t>(a.S) * ((k.D > v.D ? k.D : v.D) + 15) / 16;
+  const int64_t blocks = (pieces + 4 * 256 - 1) / (4 * 256);
+  const dim3 grid(static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 2 * a.Hkv, a.B);
+  if (k.vec && v.vec)
+    restore_kernel<true><<<grid, 256, 0, stream>>>(a, qa, k, v);
+  else
+    restore_kernel<false><<<grid, 256, 0, stream>>>(a, qa, k, v);
+  return cudaGetLastError();
+}
+
+}  // namespace fa

@@ -111,4 +111,108 @@ struct TransposeArgs {
 };
 cudaError_t launch_transpose(const TransposeArgs& a, cudaStream_t stream);
 
+// Query / key preparation and cache writes (rows of one head: D <= 128).
+struct NormArgs {
+  int on;             // 0: no norm
+  const void* weight; // [D] or null (1)
+  int weight_f32;
+  float eps;
+};
+struct RopeArgs {
+  int rot;            // 0: no rotation
+  int interleaved;
+  const float* inv_freq;
+  const int* pos;     // [pos_batch, N] or null
+  int pos_batch;
+};
+struct RowsIn {       // (B, H, N, D) rows; p == null: absent
+  const void* p;
+  int f32, H;
+  int64_t stride[3];
+};
+struct RowsOut {
+  void* p;
+  int f32;
+  int64_t stride[3];
+};
+struct PrepArgs {
+  RowsIn x[2];        // q, k
+  RowsOut y[2];
+  NormArgs norm[2];
+  RopeArgs rope;
+  int B, N, D;
+  int vec;            // every row takes 16-byte accesses
+  int tokens, heads;  // per CTA (set by the launcher)
+};
+cudaError_t launch_prep(PrepArgs a, int num_sms, cudaStream_t stream);
+
+struct PrepBwdArgs {
+  RowsIn x[2], dy[2];
+  RowsOut dx[2];
+  float* dw[2];       // fp32 [D] or null
+  NormArgs norm[2];
+  RopeArgs rope;
+  int B, N, D;
+  int vec;
+  int tokens;         // per work item (set by the launcher)
+  float* partial;     // [CTAs][2][D]
+};
+// CTAs of the backward pass at most: its partial weight gradients are summed
+// over them, so the bound fixes the workspace (and the order of the sum) on
+// every device.  Four a B200's SM.
+constexpr int kPrepBwdMaxCtas = 592;
+cudaError_t launch_prep_bwd(PrepBwdArgs a, cudaStream_t stream);
+
+struct AppendArgs {
+  int* status;
+  RowsIn k, v, q;     // q.p == null: no queries
+  RowsOut q_out;
+  NormArgs k_norm, q_norm;
+  RopeArgs rope;
+  int B, N, E, Ev;
+  int k_vec, v_vec, q_vec;  // 16-byte accesses of the inputs (and q_out)
+  // the cache: outer index (page, or sequence of a dense cache), head, slot
+  void *kc, *vc;
+  int64_t kc_stride[3], vc_stride[3];
+  int kc_vec, vc_vec;       // rows of the cache take 8-element accesses
+  int dtype;                // FA_DTYPE_* of the cache
+  float *k_scale, *v_scale;
+  int scale_block, scales_per_outer;  // e4m3
+  const int* page_table;
+  const int *cache_len, *new_len;
+  int page_size, pages_per_seq, num_outer;
+  int chunk, k_heads, q_heads;  // tokens and heads per CTA (set by the launcher)
+};
+cudaError_t launch_append(AppendArgs a, int num_sms, cudaStream_t stream);
+
+// Attention over an e4m3 cache (codes under a scale per block of slots and
+// head; FwdArgs k, v are the codes).
+struct QuantArgs {
+  const float *k_scale, *v_scale;  // [outer, Hkv, scales_per_outer]
+  int block_log;                   // log2 of the slots per scale
+  int scales_per_outer;
+};
+struct Fp8Plan {
+  int row_chunks;   // CTAs that share one KV head's cache: 16 query rows each
+  int splits;       // KV splits per (sequence, KV head, row chunk)
+  size_t workspace_bytes;
+};
+constexpr int kFp8MaxSplits = 1024;
+void plan_decode_fp8(const FwdArgs& a, int split_kv, int num_sms, Fp8Plan* plan);
+// k and v maps: bytes, boxes of 128 x `box` slots.
+cudaError_t launch_decode_fp8(const FwdArgs& a, const QuantArgs& qa, const Fp8Plan& plan, const CUtensorMap& map_k,
+                              const CUtensorMap& map_v, int box, void* workspace, cudaStream_t stream);
+
+// The visible part of an e4m3 cache (dense or paged, FwdArgs) as a dense
+// (B, Hkv, S, D) tensor of bf16 or fp32.
+struct RestoreArgs {
+  const uint8_t* codes;
+  int64_t stride[3];
+  const float* scale;
+  void* out;
+  int D, f32, vec;
+};
+cudaError_t launch_restore(const FwdArgs& a, const QuantArgs& qa, const RestoreArgs& k, const RestoreArgs& v,
+                           cudaStream_t stream);
+
 }  // namespace fa
