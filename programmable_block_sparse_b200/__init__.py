@@ -35,6 +35,7 @@ from __future__ import annotations
 import ctypes as C
 import math
 import os
+import struct
 from dataclasses import dataclass
 
 from . import _abi
@@ -456,7 +457,14 @@ def flexattn_backward(q, k, v, out, dout, lse, block_mask, q_side=None, score_mo
 # ---------------------------------------------------------------------------
 # Query / key preparation, cache writes and attention over an e4m3 cache
 # ---------------------------------------------------------------------------
+# These calls are made once a layer and token, so their structs are packed in
+# one go (a ctypes constructor takes three times as long).
 _DTYPES = {}
+_PACK_TENSOR = struct.Struct("Qii4q4q").pack
+_PACK_NORM = struct.Struct("Qif").pack
+_PACK_ROPE = struct.Struct("QQiiii").pack
+_PACK_QUANT = struct.Struct("QQii").pack
+_byref = C.byref
 
 
 def _dtype_codes():
@@ -467,16 +475,17 @@ def _dtype_codes():
     return _DTYPES
 
 
-def _device_tensor(t, name, device=None):
-    """``t`` as an fa_tensor, on ``device`` when given."""
+def _device_tensor(t, name, device):
+    """``t`` as an fa_tensor; it has to be 4-D and on ``device``, a CUDA device."""
     code = _dtype_codes().get(t.dtype)
     if code is None:
         raise FlexAttnError(6, f"{name}: unsupported dtype {t.dtype}")
-    if t.dim() != 4:
-        raise FlexAttnError(2, f"{name}: expected a 4-D tensor, got shape {tuple(t.shape)}")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise FlexAttnError(9, f"{name} is on {t.device}, expected {device or 'a CUDA device'}")
-    return _abi.fa_tensor(t.data_ptr(), code, 0, tuple(t.shape), t.stride())
+    shape = t.shape
+    if len(shape) != 4:
+        raise FlexAttnError(2, f"{name}: expected a 4-D tensor, got shape {tuple(shape)}")
+    if t.device != device or not t.is_cuda:
+        raise FlexAttnError(9, f"{name} is on {t.device}, expected {device if device.type == 'cuda' else 'a CUDA device'}")
+    return _abi.fa_tensor.from_buffer_copy(_PACK_TENSOR(t.data_ptr(), code, 0, *shape, *t.stride()))
 
 
 def _device_array(t, name, dtype, shape, device):
@@ -484,7 +493,7 @@ def _device_array(t, name, dtype, shape, device):
     (the library reads it without knowing its extent)."""
     if t.dtype != dtype:
         raise FlexAttnError(6, f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise FlexAttnError(2, f"{name}: expected shape {shape}, got {tuple(t.shape)}")
     if t.device != device:
         raise FlexAttnError(9, f"{name} is on {t.device}, expected {device}")
@@ -496,53 +505,60 @@ def _device_array(t, name, dtype, shape, device):
 def _norm_struct(spec, name, D, device):
     if spec is None:
         return None
-    n = _abi.fa_head_norm(None, _abi.FA_DTYPE_F32, float(spec.get("eps", 1e-6)))
     w = spec.get("weight")
-    if w is not None:
-        code = _dtype_codes().get(w.dtype, -1)
-        n.weight = _device_array(w, f"{name} weight", w.dtype, (D,), device)
-        n.weight_dtype = code
-    return n
+    if w is None:
+        return _abi.fa_head_norm(None, _abi.FA_DTYPE_F32, float(spec.get("eps", 1e-6)))
+    return _abi.fa_head_norm.from_buffer_copy(_PACK_NORM(
+        _device_array(w, name, w.dtype, (D,), device), _dtype_codes().get(w.dtype, -1), spec.get("eps", 1e-6)))
 
 
 def _rope_struct(spec, B, N, device):
-    import torch
     if spec is None:
         return None
+    import torch
     f = spec["inv_freq"]
-    r = _abi.fa_rope(_device_array(f, "inv_freq", torch.float32, (f.numel(),), device), None, 2 * f.numel(),
-                     1 if spec.get("interleaved") else 0, 0, 0)
+    half = f.numel()
+    ptr = rows = 0
     pos = spec.get("pos")
     if pos is not None:
         rows = pos.shape[0] if pos.dim() == 2 else 1
-        if rows not in (1, B):
+        if rows != 1 and rows != B:
             raise FlexAttnError(4, f"rope pos: {rows} rows, expected 1 or {B}")
-        r.pos = _device_array(pos, "rope pos", torch.int32, (rows, N) if pos.dim() == 2 else (N,), device)
-        r.pos_batch = rows
-    return r
+        ptr = _device_array(pos, "rope pos", torch.int32, (rows, N) if pos.dim() == 2 else (N,), device)
+    return _abi.fa_rope.from_buffer_copy(_PACK_ROPE(
+        _device_array(f, "inv_freq", torch.float32, (half,), device), ptr, 2 * half,
+        1 if spec.get("interleaved") else 0, rows, 0))
 
 
 def _ref(s):
-    return None if s is None else C.byref(s)
+    return None if s is None else _byref(s)
+
+
+def _empty_like(t, dtype=None):
+    """A new contiguous tensor of t's shape on its device."""
+    import torch
+    return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
 
 
 def _call(device, stream, fn, *args):
     """``fn(*args, stream)`` with ``device`` current; ``stream`` None is that device's current stream."""
     import torch
-    if torch.cuda.current_device() == device.index:
-        handle = _stream_handle(stream)
-        _check(fn(*args, handle))
-        return
-    with torch.cuda.device(device):
-        handle = _stream_handle(stream)
-        _check(fn(*args, handle))
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call(device, stream, fn, *args)
+    if stream is None:
+        handle = torch.cuda.current_stream().cuda_stream
+    else:
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+    status = fn(*args, handle)
+    if status:
+        _check(status)
 
 
 def flexattn_qk_norm_rope(q, k, q_norm=None, k_norm=None, rope=None, q_out=None, k_out=None, stream=None):
     """Norm (per head) and rotation of queries (B, Hq, N, D) and keys
     (B, Hkv, N, D) in one pass; returns ``(q_out, k_out)``.  Either of q, k
     may be None; the outputs may be preallocated, or the inputs themselves."""
-    import torch
     x = q if q is not None else k
     if x is None:
         raise FlexAttnError(1, "q and k are both None")
@@ -551,12 +567,12 @@ def flexattn_qk_norm_rope(q, k, q_norm=None, k_norm=None, rope=None, q_out=None,
     if q is not None:
         qs = _device_tensor(q, "q", dev)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = _empty_like(q)
         qo = _device_tensor(q_out, "q_out", dev)
     if k is not None:
         ks = _device_tensor(k, "k", dev)
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+            k_out = _empty_like(k)
         ko = _device_tensor(k_out, "k_out", dev)
     B, _, N, D = x.shape
     qn, kn = _norm_struct(q_norm, "q_norm", D, dev), _norm_struct(k_norm, "k_norm", D, dev)
@@ -585,7 +601,7 @@ def flexattn_qk_norm_rope_backward(q, k, dq_out, dk_out, q_norm=None, k_norm=Non
         if dy is None:
             return xs, None, None, None, None
         if dx is None:
-            dx = torch.empty(dy.shape, dtype=grad_dtype or dy.dtype, device=dev)
+            dx = _empty_like(dy, grad_dtype)
         dw = torch.empty(D, dtype=torch.float32, device=dev) if norm is not None and weight_grads else None
         return xs, _device_tensor(dy, f"d{name}_out", dev), _device_tensor(dx, f"d{name}", dev), dx, dw
 
@@ -637,7 +653,7 @@ def flexattn_cache_append(k, v, cache, k_norm=None, rope=None, q=None, q_norm=No
     if q is not None:
         qs = _device_tensor(q, "q", dev)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = _empty_like(q)
         qo = _device_tensor(q_out, "q_out", dev)
     kn = _norm_struct(k_norm, "k_norm", E, dev)
     qn = _norm_struct(q_norm, "q_norm", E, dev)
@@ -650,9 +666,9 @@ def flexattn_cache_append(k, v, cache, k_norm=None, rope=None, q=None, q_norm=No
 def _quant_struct(quant, k, v, device):
     import torch
     n = int(quant["scale_block"])
-    return _abi.fa_kv_quant(
+    return _abi.fa_kv_quant.from_buffer_copy(_PACK_QUANT(
         _device_array(quant["k_scale"], "k_scale", torch.float32, _scale_shape(k, n), device),
-        _device_array(quant["v_scale"], "v_scale", torch.float32, _scale_shape(v, n), device), n, 0)
+        _device_array(quant["v_scale"], "v_scale", torch.float32, _scale_shape(v, n), device), n, 0))
 
 
 def _paged_checked(paged, B, device):
@@ -664,7 +680,7 @@ def _paged_checked(paged, B, device):
 
 
 def flexattn_forward_fp8_workspace_size(q, k, v, block_mask, quant, split_kv=0, paged=None):
-    """Workspace bytes of :func:`flexattn_forward_fp8` for these arguments."""
+    """Workspace bytes of :func:`flexattn_forward_fp8` for these arguments (0: none)."""
     dev = q.device
     qs, ks, vs = _device_tensor(q, "q", dev), _device_tensor(k, "k", dev), _device_tensor(v, "v", dev)
     qt, bm = _quant_struct(quant, k, v, dev), block_mask.as_struct()

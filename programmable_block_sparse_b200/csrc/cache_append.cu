@@ -16,7 +16,9 @@
 namespace fa {
 namespace {
 
-constexpr int kAppThreads = 256;
+// A CTA has 16 groups of 16 lanes, 32 of 8, or 32 warps for rows read one
+// element at a time.
+constexpr int threads_of(int T) { return T == 32 ? 1024 : 256; }
 constexpr int kMaxChunk = 128;
 
 // 2^ceil(log2(amax / 448)) from the bits of a finite amax >= 0; 0 for 0.
@@ -29,13 +31,11 @@ __device__ __forceinline__ float pow2_scale(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// 8 floats as e4m3 codes (round to nearest even, +-448 at most, NaN kept).
-__device__ __forceinline__ uint2 e4m3x8(const float (&x)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+// Four floats as e4m3 codes (round to nearest even, +-448 at most, NaN kept).
+__device__ __forceinline__ uint32_t e4m3x4(float2 x, float2 y) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
 }
 __device__ __forceinline__ float e4m3_value(uint32_t code) {
   const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code & 0xffu), __NV_E4M3);
@@ -65,14 +65,69 @@ __device__ __forceinline__ Span append_span(const AppendArgs& a, int b) {
   return s;
 }
 
-template <int T, Pair kPair, bool kVec, int kIters>
-__global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int kGroups = kAppThreads / T;
-  extern __shared__ float tables[];  // cosines, then sines, of the chunk's tokens
+// The new rows of a group (n0, n0 + groups, ... below count) of one head; 0 elsewhere.
+template <int T, bool kVec, bool kF32, int kIters>
+__device__ __forceinline__ void load_rows(const RowsIn& in, int64_t off, int n0, int count, const Place& p,
+                                          Row (&x)[kIters]) {
+  Raw<kVec, kF32> raw[kIters];
+#pragma unroll
+  for (int it = 0; it < kIters; ++it) {
+    const int n = n0 + it * (threads_of(T) / T);
+    if (n >= 0 && n < count)
+      load_raw(row_ptr(in.p, kF32, off + n * in.stride[2]), p, raw[it]);
+    else
+      clear_raw(raw[it]);
+  }
+#pragma unroll
+  for (int it = 0; it < kIters; ++it) x[it] = unpack(raw[it]);
+}
+
+// Queries of ntok tokens from n0 on and nh heads from hq0 on.
+template <int T, bool kNext, bool kVec, bool kF32>
+__device__ __forceinline__ void append_queries(const AppendArgs& a, int b, int n0, int ntok, int hq0, int nh,
+                                               const float* cos_t, const float* sin_t) {
+  constexpr int kGroups = threads_of(T) / T;
+  constexpr int U = 2;
+  const int t = threadIdx.x % T, grp = threadIdx.x / T, rot = a.rope.rot;
+  const Place p = place_of<kNext>(t, rot, a.E);
+  const int rows = ntok * nh;
+  Row w;
+  if (a.q_norm.on) w = load_weight(a.q_norm, p);
+  for (int r0 = 0; r0 < rows; r0 += U * kGroups) {
+    Raw<kVec, kF32> raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = min(r0 + u * kGroups + grp, rows - 1), n = n0 + r % ntok, h = hq0 + r / ntok;
+      load_raw(row_ptr(a.q.p, kF32, b * a.q.stride[0] + h * a.q.stride[1] + n * a.q.stride[2]), p, raw[u]);
+    }
+    if (r0 == 0 && rot) __syncthreads();  // the angles: the first loads go ahead of them
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (r0 + u * kGroups >= rows) break;  // the same for the whole CTA
+      const int r = min(r0 + u * kGroups + grp, rows - 1), tk = r % ntok, n = n0 + tk, h = hq0 + r / ntok;
+      Row x = unpack(raw[u]);
+      if (a.q_norm.on)
+        x = product(scaled(x, norm_factor<T>(x, a.q_norm.eps, 1.0f / static_cast<float>(a.E))), w);
+      if (rot)
+        x = apply<kNext>(x, rotation<kNext>(cos_t + tk * (rot >> 1), sin_t + tk * (rot >> 1), t, p, rot, 1.0f), p, rot,
+                         a.E);
+      if (r0 + u * kGroups + grp < rows)
+        store_row<kVec>(row_ptr(a.q_out.p, a.q_out.f32,
+                                b * a.q_out.stride[0] + h * a.q_out.stride[1] + n * a.q_out.stride[2]),
+                        a.q_out.f32, p, x);
+    }
+  }
+}
+
+// kVec: of the inputs; kCVec: rows of the cache take whole pieces.
+template <int T, bool kNext, bool kVec, int kIters>
+__global__ void __launch_bounds__(threads_of(T)) append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int kThreads = threads_of(T), kGroups = kThreads / T;
+  extern __shared__ __align__(16) float tables[];  // cosines, then sines, of the chunk's tokens
   __shared__ int s_outer[kMaxChunk];
   __shared__ uint32_t s_amax[32];
   __shared__ float s_scale[32], s_old[32];
-  const int b = blockIdx.z, t = threadIdx.x % T, grp = threadIdx.x / T, e0 = 8 * t;
+  const int b = blockIdx.z, t = threadIdx.x % T, grp = threadIdx.x / T;
   const int rot = a.rope.rot, h2 = rot >> 1;
   float* cos_t = tables;
   float* sin_t = tables + a.chunk * h2;
@@ -82,8 +137,14 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_consta
   const int* pos_row =
       a.rope.pos ? a.rope.pos + static_cast<int64_t>(a.rope.pos_batch > 1 ? b : 0) * a.N : nullptr;
   const int pos0 = __ldg(a.cache_len + b);
-  auto position = [&](int n) {
-    return pos_row ? __ldg(pos_row + n) : static_cast<int>(static_cast<uint32_t>(pos0) + static_cast<uint32_t>(n));
+  // angles of `count` tokens from n0 on into the tables from row `to` on
+  auto fill = [&](int n0, int count, int to) {
+    for (int i = threadIdx.x; i < count * h2; i += kThreads) {
+      const int n = n0 + i / h2;
+      const int pos =
+          pos_row ? __ldg(pos_row + n) : static_cast<int>(static_cast<uint32_t>(pos0) + static_cast<uint32_t>(n));
+      angle(pos, __ldg(a.rope.inv_freq + i % h2), cos_t + to * h2 + i, sin_t + to * h2 + i);
+    }
   };
 
   if (static_cast<int>(blockIdx.y) >= 2 * kv_runs) {
@@ -91,35 +152,11 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_consta
     const int n0 = blockIdx.x * a.chunk, ntok = min(a.chunk, a.N - n0);
     if (ntok <= 0) return;
     const int hq0 = (blockIdx.y - 2 * kv_runs) * a.q_heads, nh = min(a.q_heads, a.q.H - hq0);
-    if (rot) {
-      for (int i = threadIdx.x; i < ntok * h2; i += kAppThreads)
-        angle(position(n0 + i / h2), __ldg(a.rope.inv_freq + i % h2), cos_t + i, sin_t + i);
-      __syncthreads();
-    }
-    float w[8];
-    if (a.q_norm.on) load_weight8(a.q_norm, e0, a.E, w);
-    const int rows = ntok * nh;
-    for (int r0 = 0; r0 < rows; r0 += kGroups) {
-      const int r = r0 + grp;
-      const bool ok = r < rows;
-      const int tk = ok ? r % ntok : 0, h = hq0 + (ok ? r / ntok : 0), n = n0 + tk;
-      float x[8], y[8];
-      load8<kVec>(row_ptr(a.q.p, a.q.f32, b * a.q.stride[0] + h * a.q.stride[1] + n * a.q.stride[2]), a.q.f32, e0, a.E,
-                  x);
-      if (a.q_norm.on) norm8<T>(x, w, a.q_norm.eps, 1.0f / static_cast<float>(a.E));
-      if (rot) {
-        float c[8], s[8];
-        lane_angles<kPair>(cos_t + tk * h2, sin_t + tk * h2, e0, rot, c, s);
-        rotate8<T, kPair>(x, c, s, 1.0f, t, rot, y);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[i];
-      }
-      if (ok)
-        store8<kVec>(row_ptr(a.q_out.p, a.q_out.f32,
-                             b * a.q_out.stride[0] + h * a.q_out.stride[1] + n * a.q_out.stride[2]),
-                     a.q_out.f32, e0, a.E, y);
-    }
+    if (rot) fill(n0, ntok, 0);
+    if (a.q.f32)
+      append_queries<T, kNext, kVec, true>(a, b, n0, ntok, hq0, nh, cos_t, sin_t);
+    else
+      append_queries<T, kNext, kVec, false>(a, b, n0, ntok, hq0, nh, cos_t, sin_t);
     return;
   }
 
@@ -132,8 +169,9 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_consta
   const int D = is_k ? a.E : a.Ev;
   const RowsIn& in = is_k ? a.k : a.v;
   const bool turn = is_k && rot, norm = is_k && a.k_norm.on;
+  const Place p = place_of<kNext>(t, is_k ? rot : 0, D);
   // page (or sequence) of each slot of the chunk that the call touches; -1: none
-  for (int i = threadIdx.x; i < a.chunk; i += kAppThreads) {
+  for (int i = threadIdx.x; i < a.chunk; i += kThreads) {
     const int slot = slot0 + i;
     int outer = -1;
     if (slot < end) {
@@ -151,55 +189,42 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_consta
     s_outer[i] = outer;
   }
   if (turn) {
-    for (int i = threadIdx.x; i < a.chunk * h2; i += kAppThreads) {
-      const int n = slot0 + i / h2 - sp.start;
-      if (n >= 0 && n < sp.count) angle(position(n), __ldg(a.rope.inv_freq + i % h2), cos_t + i, sin_t + i);
-    }
+    const int from = max(slot0, sp.start);
+    fill(from - sp.start, min(end, slot0 + a.chunk) - from, from - slot0);
   }
-  float w[8];
-  if (norm) load_weight8(a.k_norm, e0, D, w);
+  Row w;
+  if (norm) w = load_weight(a.k_norm, p);
   const int e4m3 = a.dtype == FA_DTYPE_E4M3;
   const int sb_log = e4m3 ? __ffs(a.scale_block) - 1 : 5;
   float* scales = is_k ? a.k_scale : a.v_scale;
   char* cache = static_cast<char*>(is_k ? a.kc : a.vc);
   const int64_t* cs = is_k ? a.kc_stride : a.vc_stride;
   const bool cvec = is_k ? a.kc_vec : a.vc_vec;
-  __syncthreads();
 
   for (int h = run * a.k_heads; h < min((run + 1) * a.k_heads, in.H); ++h) {
-    if (e4m3) {
-      if (threadIdx.x < 32) s_amax[threadIdx.x] = 0u;
-      __syncthreads();
-    }
-    float x[kIters][8];
-#pragma unroll
-    for (int it = 0; it < kIters; ++it) {
-      const int n = slot0 + it * kGroups + grp - sp.start;
-      if (n >= 0 && n < sp.count) {
-        load8<kVec>(row_ptr(in.p, in.f32, b * in.stride[0] + h * in.stride[1] + n * in.stride[2]), in.f32, e0, D,
-                    x[it]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[it][i] = 0.0f;
-      }
-    }
+    Row x[kIters];
+    const int64_t head_off = b * in.stride[0] + h * in.stride[1];
+    if (in.f32)
+      load_rows<T, kVec, true, kIters>(in, head_off, slot0 - sp.start + grp, sp.count, p, x);
+    else
+      load_rows<T, kVec, false, kIters>(in, head_off, slot0 - sp.start + grp, sp.count, p, x);
+    if (threadIdx.x < 32) s_amax[threadIdx.x] = 0u;
+    __syncthreads();  // also: the previous head's scales have been read, and the tables are filled
 #pragma unroll
     for (int it = 0; it < kIters; ++it) {
       const int row = it * kGroups + grp;
-      if (norm) norm8<T>(x[it], w, a.k_norm.eps, 1.0f / static_cast<float>(D));
-      if (turn) {
-        float c[8], s[8], y[8];
-        lane_angles<kPair>(cos_t + row * h2, sin_t + row * h2, e0, rot, c, s);
-        rotate8<T, kPair>(x[it], c, s, 1.0f, t, rot, y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[it][i] = y[i];
-      }
+      if (norm) x[it] = product(scaled(x[it], norm_factor<T>(x[it], a.k_norm.eps, 1.0f / static_cast<float>(D))), w);
+      if (turn)
+        x[it] = apply<kNext>(x[it], rotation<kNext>(cos_t + row * h2, sin_t + row * h2, t, p, rot, 1.0f), p, rot, D);
       if (e4m3) {
         float m = 0.0f;  // of this row's finite magnitudes (rows without a new token: 0)
         const int n = slot0 + row - sp.start;
         if (n >= 0 && n < sp.count) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[it][i]) < INFINITY ? fabsf(x[it][i]) : 0.0f);
+          for (int i = 0; i < 4; ++i) {
+            const float u = fabsf(x[it].v[i].x), v = fabsf(x[it].v[i].y);
+            m = fmaxf(m, fmaxf(u < INFINITY ? u : 0.0f, v < INFINITY ? v : 0.0f));
+          }
         }
 #pragma unroll
         for (int o = T / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -230,73 +255,72 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_consta
 #pragma unroll
     for (int it = 0; it < kIters; ++it) {
       const int row = it * kGroups + grp, slot = slot0 + row, outer = s_outer[row];
-      if (outer < 0 || e0 >= D) continue;
+      if (outer < 0) continue;
       const int64_t off = outer * cs[0] + h * cs[1] + static_cast<int64_t>(slot % a.page_size) * cs[2];
       if (!e4m3) {
         if (slot < sp.start) continue;
         const int f32 = a.dtype == FA_DTYPE_F32;
-        if (cvec)
-          store8<true>(row_ptr(static_cast<void*>(cache), f32, off), f32, e0, D, x[it]);
+        if (kVec && cvec)
+          store_row<true>(row_ptr(static_cast<void*>(cache), f32, off), f32, p, x[it]);
         else
-          store8<false>(row_ptr(static_cast<void*>(cache), f32, off), f32, e0, D, x[it]);
+          store_row<false>(row_ptr(static_cast<void*>(cache), f32, off), f32, p, x[it]);
         continue;
       }
       const float now = s_scale[row >> sb_log], inv = now > 0.0f ? 1.0f / now : 0.0f;
-      uint8_t* dst = reinterpret_cast<uint8_t*>(cache) + off + e0;
-      float y[8];
+      uint8_t* dst = reinterpret_cast<uint8_t*>(cache) + off;
+      Row y;
       if (slot >= sp.start) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[it][i] * inv;
+        y = scaled(x[it], inv);
       } else {
         // an older token of a block: rounded again where its scale grew
         const float old = s_old[row >> sb_log];
         if (!(now > old)) continue;
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = e0 + i < D ? e4m3_value(dst[i]) * (old * inv) : 0.0f;
+        for (int i = 0; i < 8; ++i)
+          v[i] = (i & 3) < (i < 4 ? p.na : p.nb) ? e4m3_value(dst[i < 4 ? p.a + i : p.b + i - 4]) * (old * inv) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y.v[i] = make_float2(v[2 * i], v[2 * i + 1]);
       }
-      const uint2 code = e4m3x8(y);
-      if (cvec) {
-        *reinterpret_cast<uint2*>(dst) = code;
+      const uint32_t ca = e4m3x4(y.v[0], y.v[1]), cb = e4m3x4(y.v[2], y.v[3]);
+      if (kVec && cvec) {
+        if (p.na) {
+          *reinterpret_cast<uint32_t*>(dst + p.a) = ca;
+          *reinterpret_cast<uint32_t*>(dst + p.b) = cb;
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (e0 + i < D) dst[i] = static_cast<uint8_t>((i < 4 ? code.x : code.y) >> (8 * (i & 3)));
+          if ((i & 3) < (i < 4 ? p.na : p.nb))
+            dst[i < 4 ? p.a + i : p.b + i - 4] = static_cast<uint8_t>((i < 4 ? ca : cb) >> (8 * (i & 3)));
       }
     }
-    // the next head's maxima are cleared only after this head's scales were read
-    if (e4m3) __syncthreads();
+    __syncthreads();  // the scales are read before the next head's maxima are cleared
   }
 }
 
-template <int T, Pair kPair, bool kVec>
-cudaError_t launch_append_i(const AppendArgs& a, dim3 grid, size_t smem, cudaStream_t st) {
-  constexpr int kUnit = T / 8;  // turns of the CTA's groups over 32 slots
-  auto kern = a.chunk == 32   ? append_kernel<T, kPair, kVec, kUnit>
-              : a.chunk == 64 ? append_kernel<T, kPair, kVec, 2 * kUnit>
-                              : append_kernel<T, kPair, kVec, 4 * kUnit>;
+// The kernel for a row layout and a chunk.
+template <int T, bool kNext, bool kVec>
+cudaError_t launch_append_t(const AppendArgs& a, dim3 grid, size_t smem, cudaStream_t st) {
+  constexpr int kUnit = T == 16 ? 2 : 1;  // turns of the CTA's groups over 32 slots
+  auto kern = a.chunk == 32   ? append_kernel<T, kNext, kVec, kUnit>
+              : a.chunk == 64 ? append_kernel<T, kNext, kVec, 2 * kUnit>
+                              : append_kernel<T, kNext, kVec, 4 * kUnit>;
   if (smem > 40 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  kern<<<grid, kAppThreads, smem, st>>>(a);
+  kern<<<grid, threads_of(T), smem, st>>>(a);
   return cudaGetLastError();
-}
-
-template <int T>
-cudaError_t launch_append_t(const AppendArgs& a, bool vec, dim3 grid, size_t smem, cudaStream_t st) {
-  if (a.rope.rot == 0 || a.rope.interleaved)
-    return vec ? launch_append_i<T, Pair::kNext, true>(a, grid, smem, st)
-               : launch_append_i<T, Pair::kNext, false>(a, grid, smem, st);
-  if (!vec) return launch_append_i<T, Pair::kHalfAny, false>(a, grid, smem, st);
-  return (a.rope.rot / 2) % 8 == 0 ? launch_append_i<T, Pair::kHalf, true>(a, grid, smem, st)
-                                   : launch_append_i<T, Pair::kHalfAny, true>(a, grid, smem, st);
 }
 
 }  // namespace
 
 cudaError_t launch_append(AppendArgs a, int num_sms, cudaStream_t st) {
-  const bool small = a.E <= 64 && a.Ev <= 64;
-  const int groups = kAppThreads / (small ? 8 : 16);
+  const bool next = a.rope.rot == 0 || a.rope.interleaved;
+  const bool vec = a.k_vec && a.v_vec && (!a.q.p || a.q_vec) && (next || a.rope.rot % 8 == 0);
+  const int lanes = !vec ? 32 : (a.E <= 64 && a.Ev <= 64 ? 8 : 16);
+  const int groups = threads_of(lanes) / lanes;
   a.chunk = a.dtype == FA_DTYPE_E4M3 && a.scale_block > 32 ? a.scale_block : 32;
   // N tokens that start anywhere in a chunk touch this many chunks at most
   const int chunks = static_cast<int>((static_cast<int64_t>(a.N) + a.chunk - 2) / a.chunk) + 1;
@@ -311,8 +335,11 @@ cudaError_t launch_append(AppendArgs a, int num_sms, cudaStream_t st) {
   const int q_runs = a.q.p ? (a.q.H + a.q_heads - 1) / a.q_heads : 0;
   const dim3 grid(chunks, 2 * kv_runs + q_runs, a.B);
   const size_t smem = static_cast<size_t>(a.chunk) * (a.rope.rot / 2) * 2 * sizeof(float);
-  const bool vec = a.k_vec && a.v_vec && (!a.q.p || a.q_vec);
-  return small ? launch_append_t<8>(a, vec, grid, smem, st) : launch_append_t<16>(a, vec, grid, smem, st);
+  if (lanes == 32)
+    return next ? launch_append_t<32, true, false>(a, grid, smem, st) : launch_append_t<32, false, false>(a, grid, smem, st);
+  if (lanes == 8)
+    return next ? launch_append_t<8, true, true>(a, grid, smem, st) : launch_append_t<8, false, true>(a, grid, smem, st);
+  return next ? launch_append_t<16, true, true>(a, grid, smem, st) : launch_append_t<16, false, true>(a, grid, smem, st);
 }
 
 }  // namespace fa

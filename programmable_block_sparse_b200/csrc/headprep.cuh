@@ -1,12 +1,18 @@
 // One head's row in registers: norm, rotation and their gradients.
 //
-// A row of D <= 8 T elements belongs to T neighbouring lanes of a warp (T = 8
-// for D <= 64, 16 for D <= 128); lane t holds elements 8 t .. 8 t + 7, one
-// 16-byte access in bf16.  The rotation is written as
-//   y_i = x_i c_i + p_i s_i,
-// p_i the element paired with i and the sign of the sine folded into s_i, so
-// that both pairings, their inverses (s -> -s) and pass-through elements
-// (c = 1, s = 0) are one formula; only the fetch of p differs.
+// A row belongs to T neighbouring lanes of a warp, and a lane holds two pieces
+// of four elements, a and b, chosen so that no rotated pair crosses lanes:
+//   pairs (i, i + h), h = rot / 2: lane t < ceil(h / 4) holds a = 4 t .. and
+//       b = h + 4 t .., the two halves of four pairs; the lanes after them
+//       hold 8 elements past rot each;
+//   pairs (2 i, 2 i + 1): lane t holds 8 t .. 8 t + 7.
+// Either way lane t turns by the angles 4 t .. 4 t + 3.  With 8 | D, 8 | rot
+// and aligned rows (kVec) a piece is one access of 8 bytes in bf16 and 16 in
+// fp32, and T is 8 for D <= 64 and 16 for D <= 128; other rows are read one
+// element at a time by a whole warp (T = 32).
+// Shuffles are left to the norm's sum.  (With 8 neighbouring elements a lane
+// and the partner fetched by shuffles, a row took 2.5 times the instructions:
+// 255 us against 165 us for 32 + 8 heads of 128 over 32768 tokens.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -14,73 +20,116 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "fastmath.cuh"
 #include "launch.h"
 
 namespace fa {
 
-// How the paired element is fetched.
-enum class Pair {
-  kHalf,     // (i, i + h) with h = rot / 2 a multiple of 8: whole lanes trade
-  kHalfAny,  // (i, i + h) with any h: lanes and places differ
-  kNext      // (2 i, 2 i + 1): within the lane
+// Where a lane's pieces lie.
+struct Place {
+  int a, b;    // first elements
+  int na, nb;  // elements held, 0..4 (0 or 4 with 16-byte rows)
+  int pairs;   // kHalf: pairs that turn; 0: both pieces pass through
 };
+template <bool kNext>
+__device__ __forceinline__ Place place_of(int t, int rot, int D) {
+  Place p;
+  const int h = rot >> 1, turning = (h + 3) >> 2;
+  if (kNext || t >= turning) {
+    const int first = kNext ? 8 * t : rot + 8 * (t - turning);
+    p.a = first;
+    p.b = first + 4;
+    p.na = min(max(D - p.a, 0), 4);
+    p.nb = min(max(D - p.b, 0), 4);
+    p.pairs = 0;
+  } else {
+    p.a = 4 * t;
+    p.b = h + 4 * t;
+    p.na = p.nb = p.pairs = min(h - 4 * t, 4);
+  }
+  return p;
+}
 
-// 8 elements of a row at element e0 (kVec: 16-byte accesses, 8 | D; else one
-// element at a time).  Elements past D are 0 and not stored.
-template <bool kVec>
-__device__ __forceinline__ void load8(const void* row, int f32, int e0, int D, float (&x)[8]) {
-  if constexpr (kVec) {
-    if (e0 < D) {
-      if (f32) {
-        const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + e0);
-        const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + e0 + 4);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-      } else {
-        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(row) + e0);
-        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+// Two pieces as loaded.  Loading and unpacking are apart so that a lane can
+// have the loads of several rows in flight.
+template <bool kVec, bool kF32>
+struct Raw {
+  uint32_t u[(kVec && !kF32) ? 4 : 8];
+};
+template <bool kVec, bool kF32>
+__device__ __forceinline__ void clear_raw(Raw<kVec, kF32>& r) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[2 * i] = __uint_as_float(u[i] << 16);
-          x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-        }
-      }
-    } else {
+  for (int i = 0; i < static_cast<int>(sizeof(r.u) / 4); ++i) r.u[i] = 0u;
+}
+template <bool kVec, bool kF32>
+__device__ __forceinline__ void load_raw(const void* row, const Place& p, Raw<kVec, kF32>& r) {
+  clear_raw(r);
+  if constexpr (!kVec) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+    for (int i = 0; i < 8; ++i) {
+      const int e = i < 4 ? p.a + i : p.b + i - 4;
+      if ((i & 3) < (i < 4 ? p.na : p.nb))
+        r.u[i] = kF32 ? __float_as_uint(static_cast<const float*>(row)[e])
+                      : static_cast<uint32_t>(static_cast<const uint16_t*>(row)[e]) << 16;
+    }
+  } else if constexpr (kF32) {
+    if (p.na) {
+      const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const float*>(row) + p.a);
+      const uint4 b = *reinterpret_cast<const uint4*>(static_cast<const float*>(row) + p.b);
+      r.u[0] = a.x; r.u[1] = a.y; r.u[2] = a.z; r.u[3] = a.w;
+      r.u[4] = b.x; r.u[5] = b.y; r.u[6] = b.z; r.u[7] = b.w;
     }
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[i] = e0 + i >= D ? 0.0f
-             : f32       ? static_cast<const float*>(row)[e0 + i]
-                         : __bfloat162float(static_cast<const __nv_bfloat16*>(row)[e0 + i]);
+    if (p.na) {
+      const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(row) + p.a);
+      const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(row) + p.b);
+      r.u[0] = a.x; r.u[1] = a.y; r.u[2] = b.x; r.u[3] = b.y;
+    }
   }
 }
 
+// The pieces as pairs of fp32: a = v[0], v[1], b = v[2], v[3].
+struct Row {
+  float2 v[4];
+};
+template <bool kVec, bool kF32>
+__device__ __forceinline__ Row unpack(const Raw<kVec, kF32>& r) {
+  Row x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kVec && !kF32)
+      x.v[i] = make_float2(__uint_as_float(r.u[i] << 16), __uint_as_float(r.u[i] & 0xffff0000u));
+    else
+      x.v[i] = make_float2(__uint_as_float(r.u[2 * i]), __uint_as_float(r.u[2 * i + 1]));
+  }
+  return x;
+}
+
 template <bool kVec>
-__device__ __forceinline__ void store8(void* row, int f32, int e0, int D, const float (&x)[8]) {
+__device__ __forceinline__ void store_row(void* row, int f32, const Place& p, const Row& x) {
   if constexpr (kVec) {
-    if (e0 < D) {
-      if (f32) {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(row) + e0);
-        o[0] = make_float4(x[0], x[1], x[2], x[3]);
-        o[1] = make_float4(x[4], x[5], x[6], x[7]);
-      } else {
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(row) + e0) =
-            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                       pack_bf16x2(x[6], x[7]));
-      }
+    if (p.na == 0) return;
+    if (f32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(row) + p.a) = make_float4(x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y);
+      *reinterpret_cast<float4*>(static_cast<float*>(row) + p.b) = make_float4(x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y);
+    } else {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(row) + p.a) =
+          make_uint2(pack_bf16x2(x.v[0].x, x.v[0].y), pack_bf16x2(x.v[1].x, x.v[1].y));
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(row) + p.b) =
+          make_uint2(pack_bf16x2(x.v[2].x, x.v[2].y), pack_bf16x2(x.v[3].x, x.v[3].y));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (e0 + i < D) {
+    for (int i = 0; i < 8; ++i) {
+      const int e = i < 4 ? p.a + i : p.b + i - 4;
+      const float v = (i & 1) ? x.v[i >> 1].y : x.v[i >> 1].x;
+      if ((i & 3) < (i < 4 ? p.na : p.nb)) {
         if (f32)
-          static_cast<float*>(row)[e0 + i] = x[i];
+          static_cast<float*>(row)[e] = v;
         else
-          static_cast<__nv_bfloat16*>(row)[e0 + i] = __float2bfloat16_rn(x[i]);
+          static_cast<__nv_bfloat16*>(row)[e] = __float2bfloat16_rn(v);
       }
+    }
   }
 }
 
@@ -98,6 +147,29 @@ __device__ __forceinline__ float row_sum(float v) {
   for (int o = T / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+__device__ __forceinline__ float dot8(const Row& x, const Row& y) {
+  float2 s = mul2(x.v[0], y.v[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = fma2(x.v[i], y.v[i], s);
+  return s.x + s.y;
+}
+// r = (mean(x^2) + eps)^(-1/2) of a row.
+template <int T>
+__device__ __forceinline__ float norm_factor(const Row& x, float eps, float inv_d) {
+  return rsqrtf(row_sum<T>(dot8(x, x)) * inv_d + eps);
+}
+__device__ __forceinline__ Row scaled(const Row& x, float f) {
+  Row y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y.v[i] = mul2(x.v[i], splat2(f));
+  return y;
+}
+__device__ __forceinline__ Row product(const Row& x, const Row& y) {
+  Row z;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z.v[i] = mul2(x.v[i], y.v[i]);
+  return z;
+}
 
 // cos and sin of pos * inv_freq.  The angle is taken in turns and reduced in
 // fp64 (pos is up to 2^31 and inv_freq a full fp32 value: in fp32 the angle of
@@ -110,95 +182,114 @@ __device__ __forceinline__ void angle(int pos, float inv_freq, float* c, float* 
   sincospif(2.0f * f, s, c);
 }
 
-// This lane's (c_i, s_i) of one token from its table of rot / 2 cosines and
-// sines (shared memory).
-template <Pair kPair>
-__device__ __forceinline__ void lane_angles(const float* cos_t, const float* sin_t, int e0, int rot, float (&c)[8],
-                                            float (&s)[8]) {
-  const int h = rot >> 1;
+// A linear map of a lane's pieces:
+//   kHalf: a' = a c_0,1 + b s_0,1,   b' = b c_2,3 + a s_2,3
+//   kNext: v' = v c + swapped(v) s for each pair
+// which a rotation, its inverse and either with the norm's weights folded in
+// all are.
+struct Turn {
+  float2 c[4], s[4];
+};
+template <bool kNext>
+__device__ __forceinline__ Row apply(const Row& x, const Turn& f, const Place& p, int rot, int D) {
+  Row y;
+  if constexpr (kNext) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = e0 + i;
-    c[i] = 1.0f;
-    s[i] = 0.0f;
-    if (e < rot) {
-      const int f = kPair == Pair::kNext ? e >> 1 : (e < h ? e : e - h);
-      const bool first = kPair == Pair::kNext ? (i & 1) == 0 : e < h;
-      c[i] = cos_t[f];
-      s[i] = first ? -sin_t[f] : sin_t[f];
-    }
-  }
-}
-
-// x[(i + k) & 7] for a k that all lanes share.
-__device__ __forceinline__ void turn8(float (&x)[8], int k) {
-#pragma unroll
-  for (int b = 1; b < 8; b <<= 1) {
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = (k & b) ? x[(i + b) & 7] : x[i];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = y[i];
-  }
-}
-
-// y_i = x_i c_i + sgn * p_i s_i (sgn -1 turns back).  Called by all lanes of
-// a warp; t is the lane's place in its row of T lanes.
-template <int T, Pair kPair>
-__device__ __forceinline__ void rotate8(const float (&x)[8], const float (&c)[8], const float (&s)[8], float sgn, int t,
-                                        int rot, float (&y)[8]) {
-  float p[8];
-  const int h = rot >> 1;
-  if constexpr (kPair == Pair::kNext) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = x[i ^ 1];
-  } else if constexpr (kPair == Pair::kHalf) {
-    const int e0 = 8 * t;
-    const int src = e0 < h ? t + (h >> 3) : (e0 < rot ? t - (h >> 3) : t);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = __shfl_sync(0xffffffffu, x[i], src, T);
+    for (int i = 0; i < 4; ++i) y.v[i] = fma2(make_float2(x.v[i].y, x.v[i].x), f.s[i], mul2(x.v[i], f.c[i]));
   } else {
-    // element i of the lane is paired with element 8 t + i +- h of the row:
-    // place (i +- h) & 7, the same for all lanes, of a lane of its own
-    float up[8], dn[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) up[i] = dn[i] = x[i];
-    turn8(up, h & 7);
-    turn8(dn, (8 - (h & 7)) & 7);
+    for (int i = 0; i < 4; ++i) y.v[i] = fma2(x.v[i ^ 2], f.s[i], mul2(x.v[i], f.c[i]));
+  }
+  // What passes through does so alone: 0 times its partner would turn an
+  // infinity there into NaN.
+  if (rot < D) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int e = 8 * t + i;
-      const float a = __shfl_sync(0xffffffffu, up[i], min((e + h) >> 3, T - 1), T);
-      const float b = __shfl_sync(0xffffffffu, dn[i], max(e - h, 0) >> 3, T);
-      p[i] = e < h ? a : b;
+      const bool turns = kNext ? p.a + i < rot : (i & 3) < p.pairs;
+      if (turns) continue;
+      if (i & 1)
+        y.v[i >> 1].y = x.v[i >> 1].y * f.c[i >> 1].y;
+      else
+        y.v[i >> 1].x = x.v[i >> 1].x * f.c[i >> 1].x;
     }
   }
-  // elements past rot pass through as they are (0 * p would turn an infinity into NaN)
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = 8 * t + i < rot ? fmaf(p[i], sgn * s[i], x[i] * c[i]) : x[i];
+  return y;
 }
 
-// A norm's weights of this lane (1 without weights, 0 past D).
-__device__ __forceinline__ void load_weight8(const NormArgs& n, int e0, int D, float (&w)[8]) {
+// The rotation by a token's angles (tables of rot / 2 cosines and sines in
+// shared memory, 16-byte aligned where 8 | rot); sign -1 turns back.
+template <bool kNext>
+__device__ __forceinline__ Turn rotation(const float* cos_t, const float* sin_t, int t, const Place& p, int rot,
+                                         float sign) {
+  float c[4], s[4];
+  const int h = rot >> 1;
+  if ((rot & 7) == 0) {
+    float4 cv = make_float4(1.0f, 1.0f, 1.0f, 1.0f), sv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (4 * t < h) {
+      cv = *reinterpret_cast<const float4*>(cos_t + 4 * t);
+      sv = *reinterpret_cast<const float4*>(sin_t + 4 * t);
+    }
+    c[0] = cv.x; c[1] = cv.y; c[2] = cv.z; c[3] = cv.w;
+    s[0] = sv.x; s[1] = sv.y; s[2] = sv.z; s[3] = sv.w;
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = e0 + i;
-    w[i] = e >= D                ? 0.0f
-           : n.weight == nullptr ? 1.0f
-           : n.weight_f32        ? __ldg(static_cast<const float*>(n.weight) + e)
-                                 : __bfloat162float(static_cast<const __nv_bfloat16*>(n.weight)[e]);
+    for (int i = 0; i < 4; ++i) {
+      const bool in = 4 * t + i < h;
+      c[i] = in ? cos_t[4 * t + i] : 1.0f;
+      s[i] = in ? sin_t[4 * t + i] : 0.0f;
+    }
+  }
+  Turn f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kNext) {
+      f.c[i] = make_float2(c[i], c[i]);
+      f.s[i] = make_float2(-sign * s[i], sign * s[i]);
+    } else {
+      const int k = 2 * (i & 1);
+      f.c[i] = make_float2(c[k], c[k + 1]);
+      const float sg = i < 2 ? -sign : sign;
+      f.s[i] = make_float2(sg * s[k], sg * s[k + 1]);
+    }
+  }
+  return f;
+}
+__device__ __forceinline__ Turn identity() {
+  Turn f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f.c[i] = make_float2(1.0f, 1.0f);
+    f.s[i] = make_float2(0.0f, 0.0f);
+  }
+  return f;
+}
+// The map that weighs by w first.
+template <bool kNext>
+__device__ __forceinline__ void fold(Turn& f, const Row& w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f.c[i] = mul2(f.c[i], w.v[i]);
+    f.s[i] = mul2(f.s[i], kNext ? make_float2(w.v[i].y, w.v[i].x) : w.v[i ^ 2]);
   }
 }
 
-// x <- x r w, r = (mean(x^2) + eps)^(-1/2).
-template <int T>
-__device__ __forceinline__ void norm8(float (&x)[8], const float (&w)[8], float eps, float inv_d) {
-  float ss = 0.0f;
+// A norm's weights of this lane: 1 without weights, 0 where it holds nothing.
+__device__ __forceinline__ Row load_weight(const NormArgs& n, const Place& p) {
+  Row w;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-  const float r = rsqrtf(row_sum<T>(ss) * inv_d + eps);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
+  for (int i = 0; i < 8; ++i) {
+    const int e = i < 4 ? p.a + i : p.b + i - 4;
+    const bool in = (i & 3) < (i < 4 ? p.na : p.nb);
+    const float v = !in                  ? 0.0f
+                    : n.weight == nullptr ? 1.0f
+                    : n.weight_f32        ? __ldg(static_cast<const float*>(n.weight) + e)
+                                          : __bfloat162float(static_cast<const __nv_bfloat16*>(n.weight)[e]);
+    if (i & 1)
+      w.v[i >> 1].y = v;
+    else
+      w.v[i >> 1].x = v;
+  }
+  return w;
 }
 
 }  // namespace fa

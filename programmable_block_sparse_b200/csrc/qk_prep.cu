@@ -3,12 +3,11 @@
 //
 // Both kernels are bound by HBM: a row is read once and written once (the
 // backward reads the row and its output gradient).  T lanes hold a row
-// (headprep.cuh), so a warp takes 2 (D <= 128) or 4 (D <= 64) rows and every
-// access is 16 bytes a lane.  A CTA takes a few tokens and all (or a run of)
-// their heads: a token's angles are the same for every head, so their fp64
-// reduction and sincos are paid once a token, into shared memory, and each
-// group of T lanes keeps its token's cosines and sines in registers while it
-// walks the heads, several rows in flight.
+// (headprep.cuh).  A CTA takes a few tokens and all (or a run of) their heads:
+// a token's angles are the same for every head, so their fp64 reduction and
+// sincos are paid once a token, into shared memory, and each group of T lanes
+// keeps its token's factors in registers while it walks the heads, several
+// rows in flight.
 #include "headprep.cuh"
 
 namespace fa {
@@ -30,63 +29,129 @@ __device__ __forceinline__ void fill_tables(const RopeArgs& r, int b, int n0, in
   }
 }
 
-template <int T, Pair kPair, bool kVec>
+// The heads h0 .. h1 - 1 of one side for this group's token.  Every lane of a
+// warp takes the same number of turns (shuffles).
+template <int T, bool kNext, bool kVec, bool kF32>
+__device__ __forceinline__ void prep_rows(const PrepArgs& a, const RowsIn& in, const RowsOut& out, int b, int n, int h0,
+                                          int h1, int sub, int per, int norm, float eps, const Place& p,
+                                          const Turn& f) {
+  constexpr int U = 4;  // rows in flight per group
+  const float inv_d = 1.0f / static_cast<float>(a.D);
+  const bool here = n < a.N;
+  const char* ip = static_cast<const char*>(in.p) +
+                   (b * in.stride[0] + n * in.stride[2] + (h0 + sub) * in.stride[1]) * (kF32 ? 4 : 2);
+  const int64_t istep = in.stride[1] * per * (kF32 ? 4 : 2);
+  char* op = static_cast<char*>(out.p) +
+             (b * out.stride[0] + n * out.stride[2] + (h0 + sub) * out.stride[1]) * (out.f32 ? 4 : 2);
+  const int64_t ostep = out.stride[1] * per * (out.f32 ? 4 : 2);
+  for (int hb = h0; hb < h1; hb += per * U) {
+    Raw<kVec, kF32> raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (here && hb + sub + u * per < h1)
+        load_raw(ip + u * istep, p, raw[u]);
+      else
+        clear_raw(raw[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (hb + u * per >= h1) break;  // the same for the whole CTA
+      const Row x = unpack(raw[u]);
+      Row y = apply<kNext>(x, f, p, a.rope.rot, a.D);
+      if (norm) y = scaled(y, norm_factor<T>(x, eps, inv_d));
+      if (here && hb + sub + u * per < h1) store_row<kVec>(op + u * ostep, out.f32, p, y);
+    }
+    ip += U * istep;
+    op += U * ostep;
+  }
+}
+
+template <int T, bool kNext, bool kVec>
 __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constant__ PrepArgs a) {
   constexpr int kGroups = kPrepThreads / T;
-  constexpr int U = 4;  // rows in flight per group
-  __shared__ float cos_t[kTableFloats], sin_t[kTableFloats];
+  __shared__ __align__(16) float cos_t[kTableFloats], sin_t[kTableFloats];
   const int b = blockIdx.z, n0 = blockIdx.x * a.tokens;
   const int t = threadIdx.x % T, grp = threadIdx.x / T;
   const int tk = grp % a.tokens, sub = grp / a.tokens, per = kGroups / a.tokens;
-  const int n = n0 + tk, e0 = 8 * t, rot = a.rope.rot;
-  float c[8], s[8];
+  const int n = n0 + tk, rot = a.rope.rot;
+  const Place p = place_of<kNext>(t, rot, a.D);
   if (rot) {
     fill_tables(a.rope, b, n0, a.tokens, a.N, cos_t, sin_t);
     __syncthreads();
-    lane_angles<kPair>(cos_t + tk * (rot >> 1), sin_t + tk * (rot >> 1), e0, rot, c, s);
   }
-  const float inv_d = 1.0f / static_cast<float>(a.D);
   const int first = blockIdx.y * a.heads, last = first + a.heads;  // of the heads of q, then of k
   int before = 0;
 #pragma unroll 1
   for (int side = 0; side < 2; ++side) {
     const RowsIn& in = a.x[side];
     if (in.p == nullptr) continue;
-    const RowsOut& out = a.y[side];
     const int h0 = max(first - before, 0), h1 = min(last - before, in.H);
     before += in.H;
     if (h0 >= h1) continue;
-    const int norm = a.norm[side].on;
-    float w[8];
-    if (norm) load_weight8(a.norm[side], e0, a.D, w);
-    const int64_t ib = b * in.stride[0] + n * in.stride[2], ob = b * out.stride[0] + n * out.stride[2];
-    // every lane of a warp takes the same number of turns (shuffles)
-    for (int hb = h0; hb < h1; hb += per * U) {
-      float x[U][8];
+    Turn f = rot ? rotation<kNext>(cos_t + tk * (rot >> 1), sin_t + tk * (rot >> 1), t, p, rot, 1.0f) : identity();
+    const NormArgs& norm = a.norm[side];
+    if (norm.on) fold<kNext>(f, load_weight(norm, p));
+    if (in.f32)
+      prep_rows<T, kNext, kVec, true>(a, in, a.y[side], b, n, h0, h1, sub, per, norm.on, norm.eps, p, f);
+    else
+      prep_rows<T, kNext, kVec, false>(a, in, a.y[side], b, n, h0, h1, sub, per, norm.on, norm.eps, p, f);
+  }
+}
+
+// Gradients of the heads of one side for this group's token; dw collects the
+// weight gradient.
+template <int T, bool kNext, bool kVec, bool kXF32, bool kGF32>
+__device__ __forceinline__ void prep_bwd_rows(const PrepBwdArgs& a, int side, int b, int n, int sub, int per,
+                                              const Place& p, const Turn& f, const Row& w, Row& dw) {
+  constexpr int U = kXF32 || kGF32 ? 2 : 4;
+  const RowsIn &dy = a.dy[side], &in = a.x[side];
+  const RowsOut& dx = a.dx[side];
+  const int norm = a.norm[side].on;
+  const float eps = a.norm[side].eps, inv_d = 1.0f / static_cast<float>(a.D);
+  const bool here = n < a.N;
+  const char* gp = static_cast<const char*>(dy.p) +
+                   (b * dy.stride[0] + n * dy.stride[2] + sub * dy.stride[1]) * (kGF32 ? 4 : 2);
+  const char* xp = static_cast<const char*>(in.p) +
+                   (b * in.stride[0] + n * in.stride[2] + sub * in.stride[1]) * (kXF32 ? 4 : 2);
+  char* op = static_cast<char*>(dx.p) +
+             (b * dx.stride[0] + n * dx.stride[2] + sub * dx.stride[1]) * (dx.f32 ? 4 : 2);
+  const int64_t gstep = dy.stride[1] * per * (kGF32 ? 4 : 2), xstep = in.stride[1] * per * (kXF32 ? 4 : 2);
+  const int64_t ostep = dx.stride[1] * per * (dx.f32 ? 4 : 2);
+  for (int hb = 0; hb < dy.H; hb += per * U) {
+    Raw<kVec, kGF32> graw[U];
+    Raw<kVec, kXF32> xraw[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = hb + sub + u * per;
-        if (n < a.N && h < h1)
-          load8<kVec>(row_ptr(in.p, in.f32, ib + h * in.stride[1]), in.f32, e0, a.D, x[u]);
-        else
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[u][i] = 0.0f;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (hb + u * per >= h1) break;  // the same for the whole CTA
-        const int h = hb + sub + u * per;
-        float y[8];
-        if (norm) norm8<T>(x[u], w, a.norm[side].eps, inv_d);
-        if (rot) {
-          rotate8<T, kPair>(x[u], c, s, 1.0f, t, rot, y);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = x[u][i];
-        }
-        if (n < a.N && h < h1) store8<kVec>(row_ptr(out.p, out.f32, ob + h * out.stride[1]), out.f32, e0, a.D, y);
-      }
+    for (int u = 0; u < U; ++u) {
+      const bool ok = here && hb + sub + u * per < dy.H;
+      if (ok)
+        load_raw(gp + u * gstep, p, graw[u]);
+      else
+        clear_raw(graw[u]);
+      if (ok && norm)
+        load_raw(xp + u * xstep, p, xraw[u]);
+      else
+        clear_raw(xraw[u]);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (hb + u * per >= dy.H) break;  // the same for the whole CTA
+      Row y = apply<kNext>(unpack(graw[u]), f, p, a.rope.rot, a.D);
+      if (norm) {
+        const Row x = unpack(xraw[u]), yw = product(y, w);
+        const float r = norm_factor<T>(x, eps, inv_d);
+        const float k = row_sum<T>(dot8(yw, x)) * inv_d * r * r;
+        const Row xr = scaled(x, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dw.v[i] = fma2(y.v[i], xr.v[i], dw.v[i]);
+          y.v[i] = fma2(splat2(-k), xr.v[i], mul2(yw.v[i], splat2(r)));
+        }
+      }
+      if (here && hb + sub + u * per < dy.H) store_row<kVec>(op + u * ostep, dx.f32, p, y);
+    }
+    gp += U * gstep;
+    xp += U * xstep;
+    op += U * ostep;
   }
 }
 
@@ -94,81 +159,42 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
 // stride of the grid, keeps this lane's share of the weight gradients in
 // registers over all of them, and writes one partial row per side; the sums
 // over CTAs follow in a second kernel in a fixed order.
-template <int T, Pair kPair, bool kVec>
+template <int T, bool kNext, bool kVec>
 __global__ void __launch_bounds__(kPrepThreads) prep_bwd_kernel(const __grid_constant__ PrepBwdArgs a) {
   constexpr int kGroups = kPrepThreads / T;
-  constexpr int U = 2;
-  __shared__ float cos_t[kTableFloats], sin_t[kTableFloats];
-  __shared__ float red[kGroups][T * 8 + 1];
+  __shared__ __align__(16) float cos_t[kTableFloats], sin_t[kTableFloats];
+  __shared__ float red[kGroups][129];
   const int t = threadIdx.x % T, grp = threadIdx.x / T;
   const int tk = grp % a.tokens, sub = grp / a.tokens, per = kGroups / a.tokens;
-  const int e0 = 8 * t, rot = a.rope.rot;
-  const float inv_d = 1.0f / static_cast<float>(a.D);
+  const int rot = a.rope.rot;
+  const Place p = place_of<kNext>(t, rot, a.D);
   const int blocks = (a.N + a.tokens - 1) / a.tokens;
-  float dw[2][8];
+  Row dw[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.0f;
+  for (int i = 0; i < 4; ++i) dw[0].v[i] = dw[1].v[i] = make_float2(0.0f, 0.0f);
   for (int64_t item = blockIdx.x; item < static_cast<int64_t>(blocks) * a.B; item += gridDim.x) {
     const int b = static_cast<int>(item / blocks), n0 = static_cast<int>(item % blocks) * a.tokens, n = n0 + tk;
-    float c[8], s[8];
+    Turn f = identity();
     if (rot) {
       __syncthreads();  // the tables of the previous item have been read
       fill_tables(a.rope, b, n0, a.tokens, a.N, cos_t, sin_t);
       __syncthreads();
-      lane_angles<kPair>(cos_t + tk * (rot >> 1), sin_t + tk * (rot >> 1), e0, rot, c, s);
+      f = rotation<kNext>(cos_t + tk * (rot >> 1), sin_t + tk * (rot >> 1), t, p, rot, -1.0f);
     }
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
-      const RowsIn& dy = a.dy[side];
-      if (dy.p == nullptr) continue;
-      const RowsIn& in = a.x[side];
-      const RowsOut& dx = a.dx[side];
-      const int norm = a.norm[side].on;
-      const float eps = a.norm[side].eps;
-      float w[8];
-      if (norm) load_weight8(a.norm[side], e0, a.D, w);
-      const int64_t gb = b * dy.stride[0] + n * dy.stride[2], xb = b * in.stride[0] + n * in.stride[2];
-      const int64_t ob = b * dx.stride[0] + n * dx.stride[2];
-      for (int hb = 0; hb < dy.H; hb += per * U) {
-        float g[U][8], x[U][8];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int h = hb + sub + u * per;
-          const bool ok = n < a.N && h < dy.H;
-          if (ok) load8<kVec>(row_ptr(dy.p, dy.f32, gb + h * dy.stride[1]), dy.f32, e0, a.D, g[u]);
-          if (ok && norm) load8<kVec>(row_ptr(in.p, in.f32, xb + h * in.stride[1]), in.f32, e0, a.D, x[u]);
-          if (!ok)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[u][i] = x[u][i] = 0.0f;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (hb + u * per >= dy.H) break;  // the same for the whole CTA
-          const int h = hb + sub + u * per;
-          float y[8];
-          if (rot) {
-            rotate8<T, kPair>(g[u], c, s, -1.0f, t, rot, y);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = g[u][i];
-          }
-          if (norm) {
-            float ss = 0.0f, dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              ss = fmaf(x[u][i], x[u][i], ss);
-              dot = fmaf(y[i] * w[i], x[u][i], dot);
-            }
-            const float r = rsqrtf(row_sum<T>(ss) * inv_d + eps);
-            const float k = row_sum<T>(dot) * inv_d * r * r;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              dw[side][i] = fmaf(y[i] * r, x[u][i], dw[side][i]);
-              y[i] = r * fmaf(-k, x[u][i], y[i] * w[i]);
-            }
-          }
-          if (n < a.N && h < dy.H) store8<kVec>(row_ptr(dx.p, dx.f32, ob + h * dx.stride[1]), dx.f32, e0, a.D, y);
-        }
+      if (a.dy[side].p == nullptr) continue;
+      const Row w = load_weight(a.norm[side], p);
+      if (a.x[side].f32) {
+        if (a.dy[side].f32)
+          prep_bwd_rows<T, kNext, kVec, true, true>(a, side, b, n, sub, per, p, f, w, dw[side]);
+        else
+          prep_bwd_rows<T, kNext, kVec, true, false>(a, side, b, n, sub, per, p, f, w, dw[side]);
+      } else {
+        if (a.dy[side].f32)
+          prep_bwd_rows<T, kNext, kVec, false, true>(a, side, b, n, sub, per, p, f, w, dw[side]);
+        else
+          prep_bwd_rows<T, kNext, kVec, false, false>(a, side, b, n, sub, per, p, f, w, dw[side]);
       }
     }
   }
@@ -177,7 +203,9 @@ __global__ void __launch_bounds__(kPrepThreads) prep_bwd_kernel(const __grid_con
     if (a.dw[side] == nullptr) continue;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) red[grp][e0 + i] = dw[side][i];
+    for (int i = 0; i < 8; ++i)
+      if ((i & 3) < (i < 4 ? p.na : p.nb))
+        red[grp][i < 4 ? p.a + i : p.b + i - 4] = (i & 1) ? dw[side].v[i >> 1].y : dw[side].v[i >> 1].x;
     __syncthreads();
     if (threadIdx.x < a.D) {
       float v = 0.0f;
@@ -210,59 +238,53 @@ __global__ void __launch_bounds__(1024) prep_dw_kernel(const float* partial, int
   }
 }
 
-Pair pair_of(const RopeArgs& r) {
-  if (r.rot == 0 || r.interleaved) return Pair::kNext;
-  return (r.rot / 2) % 8 == 0 ? Pair::kHalf : Pair::kHalfAny;
-}
+// Lanes a row, for rows that take vector accesses and others.
+int lanes_of(int D, bool vec) { return !vec ? 32 : (D <= 64 ? 8 : 16); }
 
-// The kernel of a call; rows without 16-byte accesses share the any-place
-// pairing.
-template <int T>
-cudaError_t launch_prep_t(const PrepArgs& a, dim3 grid, cudaStream_t st) {
-  const Pair pair = pair_of(a.rope);
-  auto kern = pair == Pair::kNext ? (a.vec ? prep_kernel<T, Pair::kNext, true> : prep_kernel<T, Pair::kNext, false>)
-              : !a.vec            ? prep_kernel<T, Pair::kHalfAny, false>
-              : pair == Pair::kHalf ? prep_kernel<T, Pair::kHalf, true>
-                                    : prep_kernel<T, Pair::kHalfAny, true>;
-  kern<<<grid, kPrepThreads, 0, st>>>(a);
-  return cudaGetLastError();
-}
-
-template <int T>
-cudaError_t launch_prep_bwd_t(const PrepBwdArgs& a, int ctas, cudaStream_t st) {
-  const Pair pair = pair_of(a.rope);
-  auto kern = pair == Pair::kNext
-                  ? (a.vec ? prep_bwd_kernel<T, Pair::kNext, true> : prep_bwd_kernel<T, Pair::kNext, false>)
-              : !a.vec              ? prep_bwd_kernel<T, Pair::kHalfAny, false>
-              : pair == Pair::kHalf ? prep_bwd_kernel<T, Pair::kHalf, true>
-                                    : prep_bwd_kernel<T, Pair::kHalfAny, true>;
-  kern<<<ctas, kPrepThreads, 0, st>>>(a);
-  return cudaGetLastError();
+// Tokens a CTA: four, or more where its groups would outnumber a token's heads.
+int tokens_of(int lanes, int heads) {
+  const int groups = kPrepThreads / lanes;
+  int tokens = 4;
+  while (tokens < groups && groups / tokens > heads) tokens *= 2;
+  return tokens;
 }
 
 }  // namespace
 
 cudaError_t launch_prep(PrepArgs a, int num_sms, cudaStream_t st) {
   const int heads = (a.x[0].p ? a.x[0].H : 0) + (a.x[1].p ? a.x[1].H : 0);
-  const int groups = kPrepThreads / (a.D <= 64 ? 8 : 16);
-  // Four tokens a CTA with all their heads where that fills the GPU; one token
+  const bool next = a.rope.rot == 0 || a.rope.interleaved, vec = a.vec && (next || a.rope.rot % 8 == 0);
+  const int lanes = lanes_of(a.D, vec);
+  // A few tokens a CTA with all their heads where that fills the GPU; one token
   // a CTA, and its heads cut into runs of one turn of the groups, where it
   // does not (a decode step).
-  a.tokens = 4;
+  a.tokens = tokens_of(lanes, heads);
   a.heads = heads;
-  if (static_cast<int64_t>(a.B) * ((a.N + 3) / 4) < 4 * num_sms) {
+  if (static_cast<int64_t>(a.B) * ((a.N + a.tokens - 1) / a.tokens) < 4 * num_sms) {
     a.tokens = 1;
-    a.heads = groups;
+    a.heads = kPrepThreads / lanes;
   }
+  auto kern = !vec          ? (next ? prep_kernel<32, true, false> : prep_kernel<32, false, false>)
+              : lanes == 8 ? (next ? prep_kernel<8, true, true> : prep_kernel<8, false, true>)
+                            : (next ? prep_kernel<16, true, true> : prep_kernel<16, false, true>);
   const dim3 grid((a.N + a.tokens - 1) / a.tokens, (heads + a.heads - 1) / a.heads, a.B);
-  return a.D <= 64 ? launch_prep_t<8>(a, grid, st) : launch_prep_t<16>(a, grid, st);
+  kern<<<grid, kPrepThreads, 0, st>>>(a);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_prep_bwd(PrepBwdArgs a, cudaStream_t st) {
-  a.tokens = static_cast<int64_t>(a.B) * ((a.N + 3) / 4) < kPrepBwdMaxCtas ? 1 : 4;
+  const int heads = (a.dy[0].p ? a.dy[0].H : 0) + (a.dy[1].p ? a.dy[1].H : 0);
+  const bool next = a.rope.rot == 0 || a.rope.interleaved, vec = a.vec && (next || a.rope.rot % 8 == 0);
+  const int lanes = lanes_of(a.D, vec);
+  a.tokens = tokens_of(lanes, heads);
+  if (static_cast<int64_t>(a.B) * ((a.N + a.tokens - 1) / a.tokens) < kPrepBwdMaxCtas) a.tokens = 1;
   const int64_t items = static_cast<int64_t>(a.B) * ((a.N + a.tokens - 1) / a.tokens);
   const int ctas = static_cast<int>(items < kPrepBwdMaxCtas ? items : kPrepBwdMaxCtas);
-  const cudaError_t e = a.D <= 64 ? launch_prep_bwd_t<8>(a, ctas, st) : launch_prep_bwd_t<16>(a, ctas, st);
+  auto kern = !vec          ? (next ? prep_bwd_kernel<32, true, false> : prep_bwd_kernel<32, false, false>)
+              : lanes == 8 ? (next ? prep_bwd_kernel<8, true, true> : prep_bwd_kernel<8, false, true>)
+                            : (next ? prep_bwd_kernel<16, true, true> : prep_bwd_kernel<16, false, true>);
+  kern<<<ctas, kPrepThreads, 0, st>>>(a);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (a.dw[0] == nullptr && a.dw[1] == nullptr)) return e;
   prep_dw_kernel<<<dim3((a.D + 31) / 32, 2), 1024, 0, st>>>(a.partial, ctas, a.D, a.dw[0], a.dw[1]);
   return cudaGetLastError();
