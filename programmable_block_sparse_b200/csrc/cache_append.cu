@@ -85,14 +85,12 @@ __device__ __forceinline__ void load_rows(const RowsIn& in, int64_t off, int n0,
 // Queries of ntok tokens from n0 on and nh heads from hq0 on.
 template <int T, bool kNext, bool kVec, bool kF32>
 __device__ __forceinline__ void append_queries(const AppendArgs& a, int b, int n0, int ntok, int hq0, int nh,
-                                               const float* cos_t, const float* sin_t) {
+                                               const float* cos_t, const float* sin_t, const float* s_w) {
   constexpr int kGroups = threads_of(T) / T;
   constexpr int U = 2;
   const int t = threadIdx.x % T, grp = threadIdx.x / T, rot = a.rope.rot;
   const Place p = place_of<kNext>(t, rot, a.E);
   const int rows = ntok * nh;
-  Row w;
-  if (a.q_norm.on) w = load_weight(a.q_norm, p);
   for (int r0 = 0; r0 < rows; r0 += U * kGroups) {
     Raw<kVec, kF32> raw[U];
 #pragma unroll
@@ -100,14 +98,15 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, int b, int n
       const int r = min(r0 + u * kGroups + grp, rows - 1), n = n0 + r % ntok, h = hq0 + r / ntok;
       load_raw(row_ptr(a.q.p, kF32, b * a.q.stride[0] + h * a.q.stride[1] + n * a.q.stride[2]), p, raw[u]);
     }
-    if (r0 == 0 && rot) __syncthreads();  // the angles: the first loads go ahead of them
+    if (r0 == 0) __syncthreads();  // the angles and weights: the first loads go ahead of them
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (r0 + u * kGroups >= rows) break;  // the same for the whole CTA
       const int r = min(r0 + u * kGroups + grp, rows - 1), tk = r % ntok, n = n0 + tk, h = hq0 + r / ntok;
       Row x = unpack(raw[u]);
       if (a.q_norm.on)
-        x = product(scaled(x, norm_factor<T>(x, a.q_norm.eps, 1.0f / static_cast<float>(a.E))), w);
+        x = product(scaled(x, norm_factor<T>(x, a.q_norm.eps, 1.0f / static_cast<float>(a.E))),
+                    lane_weight<kVec>(s_w, p));
       if (rot)
         x = apply<kNext>(x, rotation<kNext>(cos_t + tk * (rot >> 1), sin_t + tk * (rot >> 1), t, p, rot, 1.0f), p, rot,
                          a.E);
@@ -124,6 +123,7 @@ template <int T, bool kNext, bool kVec, int kIters>
 __global__ void __launch_bounds__(threads_of(T)) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kThreads = threads_of(T), kGroups = kThreads / T;
   extern __shared__ __align__(16) float tables[];  // cosines, then sines, of the chunk's tokens
+  __shared__ __align__(16) float s_w[128];
   __shared__ int s_outer[kMaxChunk];
   __shared__ uint32_t s_amax[32];
   __shared__ float s_scale[32], s_old[32];
@@ -153,10 +153,11 @@ __global__ void __launch_bounds__(threads_of(T)) append_kernel(const __grid_cons
     if (ntok <= 0) return;
     const int hq0 = (blockIdx.y - 2 * kv_runs) * a.q_heads, nh = min(a.q_heads, a.q.H - hq0);
     if (rot) fill(n0, ntok, 0);
+    if (a.q_norm.on) stage_weight(a.q_norm, a.E, 128, s_w);
     if (a.q.f32)
-      append_queries<T, kNext, kVec, true>(a, b, n0, ntok, hq0, nh, cos_t, sin_t);
+      append_queries<T, kNext, kVec, true>(a, b, n0, ntok, hq0, nh, cos_t, sin_t, s_w);
     else
-      append_queries<T, kNext, kVec, false>(a, b, n0, ntok, hq0, nh, cos_t, sin_t);
+      append_queries<T, kNext, kVec, false>(a, b, n0, ntok, hq0, nh, cos_t, sin_t, s_w);
     return;
   }
 
@@ -192,8 +193,7 @@ __global__ void __launch_bounds__(threads_of(T)) append_kernel(const __grid_cons
     const int from = max(slot0, sp.start);
     fill(from - sp.start, min(end, slot0 + a.chunk) - from, from - slot0);
   }
-  Row w;
-  if (norm) w = load_weight(a.k_norm, p);
+  if (norm) stage_weight(a.k_norm, D, 128, s_w);
   const int e4m3 = a.dtype == FA_DTYPE_E4M3;
   const int sb_log = e4m3 ? __ffs(a.scale_block) - 1 : 5;
   float* scales = is_k ? a.k_scale : a.v_scale;
@@ -213,7 +213,8 @@ __global__ void __launch_bounds__(threads_of(T)) append_kernel(const __grid_cons
 #pragma unroll
     for (int it = 0; it < kIters; ++it) {
       const int row = it * kGroups + grp;
-      if (norm) x[it] = product(scaled(x[it], norm_factor<T>(x[it], a.k_norm.eps, 1.0f / static_cast<float>(D))), w);
+      if (norm) x[it] = product(scaled(x[it], norm_factor<T>(x[it], a.k_norm.eps, 1.0f / static_cast<float>(D))),
+                                  lane_weight<kVec>(s_w, p));
       if (turn)
         x[it] = apply<kNext>(x[it], rotation<kNext>(cos_t + row * h2, sin_t + row * h2, t, p, rot, 1.0f), p, rot, D);
       if (e4m3) {

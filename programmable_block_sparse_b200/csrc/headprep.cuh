@@ -273,23 +273,36 @@ __device__ __forceinline__ void fold(Turn& f, const Row& w) {
   }
 }
 
-// A norm's weights of this lane: 1 without weights, 0 where it holds nothing.
-__device__ __forceinline__ Row load_weight(const NormArgs& n, const Place& p) {
-  Row w;
+// A norm's weights as fp32 in shared memory (1 without weights; `pad` floats,
+// 0 past D), and a lane's share of them.
+__device__ __forceinline__ void stage_weight(const NormArgs& n, int D, int pad, float* w) {
+  for (int e = threadIdx.x; e < pad; e += blockDim.x)
+    w[e] = e >= D                ? 0.0f
+           : n.weight == nullptr ? 1.0f
+           : n.weight_f32        ? __ldg(static_cast<const float*>(n.weight) + e)
+                                 : __bfloat162float(static_cast<const __nv_bfloat16*>(n.weight)[e]);
+}
+template <bool kVec>
+__device__ __forceinline__ Row lane_weight(const float* w, const Place& p) {
+  Row r;
+  if constexpr (kVec) {  // pieces are whole and start on multiples of 4
+    const float4 a = p.na ? *reinterpret_cast<const float4*>(w + p.a) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float4 b = p.nb ? *reinterpret_cast<const float4*>(w + p.b) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    r.v[0] = make_float2(a.x, a.y);
+    r.v[1] = make_float2(a.z, a.w);
+    r.v[2] = make_float2(b.x, b.y);
+    r.v[3] = make_float2(b.z, b.w);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = i < 4 ? p.a + i : p.b + i - 4;
-    const bool in = (i & 3) < (i < 4 ? p.na : p.nb);
-    const float v = !in                  ? 0.0f
-                    : n.weight == nullptr ? 1.0f
-                    : n.weight_f32        ? __ldg(static_cast<const float*>(n.weight) + e)
-                                          : __bfloat162float(static_cast<const __nv_bfloat16*>(n.weight)[e]);
-    if (i & 1)
-      w.v[i >> 1].y = v;
-    else
-      w.v[i >> 1].x = v;
+    for (int i = 0; i < 8; ++i) {
+      const float v = (i & 3) < (i < 4 ? p.na : p.nb) ? w[i < 4 ? p.a + i : p.b + i - 4] : 0.0f;
+      if (i & 1)
+        r.v[i >> 1].y = v;
+      else
+        r.v[i >> 1].x = v;
+    }
   }
-  return w;
+  return r;
 }
 
 }  // namespace fa

@@ -159,8 +159,8 @@ struct PrepBwdArgs {
 };
 // CTAs of the backward pass at most: its partial weight gradients are summed
 // over them, so the bound fixes the workspace (and the order of the sum) on
-// every device.  Four a B200's SM.
-constexpr int kPrepBwdMaxCtas = 592;
+// every device.  Three a B200's SM.
+constexpr int kPrepBwdMaxCtas = 444;
 cudaError_t launch_prep_bwd(PrepBwdArgs a, cudaStream_t stream);
 
 struct AppendArgs {

@@ -35,7 +35,7 @@ template <int T, bool kNext, bool kVec, bool kF32>
 __device__ __forceinline__ void prep_rows(const PrepArgs& a, const RowsIn& in, const RowsOut& out, int b, int n, int h0,
                                           int h1, int sub, int per, int norm, float eps, const Place& p,
                                           const Turn& f) {
-  constexpr int U = 4;  // rows in flight per group
+  constexpr int U = kVec && !kF32 ? 4 : 2;  // rows in flight per group
   const float inv_d = 1.0f / static_cast<float>(a.D);
   const bool here = n < a.N;
   const char* ip = static_cast<const char*>(in.p) +
@@ -67,18 +67,18 @@ __device__ __forceinline__ void prep_rows(const PrepArgs& a, const RowsIn& in, c
 }
 
 template <int T, bool kNext, bool kVec>
-__global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constant__ PrepArgs a) {
+__global__ void __launch_bounds__(kPrepThreads, kVec ? 4 : 2) prep_kernel(const __grid_constant__ PrepArgs a) {
   constexpr int kGroups = kPrepThreads / T;
-  __shared__ __align__(16) float cos_t[kTableFloats], sin_t[kTableFloats];
+  __shared__ __align__(16) float cos_t[kTableFloats], sin_t[kTableFloats], s_w[2][128];
   const int b = blockIdx.z, n0 = blockIdx.x * a.tokens;
   const int t = threadIdx.x % T, grp = threadIdx.x / T;
   const int tk = grp % a.tokens, sub = grp / a.tokens, per = kGroups / a.tokens;
   const int n = n0 + tk, rot = a.rope.rot;
   const Place p = place_of<kNext>(t, rot, a.D);
-  if (rot) {
-    fill_tables(a.rope, b, n0, a.tokens, a.N, cos_t, sin_t);
-    __syncthreads();
-  }
+  for (int side = 0; side < 2; ++side)
+    if (a.norm[side].on) stage_weight(a.norm[side], a.D, 128, s_w[side]);
+  if (rot) fill_tables(a.rope, b, n0, a.tokens, a.N, cos_t, sin_t);
+  __syncthreads();
   const int first = blockIdx.y * a.heads, last = first + a.heads;  // of the heads of q, then of k
   int before = 0;
 #pragma unroll 1
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
     if (h0 >= h1) continue;
     Turn f = rot ? rotation<kNext>(cos_t + tk * (rot >> 1), sin_t + tk * (rot >> 1), t, p, rot, 1.0f) : identity();
     const NormArgs& norm = a.norm[side];
-    if (norm.on) fold<kNext>(f, load_weight(norm, p));
+    if (norm.on) fold<kNext>(f, lane_weight<kVec>(s_w[side], p));
     if (in.f32)
       prep_rows<T, kNext, kVec, true>(a, in, a.y[side], b, n, h0, h1, sub, per, norm.on, norm.eps, p, f);
     else
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_kernel(const __grid_constan
 template <int T, bool kNext, bool kVec, bool kXF32, bool kGF32>
 __device__ __forceinline__ void prep_bwd_rows(const PrepBwdArgs& a, int side, int b, int n, int sub, int per,
                                               const Place& p, const Turn& f, const Row& w, Row& dw) {
-  constexpr int U = kXF32 || kGF32 ? 2 : 4;
+  constexpr int U = kVec && !kXF32 && !kGF32 ? 2 : 1;  // rows in flight per group, two reads each
   const RowsIn &dy = a.dy[side], &in = a.x[side];
   const RowsOut& dx = a.dx[side];
   const int norm = a.norm[side].on;
@@ -160,15 +160,17 @@ __device__ __forceinline__ void prep_bwd_rows(const PrepBwdArgs& a, int side, in
 // registers over all of them, and writes one partial row per side; the sums
 // over CTAs follow in a second kernel in a fixed order.
 template <int T, bool kNext, bool kVec>
-__global__ void __launch_bounds__(kPrepThreads) prep_bwd_kernel(const __grid_constant__ PrepBwdArgs a) {
+__global__ void __launch_bounds__(kPrepThreads, kVec ? 3 : 1) prep_bwd_kernel(const __grid_constant__ PrepBwdArgs a) {
   constexpr int kGroups = kPrepThreads / T;
-  __shared__ __align__(16) float cos_t[kTableFloats], sin_t[kTableFloats];
+  __shared__ __align__(16) float cos_t[kTableFloats], sin_t[kTableFloats], s_w[2][128];
   __shared__ float red[kGroups][129];
   const int t = threadIdx.x % T, grp = threadIdx.x / T;
   const int tk = grp % a.tokens, sub = grp / a.tokens, per = kGroups / a.tokens;
   const int rot = a.rope.rot;
   const Place p = place_of<kNext>(t, rot, a.D);
   const int blocks = (a.N + a.tokens - 1) / a.tokens;
+  for (int side = 0; side < 2; ++side) stage_weight(a.norm[side], a.D, 128, s_w[side]);
+  __syncthreads();
   Row dw[2];
 #pragma unroll
   for (int i = 0; i < 4; ++i) dw[0].v[i] = dw[1].v[i] = make_float2(0.0f, 0.0f);
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(kPrepThreads) prep_bwd_kernel(const __grid_con
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       if (a.dy[side].p == nullptr) continue;
-      const Row w = load_weight(a.norm[side], p);
+      const Row w = lane_weight<kVec>(s_w[side], p);
       if (a.x[side].f32) {
         if (a.dy[side].f32)
           prep_bwd_rows<T, kNext, kVec, true, true>(a, side, b, n, sub, per, p, f, w, dw[side]);
@@ -241,11 +243,11 @@ __global__ void __launch_bounds__(1024) prep_dw_kernel(const float* partial, int
 // Lanes a row, for rows that take vector accesses and others.
 int lanes_of(int D, bool vec) { return !vec ? 32 : (D <= 64 ? 8 : 16); }
 
-// Tokens a CTA: four, or more where its groups would outnumber a token's heads.
-int tokens_of(int lanes, int heads) {
-  const int groups = kPrepThreads / lanes;
-  int tokens = 4;
-  while (tokens < groups && groups / tokens > heads) tokens *= 2;
+// Tokens a CTA: one for each of its groups, fewer (and more groups a token)
+// until there are `ctas` CTAs.
+int tokens_of(int lanes, int B, int N, int ctas) {
+  int tokens = kPrepThreads / lanes;
+  while (tokens > 1 && static_cast<int64_t>(B) * ((N + tokens - 1) / tokens) < ctas) tokens /= 2;
   return tokens;
 }
 
@@ -255,15 +257,12 @@ cudaError_t launch_prep(PrepArgs a, int num_sms, cudaStream_t st) {
   const int heads = (a.x[0].p ? a.x[0].H : 0) + (a.x[1].p ? a.x[1].H : 0);
   const bool next = a.rope.rot == 0 || a.rope.interleaved, vec = a.vec && (next || a.rope.rot % 8 == 0);
   const int lanes = lanes_of(a.D, vec);
-  // A few tokens a CTA with all their heads where that fills the GPU; one token
-  // a CTA, and its heads cut into runs of one turn of the groups, where it
-  // does not (a decode step).
-  a.tokens = tokens_of(lanes, heads);
+  // As many tokens a CTA as leave eight CTAs an SM (a group's factors serve all
+  // heads of its token); one token a CTA, and its heads cut into runs of one
+  // turn of the groups, where even that does not (a decode step).
+  a.tokens = tokens_of(lanes, a.B, a.N, 8 * num_sms);
   a.heads = heads;
-  if (static_cast<int64_t>(a.B) * ((a.N + a.tokens - 1) / a.tokens) < 4 * num_sms) {
-    a.tokens = 1;
-    a.heads = kPrepThreads / lanes;
-  }
+  if (static_cast<int64_t>(a.B) * ((a.N + a.tokens - 1) / a.tokens) < 4 * num_sms) a.heads = kPrepThreads / lanes;
   auto kern = !vec          ? (next ? prep_kernel<32, true, false> : prep_kernel<32, false, false>)
               : lanes == 8 ? (next ? prep_kernel<8, true, true> : prep_kernel<8, false, true>)
                             : (next ? prep_kernel<16, true, true> : prep_kernel<16, false, true>);
@@ -273,11 +272,10 @@ cudaError_t launch_prep(PrepArgs a, int num_sms, cudaStream_t st) {
 }
 
 cudaError_t launch_prep_bwd(PrepBwdArgs a, cudaStream_t st) {
-  const int heads = (a.dy[0].p ? a.dy[0].H : 0) + (a.dy[1].p ? a.dy[1].H : 0);
   const bool next = a.rope.rot == 0 || a.rope.interleaved, vec = a.vec && (next || a.rope.rot % 8 == 0);
   const int lanes = lanes_of(a.D, vec);
-  a.tokens = tokens_of(lanes, heads);
-  if (static_cast<int64_t>(a.B) * ((a.N + a.tokens - 1) / a.tokens) < kPrepBwdMaxCtas) a.tokens = 1;
+  // ten items a CTA, so that the last round is short, or one token an item
+  a.tokens = tokens_of(lanes, a.B, a.N, 10 * kPrepBwdMaxCtas);
   const int64_t items = static_cast<int64_t>(a.B) * ((a.N + a.tokens - 1) / a.tokens);
   const int ctas = static_cast<int>(items < kPrepBwdMaxCtas ? items : kPrepBwdMaxCtas);
   auto kern = !vec          ? (next ? prep_bwd_kernel<32, true, false> : prep_bwd_kernel<32, false, false>)
