@@ -158,9 +158,10 @@ struct PrepBwdArgs {
   float* partial;     // [CTAs][2][D]
 };
 // CTAs of the backward pass at most: its partial weight gradients are summed
-// over them, so the bound fixes the workspace (and the order of the sum) on
-// every device.  Three a B200's SM.
-constexpr int kPrepBwdMaxCtas = 444;
+// over them, so the bound fixes the workspace (2 MB) and the order of the sum
+// on every device.  Four rounds of three CTAs an SM, so that the last round's
+// idle share is small.
+constexpr int kPrepBwdMaxCtas = 2048;
 cudaError_t launch_prep_bwd(PrepBwdArgs a, cudaStream_t stream);
 
 struct AppendArgs {

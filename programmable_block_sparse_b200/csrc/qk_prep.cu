@@ -218,25 +218,25 @@ __global__ void __launch_bounds__(kPrepThreads, kVec ? 3 : 1) prep_bwd_kernel(co
   }
 }
 
-// dw[side][e] = sum over CTAs of partial[cta][side][e]: 32 columns a block, 32
-// threads a column, each over every 32nd CTA, joined in a fixed order.
+// dw[side][e] = sum over CTAs of partial[cta][side][e]: 8 columns a block, 128
+// threads a column, each over every 128th CTA, joined in a fixed order.
 __global__ void __launch_bounds__(1024) prep_dw_kernel(const float* partial, int ctas, int D, float* dq, float* dk) {
-  __shared__ float red[32][33];
-  const int side = blockIdx.y, e = blockIdx.x * 32 + (threadIdx.x & 31), sl = threadIdx.x >> 5;
+  __shared__ float red[128][9];
+  const int side = blockIdx.y, col = threadIdx.x & 7, e = blockIdx.x * 8 + col, sl = threadIdx.x >> 3;
   float* out = side ? dk : dq;
   if (out == nullptr) return;
   float v = 0.0f;
   if (e < D) {
-#pragma unroll 4
-    for (int cta = sl; cta < ctas; cta += 32) v += partial[(static_cast<int64_t>(cta) * 2 + side) * D + e];
+#pragma unroll 16
+    for (int cta = sl; cta < ctas; cta += 128) v += partial[(static_cast<int64_t>(cta) * 2 + side) * D + e];
   }
-  red[sl][threadIdx.x & 31] = v;
+  red[sl][col] = v;
   __syncthreads();
-  if (sl == 0 && e < D) {
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) sum += red[i][threadIdx.x];
-    out[e] = sum;
+  if (threadIdx.x < 256) {  // one warp a column: four values a lane, then a tree
+    const int c = threadIdx.x >> 5, l = threadIdx.x & 31;
+    float sum = (red[l][c] + red[l + 32][c]) + (red[l + 64][c] + red[l + 96][c]);
+    sum = row_sum<32>(sum);
+    if (l == 0 && blockIdx.x * 8 + c < D) out[blockIdx.x * 8 + c] = sum;
   }
 }
 
@@ -274,8 +274,7 @@ cudaError_t launch_prep(PrepArgs a, int num_sms, cudaStream_t st) {
 cudaError_t launch_prep_bwd(PrepBwdArgs a, cudaStream_t st) {
   const bool next = a.rope.rot == 0 || a.rope.interleaved, vec = a.vec && (next || a.rope.rot % 8 == 0);
   const int lanes = lanes_of(a.D, vec);
-  // ten items a CTA, so that the last round is short, or one token an item
-  a.tokens = tokens_of(lanes, a.B, a.N, 10 * kPrepBwdMaxCtas);
+  a.tokens = tokens_of(lanes, a.B, a.N, kPrepBwdMaxCtas / 2);
   const int64_t items = static_cast<int64_t>(a.B) * ((a.N + a.tokens - 1) / a.tokens);
   const int ctas = static_cast<int>(items < kPrepBwdMaxCtas ? items : kPrepBwdMaxCtas);
   auto kern = !vec          ? (next ? prep_bwd_kernel<32, true, false> : prep_bwd_kernel<32, false, false>)
@@ -284,7 +283,7 @@ cudaError_t launch_prep_bwd(PrepBwdArgs a, cudaStream_t st) {
   kern<<<ctas, kPrepThreads, 0, st>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (a.dw[0] == nullptr && a.dw[1] == nullptr)) return e;
-  prep_dw_kernel<<<dim3((a.D + 31) / 32, 2), 1024, 0, st>>>(a.partial, ctas, a.D, a.dw[0], a.dw[1]);
+  prep_dw_kernel<<<dim3((a.D + 7) / 8, 2), 1024, 0, st>>>(a.partial, ctas, a.D, a.dw[0], a.dw[1]);
   return cudaGetLastError();
 }
 
