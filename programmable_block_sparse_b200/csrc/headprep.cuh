@@ -88,6 +88,38 @@ __device__ __forceinline__ void load_raw(const void* row, const Place& p, Raw<kV
   }
 }
 
+// The same through shared memory: a lane copies its own two pieces into its own
+// slot (16 bytes of bf16 or 32 of fp32) and reads them back itself, so the
+// only wait is for its own copies, and rows in flight cost no registers.
+template <bool kF32>
+__device__ __forceinline__ void copy_raw(uint32_t slot, const void* row, const Place& p, bool valid) {
+  constexpr int kPiece = kF32 ? 16 : 8;
+  const int bytes = valid && p.na ? kPiece : 0;  // 0: the slot is filled with zeros
+  const char* src = static_cast<const char*>(row);
+  const char *a = bytes ? src + p.a * (kPiece / 4) : src, *b = bytes ? src + p.b * (kPiece / 4) : src;
+  if constexpr (kF32) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot), "l"(a), "r"(bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + 16), "l"(b), "r"(bytes) : "memory");
+  } else {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(slot), "l"(a), "r"(bytes) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(slot + 8), "l"(b), "r"(bytes) : "memory");
+  }
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+template <bool kF32>
+__device__ __forceinline__ void read_raw(uint32_t slot, Raw<true, kF32>& r) {
+#pragma unroll
+  for (int w = 0; w < (kF32 ? 2 : 1); ++w)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.u[4 * w]), "=r"(r.u[4 * w + 1]), "=r"(r.u[4 * w + 2]), "=r"(r.u[4 * w + 3])
+                 : "r"(slot + 16 * w)
+                 : "memory");
+}
+
 // The pieces as pairs of fp32: a = v[0], v[1], b = v[2], v[3].
 struct Row {
   float2 v[4];
