@@ -16,9 +16,10 @@
 namespace fa {
 namespace {
 
-// A CTA has 16 groups of 16 lanes, 32 of 8, or 32 warps for rows read one
-// element at a time.
-constexpr int threads_of(int T) { return T == 32 ? 1024 : 256; }
+// A CTA has 32 groups: of 8 lanes, or whole warps for rows read one element at
+// a time.
+constexpr int kGroups = 32;
+constexpr int threads_of(int T) { return kGroups * T; }
 constexpr int kMaxChunk = 128;
 
 // 2^ceil(log2(amax / 448)) from the bits of a finite amax >= 0; 0 for 0.
@@ -66,13 +67,13 @@ __device__ __forceinline__ Span append_span(const AppendArgs& a, int b) {
 }
 
 // The new rows of a group (n0, n0 + groups, ... below count) of one head; 0 elsewhere.
-template <int T, bool kVec, bool kF32, int kIters>
+template <int P, bool kVec, bool kF32, int kIters>
 __device__ __forceinline__ void load_rows(const RowsIn& in, int64_t off, int n0, int count, const Place& p,
-                                          Row (&x)[kIters]) {
-  Raw<kVec, kF32> raw[kIters];
+                                          Row<P> (&x)[kIters]) {
+  Raw<P, kVec, kF32> raw[kIters];
 #pragma unroll
   for (int it = 0; it < kIters; ++it) {
-    const int n = n0 + it * (threads_of(T) / T);
+    const int n = n0 + it * kGroups;
     if (n >= 0 && n < count)
       load_raw(row_ptr(in.p, kF32, off + n * in.stride[2]), p, raw[it]);
     else
@@ -83,16 +84,15 @@ __device__ __forceinline__ void load_rows(const RowsIn& in, int64_t off, int n0,
 }
 
 // Queries of ntok tokens from n0 on and nh heads from hq0 on.
-template <int T, bool kNext, bool kVec, bool kF32>
+template <int T, int P, bool kNext, bool kVec, bool kF32>
 __device__ __forceinline__ void append_queries(const AppendArgs& a, int b, int n0, int ntok, int hq0, int nh,
                                                const float* cos_t, const float* sin_t, const float* s_w) {
-  constexpr int kGroups = threads_of(T) / T;
   constexpr int U = 2;
   const int t = threadIdx.x % T, grp = threadIdx.x / T, rot = a.rope.rot;
-  const Place p = place_of<kNext>(t, rot, a.E);
+  const Place p = place_of<P, kNext>(t, rot, a.E);
   const int rows = ntok * nh;
   for (int r0 = 0; r0 < rows; r0 += U * kGroups) {
-    Raw<kVec, kF32> raw[U];
+    Raw<P, kVec, kF32> raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int r = min(r0 + u * kGroups + grp, rows - 1), n = n0 + r % ntok, h = hq0 + r / ntok;
@@ -103,12 +103,12 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, int b, int n
     for (int u = 0; u < U; ++u) {
       if (r0 + u * kGroups >= rows) break;  // the same for the whole CTA
       const int r = min(r0 + u * kGroups + grp, rows - 1), tk = r % ntok, n = n0 + tk, h = hq0 + r / ntok;
-      Row x = unpack(raw[u]);
+      Row<P> x = unpack(raw[u]);
       if (a.q_norm.on)
         x = product(scaled(x, norm_factor<T>(x, a.q_norm.eps, 1.0f / static_cast<float>(a.E))),
-                    lane_weight<kVec>(s_w, p));
+                    lane_weight<kVec, P>(s_w, p));
       if (rot)
-        x = apply<kNext>(x, rotation<kNext>(cos_t + tk * (rot >> 1), sin_t + tk * (rot >> 1), t, p, rot, 1.0f), p, rot,
+        x = apply<kNext>(x, rotation<kNext, P>(cos_t + tk * (rot >> 1), sin_t + tk * (rot >> 1), t, rot, 1.0f), p, rot,
                          a.E);
       if (r0 + u * kGroups + grp < rows)
         store_row<kVec>(row_ptr(a.q_out.p, a.q_out.f32,
@@ -119,9 +119,9 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, int b, int n
 }
 
 // kVec: of the inputs; kCVec: rows of the cache take whole pieces.
-template <int T, bool kNext, bool kVec, int kIters>
+template <int T, int P, bool kNext, bool kVec, int kIters>
 __global__ void __launch_bounds__(threads_of(T)) append_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int kThreads = threads_of(T), kGroups = kThreads / T;
+  constexpr int kThreads = threads_of(T);
   extern __shared__ __align__(16) float tables[];  // cosines, then sines, of the chunk's tokens
   __shared__ __align__(16) float s_w[128];
   __shared__ int s_outer[kMaxChunk];
@@ -155,9 +155,9 @@ __global__ void __launch_bounds__(threads_of(T)) append_kernel(const __grid_cons
     if (rot) fill(n0, ntok, 0);
     if (a.q_norm.on) stage_weight(a.q_norm, a.E, 128, s_w);
     if (a.q.f32)
-      append_queries<T, kNext, kVec, true>(a, b, n0, ntok, hq0, nh, cos_t, sin_t, s_w);
+      append_queries<T, P, kNext, kVec, true>(a, b, n0, ntok, hq0, nh, cos_t, sin_t, s_w);
     else
-      append_queries<T, kNext, kVec, false>(a, b, n0, ntok, hq0, nh, cos_t, sin_t, s_w);
+      append_queries<T, P, kNext, kVec, false>(a, b, n0, ntok, hq0, nh, cos_t, sin_t, s_w);
     return;
   }
 
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(threads_of(T)) append_kernel(const __grid_cons
   const int D = is_k ? a.E : a.Ev;
   const RowsIn& in = is_k ? a.k : a.v;
   const bool turn = is_k && rot, norm = is_k && a.k_norm.on;
-  const Place p = place_of<kNext>(t, is_k ? rot : 0, D);
+  const Place p = place_of<P, kNext>(t, is_k ? rot : 0, D);
   // page (or sequence) of each slot of the chunk that the call touches; -1: none
   for (int i = threadIdx.x; i < a.chunk; i += kThreads) {
     const int slot = slot0 + i;
@@ -202,27 +202,27 @@ __global__ void __launch_bounds__(threads_of(T)) append_kernel(const __grid_cons
   const bool cvec = is_k ? a.kc_vec : a.vc_vec;
 
   for (int h = run * a.k_heads; h < min((run + 1) * a.k_heads, in.H); ++h) {
-    Row x[kIters];
+    Row<P> x[kIters];
     const int64_t head_off = b * in.stride[0] + h * in.stride[1];
     if (in.f32)
-      load_rows<T, kVec, true, kIters>(in, head_off, slot0 - sp.start + grp, sp.count, p, x);
+      load_rows<P, kVec, true, kIters>(in, head_off, slot0 - sp.start + grp, sp.count, p, x);
     else
-      load_rows<T, kVec, false, kIters>(in, head_off, slot0 - sp.start + grp, sp.count, p, x);
+      load_rows<P, kVec, false, kIters>(in, head_off, slot0 - sp.start + grp, sp.count, p, x);
     if (threadIdx.x < 32) s_amax[threadIdx.x] = 0u;
     __syncthreads();  // also: the previous head's scales have been read, and the tables are filled
 #pragma unroll
     for (int it = 0; it < kIters; ++it) {
       const int row = it * kGroups + grp;
       if (norm) x[it] = product(scaled(x[it], norm_factor<T>(x[it], a.k_norm.eps, 1.0f / static_cast<float>(D))),
-                                  lane_weight<kVec>(s_w, p));
+                                  lane_weight<kVec, P>(s_w, p));
       if (turn)
-        x[it] = apply<kNext>(x[it], rotation<kNext>(cos_t + row * h2, sin_t + row * h2, t, p, rot, 1.0f), p, rot, D);
+        x[it] = apply<kNext>(x[it], rotation<kNext, P>(cos_t + row * h2, sin_t + row * h2, t, rot, 1.0f), p, rot, D);
       if (e4m3) {
         float m = 0.0f;  // of this row's finite magnitudes (rows without a new token: 0)
         const int n = slot0 + row - sp.start;
         if (n >= 0 && n < sp.count) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < P; ++i) {
             const float u = fabsf(x[it].v[i].x), v = fabsf(x[it].v[i].y);
             m = fmaxf(m, fmaxf(u < INFINITY ? u : 0.0f, v < INFINITY ? v : 0.0f));
           }
@@ -269,31 +269,34 @@ __global__ void __launch_bounds__(threads_of(T)) append_kernel(const __grid_cons
       }
       const float now = s_scale[row >> sb_log], inv = now > 0.0f ? 1.0f / now : 0.0f;
       uint8_t* dst = reinterpret_cast<uint8_t*>(cache) + off;
-      Row y;
+      Row<P> y;
       if (slot >= sp.start) {
         y = scaled(x[it], inv);
       } else {
         // an older token of a block: rounded again where its scale grew
         const float old = s_old[row >> sb_log];
         if (!(now > old)) continue;
-        float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          v[i] = (i & 3) < (i < 4 ? p.na : p.nb) ? e4m3_value(dst[i < 4 ? p.a + i : p.b + i - 4]) * (old * inv) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y.v[i] = make_float2(v[2 * i], v[2 * i + 1]);
+        for (int i = 0; i < 2 * P; ++i)
+          put(y, i, has<P>(p, i) ? e4m3_value(dst[element<P>(p, i)]) * (old * inv) : 0.0f);
       }
-      const uint32_t ca = e4m3x4(y.v[0], y.v[1]), cb = e4m3x4(y.v[2], y.v[3]);
+      uint32_t code[P / 2];
+#pragma unroll
+      for (int i = 0; i < P / 2; ++i) code[i] = e4m3x4(y.v[2 * i], y.v[2 * i + 1]);
       if (kVec && cvec) {
-        if (p.na) {
-          *reinterpret_cast<uint32_t*>(dst + p.a) = ca;
-          *reinterpret_cast<uint32_t*>(dst + p.b) = cb;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if (!(q ? p.nb : p.na)) continue;
+          uint8_t* d = dst + (q ? p.b : p.a);
+          if constexpr (P == 8)
+            *reinterpret_cast<uint2*>(d) = make_uint2(code[2 * q], code[2 * q + 1]);
+          else
+            *reinterpret_cast<uint32_t*>(d) = code[q];
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if ((i & 3) < (i < 4 ? p.na : p.nb))
-            dst[i < 4 ? p.a + i : p.b + i - 4] = static_cast<uint8_t>((i < 4 ? ca : cb) >> (8 * (i & 3)));
+        for (int i = 0; i < 2 * P; ++i)
+          if (has<P>(p, i)) dst[element<P>(p, i)] = static_cast<uint8_t>(code[i >> 2] >> (8 * (i & 3)));
       }
     }
     __syncthreads();  // the scales are read before the next head's maxima are cleared
@@ -301,12 +304,11 @@ __global__ void __launch_bounds__(threads_of(T)) append_kernel(const __grid_cons
 }
 
 // The kernel for a row layout and a chunk.
-template <int T, bool kNext, bool kVec>
+template <int T, int P, bool kNext, bool kVec>
 cudaError_t launch_append_t(const AppendArgs& a, dim3 grid, size_t smem, cudaStream_t st) {
-  constexpr int kUnit = T == 16 ? 2 : 1;  // turns of the CTA's groups over 32 slots
-  auto kern = a.chunk == 32   ? append_kernel<T, kNext, kVec, kUnit>
-              : a.chunk == 64 ? append_kernel<T, kNext, kVec, 2 * kUnit>
-                              : append_kernel<T, kNext, kVec, 4 * kUnit>;
+  auto kern = a.chunk == 32   ? append_kernel<T, P, kNext, kVec, 1>
+              : a.chunk == 64 ? append_kernel<T, P, kNext, kVec, 2>
+                              : append_kernel<T, P, kNext, kVec, 4>;
   if (smem > 40 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
@@ -319,9 +321,7 @@ cudaError_t launch_append_t(const AppendArgs& a, dim3 grid, size_t smem, cudaStr
 
 cudaError_t launch_append(AppendArgs a, int num_sms, cudaStream_t st) {
   const bool next = a.rope.rot == 0 || a.rope.interleaved;
-  const bool vec = a.k_vec && a.v_vec && (!a.q.p || a.q_vec) && (next || a.rope.rot % 8 == 0);
-  const int lanes = !vec ? 32 : (a.E <= 64 && a.Ev <= 64 ? 8 : 16);
-  const int groups = threads_of(lanes) / lanes;
+  const Layout l = layout_of(a.E > a.Ev ? a.E : a.Ev, a.rope.rot, next, a.k_vec && a.v_vec && (!a.q.p || a.q_vec), 8);
   a.chunk = a.dtype == FA_DTYPE_E4M3 && a.scale_block > 32 ? a.scale_block : 32;
   // N tokens that start anywhere in a chunk touch this many chunks at most
   const int chunks = static_cast<int>((static_cast<int64_t>(a.N) + a.chunk - 2) / a.chunk) + 1;
@@ -331,16 +331,19 @@ cudaError_t launch_append(AppendArgs a, int num_sms, cudaStream_t st) {
   a.k_heads = 1;
   while (2 * a.k_heads <= a.k.H && per_head * (a.k.H / (2 * a.k_heads)) >= 4 * num_sms) a.k_heads *= 2;
   const int ntok = a.N < a.chunk ? a.N : a.chunk;
-  a.q_heads = ntok < groups ? (groups + ntok - 1) / ntok : 8;
+  a.q_heads = ntok < kGroups ? (kGroups + ntok - 1) / ntok : 8;
   const int kv_runs = (a.k.H + a.k_heads - 1) / a.k_heads;
   const int q_runs = a.q.p ? (a.q.H + a.q_heads - 1) / a.q_heads : 0;
   const dim3 grid(chunks, 2 * kv_runs + q_runs, a.B);
   const size_t smem = static_cast<size_t>(a.chunk) * (a.rope.rot / 2) * 2 * sizeof(float);
-  if (lanes == 32)
-    return next ? launch_append_t<32, true, false>(a, grid, smem, st) : launch_append_t<32, false, false>(a, grid, smem, st);
-  if (lanes == 8)
-    return next ? launch_append_t<8, true, true>(a, grid, smem, st) : launch_append_t<8, false, true>(a, grid, smem, st);
-  return next ? launch_append_t<16, true, true>(a, grid, smem, st) : launch_append_t<16, false, true>(a, grid, smem, st);
+  if (!l.vec)
+    return next ? launch_append_t<32, 4, true, false>(a, grid, smem, st)
+                : launch_append_t<32, 4, false, false>(a, grid, smem, st);
+  if (l.P == 8)
+    return next ? launch_append_t<8, 8, true, true>(a, grid, smem, st)
+                : launch_append_t<8, 8, false, true>(a, grid, smem, st);
+  return next ? launch_append_t<8, 4, true, true>(a, grid, smem, st)
+              : launch_append_t<8, 4, false, true>(a, grid, smem, st);
 }
 
 }  // namespace fa

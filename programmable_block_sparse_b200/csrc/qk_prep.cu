@@ -14,7 +14,6 @@ namespace fa {
 namespace {
 
 constexpr int kPrepThreads = 256;
-constexpr int kTableFloats = 16 * 64;  // tokens of a CTA x rot / 2, at most: 16 x 64 or 32 x 32
 
 // cos / sin tables of tokens n0 .. n0 + count - 1 (the caller synchronises).
 __device__ __forceinline__ void fill_tables(const RopeArgs& r, int b, int n0, int count, int N, float* cos_t,
@@ -31,10 +30,10 @@ __device__ __forceinline__ void fill_tables(const RopeArgs& r, int b, int n0, in
 
 // The heads h0 .. h1 - 1 of one side for this group's token.  Every lane of a
 // warp takes the same number of turns (shuffles).
-template <int T, bool kNext, bool kVec, bool kF32>
+template <int T, int P, bool kNext, bool kVec, bool kF32>
 __device__ __forceinline__ void prep_rows(const PrepArgs& a, const RowsIn& in, const RowsOut& out, int b, int n, int h0,
                                           int h1, int sub, int per, int norm, float eps, const Place& p,
-                                          const Turn& f) {
+                                          const Turn<P>& f) {
   constexpr int U = kVec && !kF32 ? 4 : 2;  // rows in flight per group
   const float inv_d = 1.0f / static_cast<float>(a.D);
   const bool here = n < a.N;
@@ -45,7 +44,7 @@ __device__ __forceinline__ void prep_rows(const PrepArgs& a, const RowsIn& in, c
              (b * out.stride[0] + n * out.stride[2] + (h0 + sub) * out.stride[1]) * (out.f32 ? 4 : 2);
   const int64_t ostep = out.stride[1] * per * (out.f32 ? 4 : 2);
   for (int hb = h0; hb < h1; hb += per * U) {
-    Raw<kVec, kF32> raw[U];
+    Raw<P, kVec, kF32> raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (here && hb + sub + u * per < h1)
@@ -56,8 +55,8 @@ __device__ __forceinline__ void prep_rows(const PrepArgs& a, const RowsIn& in, c
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (hb + u * per >= h1) break;  // the same for the whole CTA
-      const Row x = unpack(raw[u]);
-      Row y = apply<kNext>(x, f, p, a.rope.rot, a.D);
+      const Row<P> x = unpack(raw[u]);
+      Row<P> y = apply<kNext>(x, f, p, a.rope.rot, a.D);
       if (norm) y = scaled(y, norm_factor<T>(x, eps, inv_d));
       if (here && hb + sub + u * per < h1) store_row<kVec>(op + u * ostep, out.f32, p, y);
     }
@@ -66,15 +65,19 @@ __device__ __forceinline__ void prep_rows(const PrepArgs& a, const RowsIn& in, c
   }
 }
 
-template <int T, bool kNext, bool kVec>
+// A CTA takes a block of tokens (one for each group of T lanes, or several
+// groups a token) and a run of the heads of q and then k.
+template <int T, int P, bool kNext, bool kVec>
 __global__ void __launch_bounds__(kPrepThreads, kVec ? 4 : 2) prep_kernel(const __grid_constant__ PrepArgs a) {
   constexpr int kGroups = kPrepThreads / T;
-  __shared__ __align__(16) float cos_t[kTableFloats], sin_t[kTableFloats], s_w[2][128];
+  extern __shared__ __align__(16) float tables[];  // cosines, then sines, of the CTA's tokens
+  __shared__ __align__(16) float s_w[2][128];
   const int b = blockIdx.z, n0 = blockIdx.x * a.tokens;
   const int t = threadIdx.x % T, grp = threadIdx.x / T;
   const int tk = grp % a.tokens, sub = grp / a.tokens, per = kGroups / a.tokens;
   const int n = n0 + tk, rot = a.rope.rot;
-  const Place p = place_of<kNext>(t, rot, a.D);
+  float *cos_t = tables, *sin_t = tables + a.tokens * (rot >> 1);
+  const Place p = place_of<P, kNext>(t, rot, a.D);
   for (int side = 0; side < 2; ++side)
     if (a.norm[side].on) stage_weight(a.norm[side], a.D, 128, s_w[side]);
   if (rot) fill_tables(a.rope, b, n0, a.tokens, a.N, cos_t, sin_t);
@@ -88,54 +91,57 @@ __global__ void __launch_bounds__(kPrepThreads, kVec ? 4 : 2) prep_kernel(const 
     const int h0 = max(first - before, 0), h1 = min(last - before, in.H);
     before += in.H;
     if (h0 >= h1) continue;
-    Turn f = rot ? rotation<kNext>(cos_t + tk * (rot >> 1), sin_t + tk * (rot >> 1), t, p, rot, 1.0f) : identity();
+    Turn<P> f = rot ? rotation<kNext, P>(cos_t + tk * (rot >> 1), sin_t + tk * (rot >> 1), t, rot, 1.0f) : identity<P>();
     const NormArgs& norm = a.norm[side];
-    if (norm.on) fold<kNext>(f, lane_weight<kVec>(s_w[side], p));
+    if (norm.on) fold<kNext>(f, lane_weight<kVec, P>(s_w[side], p));
     if (in.f32)
-      prep_rows<T, kNext, kVec, true>(a, in, a.y[side], b, n, h0, h1, sub, per, norm.on, norm.eps, p, f);
+      prep_rows<T, P, kNext, kVec, true>(a, in, a.y[side], b, n, h0, h1, sub, per, norm.on, norm.eps, p, f);
     else
-      prep_rows<T, kNext, kVec, false>(a, in, a.y[side], b, n, h0, h1, sub, per, norm.on, norm.eps, p, f);
+      prep_rows<T, P, kNext, kVec, false>(a, in, a.y[side], b, n, h0, h1, sub, per, norm.on, norm.eps, p, f);
   }
 }
 
+// A thread's walk over its token's heads of one tensor, every `per`-th from
+// sub on: the two pieces of its next row.
+struct Walk {
+  const char *a, *b;
+  int64_t step;
+  int head, end, left;  // next head; turns left (the same for the whole CTA)
+};
+__device__ __forceinline__ Walk walk_of(const RowsIn& in, const Place& p, int b, int n, int N, int sub, int per) {
+  const int el = in.f32 ? 4 : 2;
+  Walk w;
+  w.end = in.p ? in.H : 0;
+  w.left = (w.end + per - 1) / per;
+  w.head = n < N ? sub : w.end;  // a token past the end has no heads
+  const char* row = static_cast<const char*>(in.p) + (b * in.stride[0] + n * in.stride[2] + sub * in.stride[1]) * el;
+  w.a = row + p.a * el;
+  w.b = row + p.b * el;
+  w.step = in.stride[1] * per * el;
+  return w;
+}
+// Bytes of one row's slots over a CTA's threads.
+constexpr int slot_bytes(int P, bool f32) { return kPrepThreads * 2 * P * (f32 ? 4 : 2); }
+
 // One row's gradient: y, the output gradient turned back, becomes the input
 // gradient, and dw takes its share of the weight gradient.
-template <int T>
-__device__ __forceinline__ void norm_gradient(Row& y, const Row& x, const Row& w, float eps, float inv_d, Row& dw) {
-  const Row yw = product(y, w);
-  float ss = dot8(x, x), sd = dot8(yw, x);
+template <int T, int P>
+__device__ __forceinline__ void norm_gradient(Row<P>& y, const Row<P>& x, const Row<P>& w, float eps, float inv_d,
+                                              Row<P>& dw) {
+  const Row<P> yw = product(y, w);
+  float ss = dot(x, x), sd = dot(yw, x);
 #pragma unroll
   for (int o = T / 2; o > 0; o >>= 1) {
     ss += __shfl_xor_sync(0xffffffffu, ss, o);
     sd += __shfl_xor_sync(0xffffffffu, sd, o);
   }
   const float r = rsqrtf(ss * inv_d + eps), k = sd * inv_d * r * r;
-  const Row xr = scaled(x, r);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    dw.v[i] = fma2(y.v[i], xr.v[i], dw.v[i]);
-    y.v[i] = fma2(splat2(-k), xr.v[i], mul2(yw.v[i], splat2(r)));
+  for (int i = 0; i < P; ++i) {
+    const float2 xr = mul2(x.v[i], splat2(r));
+    dw.v[i] = fma2(y.v[i], xr, dw.v[i]);
+    y.v[i] = fma2(splat2(-k), xr, mul2(yw.v[i], splat2(r)));
   }
-}
-
-// What one thread walks in a work item: its token's heads of one side, every
-// `per`-th from `sub` on.
-struct HeadWalk {
-  const char *g, *x;  // first head's rows
-  int64_t gstep, xstep;
-  int heads, turns;
-};
-__device__ __forceinline__ HeadWalk walk_of(const PrepBwdArgs& a, int side, int b, int n, int sub, int per) {
-  const RowsIn &dy = a.dy[side], &in = a.x[side];
-  const int ge = dy.f32 ? 4 : 2, xe = in.f32 ? 4 : 2;
-  HeadWalk w;
-  w.heads = dy.p ? dy.H : 0;
-  w.turns = (w.heads + per - 1) / per;
-  w.g = static_cast<const char*>(dy.p) + (b * dy.stride[0] + n * dy.stride[2] + sub * dy.stride[1]) * ge;
-  w.x = static_cast<const char*>(in.p) + (b * in.stride[0] + n * in.stride[2] + sub * in.stride[1]) * xe;
-  w.gstep = dy.stride[1] * per * ge;
-  w.xstep = in.stride[1] * per * xe;
-  return w;
 }
 
 // Gradients.  A CTA walks work items (a token block of one sequence) with a
@@ -145,94 +151,111 @@ __device__ __forceinline__ HeadWalk walk_of(const PrepBwdArgs& a, int side, int 
 // A row takes two reads, so the walk over q's heads and then k's keeps
 // kStages - 1 rows a lane in flight through shared memory (copy_raw).  Rows
 // that are read one element at a time go without.
-template <int T, bool kNext, bool kVec, bool kXF32, bool kGF32>
-__global__ void __launch_bounds__(kPrepThreads, kVec ? 3 : 1) prep_bwd_kernel(const __grid_constant__ PrepBwdArgs a) {
+constexpr int kBwdStages = 4;
+
+template <int T, int P, bool kNext, bool kVec, bool kXF32, bool kGF32>
+__global__ void __launch_bounds__(kPrepThreads, kVec ? 3 : 1)
+    prep_bwd_kernel(const __grid_constant__ PrepBwdArgs a) {
   constexpr int kGroups = kPrepThreads / T;
-  constexpr int kStages = 5;
-  constexpr int kXSlot = kXF32 ? 32 : 16, kGSlot = kGF32 ? 32 : 16;
-  constexpr int kStageBytes = kPrepThreads * (kXSlot + kGSlot);
-  extern __shared__ __align__(16) uint8_t ring[];  // kVec: kStages x (g slots, x slots)
-  __shared__ __align__(16) float cos_t[kTableFloats], sin_t[kTableFloats], s_w[2][128];
+  constexpr int kStages = kBwdStages;
+  constexpr int kXOffset = slot_bytes(P, kGF32), kStageBytes = kXOffset + slot_bytes(P, kXF32);  // g's slots, x's
+  // kVec: kStages stages; then cosines and sines of the CTA's tokens
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  __shared__ __align__(16) float s_w[2][128];
   __shared__ float red[2][kGroups][129];
   const int t = threadIdx.x % T, grp = threadIdx.x / T;
   const int tk = grp % a.tokens, sub = grp / a.tokens, per = kGroups / a.tokens;
   const int rot = a.rope.rot;
-  const Place p = place_of<kNext>(t, rot, a.D);
+  float* cos_t = reinterpret_cast<float*>(dynamic + (kVec ? kStages * kStageBytes : 0));
+  float* sin_t = cos_t + a.tokens * (rot >> 1);
+  const Place p = place_of<P, kNext>(t, rot, a.D);
   const float inv_d = 1.0f / static_cast<float>(a.D);
   const int blocks = (a.N + a.tokens - 1) / a.tokens;
   for (int side = 0; side < 2; ++side) stage_weight(a.norm[side], a.D, 128, s_w[side]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i)  // each lane clears, and later adds to, its own places
-    if ((i & 3) < (i < 4 ? p.na : p.nb)) red[0][grp][i < 4 ? p.a + i : p.b + i - 4] = red[1][grp][i < 4 ? p.a + i : p.b + i - 4] = 0.0f;
-  const uint32_t my_g = kVec ? smem_u32(ring) + threadIdx.x * kGSlot : 0;
-  const uint32_t my_x = kVec ? smem_u32(ring) + kPrepThreads * kGSlot + threadIdx.x * kXSlot : 0;
+  for (int i = 0; i < 2 * P; ++i)  // each lane clears, and later adds to, its own places
+    if (has<P>(p, i)) red[0][grp][element<P>(p, i)] = red[1][grp][element<P>(p, i)] = 0.0f;
+  const uint32_t mine = kVec ? smem_u32(dynamic) + threadIdx.x * 16 : 0;
   __syncthreads();
   for (int64_t item = blockIdx.x; item < static_cast<int64_t>(blocks) * a.B; item += gridDim.x) {
     const int b = static_cast<int>(item / blocks), n0 = static_cast<int>(item % blocks) * a.tokens, n = n0 + tk;
-    const bool here = n < a.N;
-    const HeadWalk w0 = walk_of(a, 0, b, n, sub, per), w1 = walk_of(a, 1, b, n, sub, per);
-    const int turns = w0.turns + w1.turns;  // the same for the whole CTA
-    auto issue = [&](int i, int stage) {
-      if (i < turns) {
-        const bool second = i >= w0.turns;
-        const HeadWalk& w = second ? w1 : w0;
-        const int k = second ? i - w0.turns : i;
-        const bool ok = here && sub + k * per < w.heads;
-        copy_raw<kGF32>(my_g + stage * kStageBytes, w.g + k * w.gstep, p, ok);
-        copy_raw<kXF32>(my_x + stage * kStageBytes, w.x + k * w.xstep, p, ok && a.norm[second].on);
+    // the copies run ahead of the arithmetic, from one side into the next
+    Walk ag = walk_of(a.dy[0], p, b, n, a.N, sub, per);
+    Walk ax = walk_of(a.x[0], p, b, n, a.N, sub, per);  // no rows without a norm
+    bool second = false;
+    uint32_t fill = mine;
+    auto issue = [&]() {
+      if (ag.left <= 0 && !second) {
+        ag = walk_of(a.dy[1], p, b, n, a.N, sub, per);
+        ax = walk_of(a.x[1], p, b, n, a.N, sub, per);
+        second = true;
+      }
+      if (ag.left > 0) {
+        copy_raw<P, kGF32, kPrepThreads>(fill, ag.a, ag.b, p, ag.head < ag.end);
+        copy_raw<P, kXF32, kPrepThreads>(fill + kXOffset, ax.a, ax.b, p, ag.head < ax.end);
+        ag.a += ag.step;
+        ag.b += ag.step;
+        ax.a += ax.step;
+        ax.b += ax.step;
+        ag.head += per;
+        --ag.left;
       }
       copy_commit();
+      fill = fill == mine + (kStages - 1) * kStageBytes ? mine : fill + kStageBytes;
     };
     if constexpr (kVec) {
-#pragma unroll
-      for (int i = 0; i < kStages - 1; ++i) issue(i, i);
+#pragma unroll 1
+      for (int i = 0; i < kStages - 1; ++i) issue();
     }
-    Turn f = identity();
+    Turn<P> f = identity<P>();
     if (rot) {
       __syncthreads();  // the tables of the previous item have been read
       fill_tables(a.rope, b, n0, a.tokens, a.N, cos_t, sin_t);
       __syncthreads();
-      f = rotation<kNext>(cos_t + tk * (rot >> 1), sin_t + tk * (rot >> 1), t, p, rot, -1.0f);
+      f = rotation<kNext, P>(cos_t + tk * (rot >> 1), sin_t + tk * (rot >> 1), t, rot, -1.0f);
     }
-    int stage = 0;
+    uint32_t take = mine;
 #pragma unroll 1
     for (int side = 0; side < 2; ++side) {
-      const HeadWalk& wk = side ? w1 : w0;
-      if (wk.turns == 0) continue;
-      const int norm = a.norm[side].on, before = side ? w0.turns : 0;
+      if (a.dy[side].p == nullptr) continue;
+      const int norm = a.norm[side].on, heads = a.dy[side].H, turns = (heads + per - 1) / per;
       const float eps = a.norm[side].eps;
-      const Row w = lane_weight<kVec>(s_w[side], p);
+      const Row<P> w = lane_weight<kVec, P>(s_w[side], p);
       const RowsOut& dx = a.dx[side];
       char* op = static_cast<char*>(dx.p) +
                  (b * dx.stride[0] + n * dx.stride[2] + sub * dx.stride[1]) * (dx.f32 ? 4 : 2);
       const int64_t ostep = dx.stride[1] * per * (dx.f32 ? 4 : 2);
-      Row dw;
+      Row<P> dw;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dw.v[i] = make_float2(0.0f, 0.0f);
-      for (int k = 0; k < wk.turns; ++k) {
-        const bool ok = here && sub + k * per < wk.heads;
-        Raw<kVec, kGF32> graw;
-        Raw<kVec, kXF32> xraw;
+      for (int i = 0; i < P; ++i) dw.v[i] = make_float2(0.0f, 0.0f);
+      int head = n < a.N ? sub : heads;
+      for (int k = 0; k < turns; ++k) {
+        Raw<P, kVec, kGF32> graw;
+        Raw<P, kVec, kXF32> xraw;
         if constexpr (kVec) {
-          issue(before + k + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+          issue();
           copy_wait<kStages - 1>();
-          read_raw<kGF32>(my_g + stage * kStageBytes, graw);
-          read_raw<kXF32>(my_x + stage * kStageBytes, xraw);
-          stage = stage == kStages - 1 ? 0 : stage + 1;
+          read_raw<P, kGF32, kPrepThreads>(take, graw);
+          read_raw<P, kXF32, kPrepThreads>(take + kXOffset, xraw);
+          take = take == mine + (kStages - 1) * kStageBytes ? mine : take + kStageBytes;
         } else {
           clear_raw(graw);
           clear_raw(xraw);
-          if (ok) load_raw(wk.g + k * wk.gstep, p, graw);
-          if (ok && norm) load_raw(wk.x + k * wk.xstep, p, xraw);
+          if (head < heads) {
+            const RowsIn &dy = a.dy[side], &in = a.x[side];
+            load_raw(row_ptr(dy.p, kGF32, b * dy.stride[0] + n * dy.stride[2] + head * dy.stride[1]), p, graw);
+            if (norm) load_raw(row_ptr(in.p, kXF32, b * in.stride[0] + n * in.stride[2] + head * in.stride[1]), p, xraw);
+          }
         }
-        Row y = apply<kNext>(unpack(graw), f, p, rot, a.D);
+        Row<P> y = apply<kNext>(unpack(graw), f, p, rot, a.D);
         if (norm) norm_gradient<T>(y, unpack(xraw), w, eps, inv_d, dw);
-        if (ok) store_row<kVec>(op + k * ostep, dx.f32, p, y);
+        if (head < heads) store_row<kVec>(op, dx.f32, p, y);
+        op += ostep;
+        head += per;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if ((i & 3) < (i < 4 ? p.na : p.nb))
-          red[side][grp][i < 4 ? p.a + i : p.b + i - 4] += (i & 1) ? dw.v[i >> 1].y : dw.v[i >> 1].x;
+      for (int i = 0; i < 2 * P; ++i)
+        if (has<P>(p, i)) red[side][grp][element<P>(p, i)] += at(dw, i);
     }
     if constexpr (kVec) copy_wait<0>();
   }
@@ -246,15 +269,22 @@ __global__ void __launch_bounds__(kPrepThreads, kVec ? 3 : 1) prep_bwd_kernel(co
   }
 }
 
-template <int T, bool kNext, bool kVec>
-cudaError_t launch_bwd_t(const PrepBwdArgs& a, int ctas, bool xf32, bool gf32, cudaStream_t st) {
-  auto kern = xf32 ? (gf32 ? prep_bwd_kernel<T, kNext, kVec, true, true> : prep_bwd_kernel<T, kNext, kVec, true, false>)
-                   : (gf32 ? prep_bwd_kernel<T, kNext, kVec, false, true> : prep_bwd_kernel<T, kNext, kVec, false, false>);
-  const int ring = kVec ? 5 * kPrepThreads * ((xf32 ? 32 : 16) + (gf32 ? 32 : 16)) : 0;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+template <int T, int P, bool kNext, bool kVec, bool kXF32, bool kGF32>
+cudaError_t launch_bwd_one(const PrepBwdArgs& a, int ctas, cudaStream_t st) {
+  auto kern = prep_bwd_kernel<T, P, kNext, kVec, kXF32, kGF32>;
+  const int bytes = (kVec ? kBwdStages * (slot_bytes(P, kXF32) + slot_bytes(P, kGF32)) : 0) + a.tokens * a.rope.rot * 4;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  kern<<<ctas, kPrepThreads, ring, st>>>(a);
+  kern<<<ctas, kPrepThreads, bytes, st>>>(a);
   return cudaGetLastError();
+}
+template <int T, int P, bool kNext, bool kVec>
+cudaError_t launch_bwd_t(const PrepBwdArgs& a, int ctas, bool xf32, bool gf32, cudaStream_t st) {
+  if (xf32)
+    return gf32 ? launch_bwd_one<T, P, kNext, kVec, true, true>(a, ctas, st)
+                : launch_bwd_one<T, P, kNext, kVec, true, false>(a, ctas, st);
+  return gf32 ? launch_bwd_one<T, P, kNext, kVec, false, true>(a, ctas, st)
+              : launch_bwd_one<T, P, kNext, kVec, false, false>(a, ctas, st);
 }
 
 // dw[side][e] = sum over CTAs of partial[cta][side][e]: 8 columns a block, 128
@@ -279,9 +309,6 @@ __global__ void __launch_bounds__(1024) prep_dw_kernel(const float* partial, int
   }
 }
 
-// Lanes a row, for rows that take vector accesses and others.
-int lanes_of(int D, bool vec) { return !vec ? 32 : (D <= 64 ? 8 : 16); }
-
 // Tokens a CTA: one for each of its groups, fewer (and more groups a token)
 // until there are `ctas` CTAs.
 int tokens_of(int lanes, int B, int N, int ctas) {
@@ -294,19 +321,19 @@ int tokens_of(int lanes, int B, int N, int ctas) {
 
 cudaError_t launch_prep(PrepArgs a, int num_sms, cudaStream_t st) {
   const int heads = (a.x[0].p ? a.x[0].H : 0) + (a.x[1].p ? a.x[1].H : 0);
-  const bool next = a.rope.rot == 0 || a.rope.interleaved, vec = a.vec && (next || a.rope.rot % 8 == 0);
-  const int lanes = lanes_of(a.D, vec);
+  const bool next = a.rope.rot == 0 || a.rope.interleaved;
+  const Layout l = layout_of(a.D, a.rope.rot, next, a.vec, 4);
   // As many tokens a CTA as leave eight CTAs an SM (a group's factors serve all
   // heads of its token); one token a CTA, and its heads cut into runs of one
   // turn of the groups, where even that does not (a decode step).
-  a.tokens = tokens_of(lanes, a.B, a.N, 8 * num_sms);
+  a.tokens = tokens_of(l.T, a.B, a.N, 8 * num_sms);
   a.heads = heads;
-  if (static_cast<int64_t>(a.B) * ((a.N + a.tokens - 1) / a.tokens) < 4 * num_sms) a.heads = kPrepThreads / lanes;
-  auto kern = !vec          ? (next ? prep_kernel<32, true, false> : prep_kernel<32, false, false>)
-              : lanes == 8 ? (next ? prep_kernel<8, true, true> : prep_kernel<8, false, true>)
-                            : (next ? prep_kernel<16, true, true> : prep_kernel<16, false, true>);
+  if (static_cast<int64_t>(a.B) * ((a.N + a.tokens - 1) / a.tokens) < 4 * num_sms) a.heads = kPrepThreads / l.T;
+  auto kern = !l.vec     ? (next ? prep_kernel<32, 4, true, false> : prep_kernel<32, 4, false, false>)
+              : l.T == 8 ? (next ? prep_kernel<8, 4, true, true> : prep_kernel<8, 4, false, true>)
+                         : (next ? prep_kernel<16, 4, true, true> : prep_kernel<16, 4, false, true>);
   const dim3 grid((a.N + a.tokens - 1) / a.tokens, (heads + a.heads - 1) / a.heads, a.B);
-  kern<<<grid, kPrepThreads, 0, st>>>(a);
+  kern<<<grid, kPrepThreads, a.tokens * a.rope.rot * 4, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -318,27 +345,29 @@ cudaError_t launch_prep_bwd(PrepBwdArgs a, cudaStream_t st) {
   if (two) {
     for (int side = 0; side < 2; ++side) {
       PrepBwdArgs one = a;
-      one.dy[1 - side] = RowsIn{};
+      one.dy[1 - side] = one.x[1 - side] = RowsIn{};
       one.dw[1 - side] = nullptr;
       const cudaError_t e = launch_prep_bwd(one, st);
       if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
   }
-  const bool next = a.rope.rot == 0 || a.rope.interleaved, vec = a.vec && (next || a.rope.rot % 8 == 0);
-  const int lanes = lanes_of(a.D, vec);
-  a.tokens = tokens_of(lanes, a.B, a.N, kPrepBwdMaxCtas / 2);
+  const bool next = a.rope.rot == 0 || a.rope.interleaved;
+  const Layout l = layout_of(a.D, a.rope.rot, next, a.vec, 4);
+  a.tokens = tokens_of(l.T, a.B, a.N, kPrepBwdMaxCtas / 2);
   const int64_t items = static_cast<int64_t>(a.B) * ((a.N + a.tokens - 1) / a.tokens);
   const int ctas = static_cast<int>(items < kPrepBwdMaxCtas ? items : kPrepBwdMaxCtas);
-  const bool gf32 = a.dy[a.dy[0].p ? 0 : 1].f32;
-  const bool xf32 = a.x[0].p && a.dy[0].p ? a.x[0].f32 : a.x[1].f32;
+  const bool gf32 = a.dy[a.dy[0].p ? 0 : 1].f32, xf32 = a.x[a.x[0].p ? 0 : 1].f32;
   cudaError_t e;
-  if (!vec)
-    e = next ? launch_bwd_t<32, true, false>(a, ctas, xf32, gf32, st) : launch_bwd_t<32, false, false>(a, ctas, xf32, gf32, st);
-  else if (lanes == 8)
-    e = next ? launch_bwd_t<8, true, true>(a, ctas, xf32, gf32, st) : launch_bwd_t<8, false, true>(a, ctas, xf32, gf32, st);
+  if (!l.vec)
+    e = next ? launch_bwd_t<32, 4, true, false>(a, ctas, xf32, gf32, st)
+             : launch_bwd_t<32, 4, false, false>(a, ctas, xf32, gf32, st);
+  else if (l.T == 16)
+    e = next ? launch_bwd_t<16, 4, true, true>(a, ctas, xf32, gf32, st)
+             : launch_bwd_t<16, 4, false, true>(a, ctas, xf32, gf32, st);
   else
-    e = next ? launch_bwd_t<16, true, true>(a, ctas, xf32, gf32, st) : launch_bwd_t<16, false, true>(a, ctas, xf32, gf32, st);
+    e = next ? launch_bwd_t<8, 4, true, true>(a, ctas, xf32, gf32, st)
+             : launch_bwd_t<8, 4, false, true>(a, ctas, xf32, gf32, st);
   if (e != cudaSuccess || (a.dw[0] == nullptr && a.dw[1] == nullptr)) return e;
   prep_dw_kernel<<<dim3((a.D + 7) / 8, 2), 1024, 0, st>>>(a.partial, ctas, a.D, a.dw[0], a.dw[1]);
   return cudaGetLastError();
