@@ -16,8 +16,8 @@
 //   * a softmax weight w is likewise hi + lo / 16, rounded: at most 2^-8 w, as
 //     a rounding to bf16, and a third of that in the mean square.
 //
-// hi and lo are neighbouring columns of the small N side: 16 query rows make
-// N = 32, which costs the tensor core what N = 16 does.  With s^k_j, s^v_j the
+// hi and lo are columns of the small N side: 16 query rows make N = 32, 4 or 8
+// rows N = 16.  With s^k_j, s^v_j the
 // scales of key j, c_j the codes, in log2 units:
 //   t_rj  = rule(s_r s^k_j scale (hi_r + lo_r / 16) . c^k_j)
 //   w_rj  = 2^(t_rj + log2 s^v_j - m_r + 6),  m_r the running maximum of
@@ -48,14 +48,8 @@ namespace {
 
 constexpr int kThreads = 192;
 constexpr int kKeys = 128;        // keys per tile: the M side
-constexpr int kRows = 16;         // query rows per CTA
-constexpr int kCols = 2 * kRows;  // hi and lo columns: the N side
-constexpr int kTmemCols = 128;    // S^T buffers at 0 and 32, O^T at 64
-constexpr int kRing = 6;          // K or V tiles of 16 KB in flight
+constexpr int kMaxRows = 16;      // query rows per CTA
 constexpr int kTileBytes = kKeys * 128;
-constexpr int kQBytes = kCols * 128;
-constexpr int kPBytes = kCols * 128;
-constexpr int kSmemBytes = kRing * kTileBytes + kQBytes + 2 * kPBytes + 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // Start of the running maximum: finite and below any real score.
@@ -64,6 +58,20 @@ constexpr float kNoKeyMax = -1.0e30f;
 // 2^kShift, so they stay below 2^(kSlack + kShift) = 256 < 448.
 constexpr float kSlack = 2.0f;
 constexpr float kShift = 6.0f;
+
+// A CTA of R = 4, 8 or 16 query rows: the softmax works on R scores a key, so
+// fewer rows are that much less work (one query of a group of 4 heads on 16
+// rows: 330 us, on 4: see the launcher).  CTAs of up to 8 rows leave registers
+// for three an SM, with rings of 4 tiles (192 KB in flight an SM either way).
+template <int R>
+struct Cfg {
+  static constexpr int kCols = 2 * R < 16 ? 16 : 2 * R;  // N: hi at 0, lo at R (M = 128 takes N in 16s)
+  static constexpr int kCtas = R <= 8 ? 3 : 2;
+  static constexpr int kRing = R <= 8 ? 4 : 6;           // K or V tiles of 16 KB in flight
+  static constexpr int kTmemCols = R <= 8 ? 64 : 128;    // two S^T buffers, then O^T
+  static constexpr int kOpBytes = kCols * 128;           // Q, or one buffer of weights
+  static constexpr int kSmemBytes = kRing * kTileBytes + 3 * kOpBytes + 1024;
+};
 
 // kind::f8f6f4 instruction descriptor: e4m3 A and B, fp32 accumulator.
 constexpr uint32_t idesc_e4m3(int M, int N, int a_mn_major) {
@@ -86,6 +94,7 @@ __device__ __forceinline__ void split_e4m3(float v0, float v1, uint32_t& hi, uin
   lo = __nv_cvt_float2_to_fp8x2(make_float2((v0 - h.x) * 16.0f, (v1 - h.y) * 16.0f), __NV_SATFINITE, __NV_E4M3);
 }
 
+template <int kRing>
 struct Bars {
   uint64_t full[kRing], empty[kRing];
   uint64_t s_full[2], s_free[2], p_full[2], p_free[2], o_final;
@@ -98,29 +107,47 @@ __device__ __forceinline__ int listed_tile(const FwdArgs& a, int64_t brow, int n
                    : __ldg(a.bm.kv_indices + brow * a.bm.Nb + (j - nfull));
 }
 
-// Reduce-scatter of 16 values per lane over a warp: lane l gets the reduction
-// over all lanes of value (l >> 1) & 15, in sixteen shuffles.
-template <bool kMax>
-__device__ __forceinline__ float reduce_rows(const float (&v)[16], int lane) {
+// Reduce-scatter of R values per lane over a warp: every lane gets the
+// reduction over all lanes of value (lane * R / 32).
+template <bool kMax, int R>
+__device__ __forceinline__ float reduce_rows(const float (&v)[R], int lane) {
   auto op = [](float x, float y) { return kMax ? fmaxf(x, y) : x + y; };
-  float a[16];
+  float a[R];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) a[i] = v[i];
+  for (int i = 0; i < R; ++i) a[i] = v[i];
+  int d = 16;
 #pragma unroll
-  for (int w = 8; w >= 1; w >>= 1) {
-    const bool up = lane & (2 * w);
+  for (int w = R / 2; w >= 1; w >>= 1, d >>= 1) {
+    const bool up = lane & d;
 #pragma unroll
-    for (int i = 0; i < w; ++i)
-      a[i] = op(up ? a[w + i] : a[i], __shfl_xor_sync(0xffffffffu, up ? a[i] : a[w + i], 2 * w));
+    for (int i = 0; i < w; ++i) a[i] = op(up ? a[w + i] : a[i], __shfl_xor_sync(0xffffffffu, up ? a[i] : a[w + i], d));
   }
-  return op(a[0], __shfl_xor_sync(0xffffffffu, a[0], 1));
+#pragma unroll
+  for (; d >= 1; d >>= 1) a[0] = op(a[0], __shfl_xor_sync(0xffffffffu, a[0], d));
+  return a[0];
+}
+
+// 32 lanes x 32 bit, 8 consecutive columns per thread.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+// The hi and lo columns of a thread's TMEM lane: 2 R values.
+template <int R>
+__device__ __forceinline__ void tmem_rows(uint32_t taddr, uint32_t (&r)[2 * R]) {
+#pragma unroll
+  for (int c = 0; c < 2 * R; c += 8) tmem_ld8(taddr + c, r + c);
+  tmem_wait_ld();
+#pragma unroll
+  for (int c = 0; c < 2 * R; ++c) asm volatile("" : "+r"(r[c]));  // no use is scheduled before the wait
 }
 
 // The sequence of the given rank by length of its list of tiles, longest first
 // (ties by index), for up to 32 sequences with lists of their own; else the
 // batch order.  Called by every lane of a warp.
 __device__ __forceinline__ int ranked_sequence(const FwdArgs& a, int rank) {
-  if (a.B > 32 || a.bm.B == 1) return rank;
+  if (a.B > 32 || a.B == 1 || a.bm.B == 1) return rank;
   const int lane = threadIdx.x & 31;
   int cnt = -1;
   if (lane < a.B) {
@@ -145,32 +172,33 @@ __device__ __forceinline__ float tanh_large(float y) {
   return copysignf(1.0f - __fdividef(2.0f, 1.0f + e), y);
 }
 
-template <int SCORE>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int SCORE, int R>
+__global__ void __launch_bounds__(kThreads, Cfg<R>::kCtas)
     decode_fp8_kernel(const __grid_constant__ FwdArgs a, const __grid_constant__ QuantArgs qa, const Fp8Plan p,
                       const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, int box,
                       float* ws_o, float* ws_lse, float* ws_max) {
-  constexpr int R = kRing;
+  using C = Cfg<R>;
+  constexpr int kRing = C::kRing, kCols = C::kCols;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Bars bars;
-  __shared__ float s_red[2][4][kRows];
-  __shared__ int s_qpos[kRows], s_head[kRows], s_row[kRows], s_pq[kRows];
-  __shared__ float s_slope[kRows], s_unit[kRows];
+  __shared__ Bars<kRing> bars;
+  __shared__ float s_red[2][4][R];
+  __shared__ int s_qpos[R], s_head[R], s_row[R], s_pq[R];
+  __shared__ float s_slope[R], s_unit[R];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sKV = smem;
-  uint8_t* sQ = smem + R * kTileBytes;
-  uint8_t* sP = sQ + kQBytes;
+  uint8_t* sQ = smem + kRing * kTileBytes;
+  uint8_t* sP = sQ + C::kOpBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // grid (KV head x row chunk, split, rank): the longest sequences start first
   const int split = blockIdx.y;
   const int hk = blockIdx.x / p.row_chunks, rc = blockIdx.x % p.row_chunks;
   const int b = ranked_sequence(a, static_cast<int>(blockIdx.z));
   const int S_b = seq_len_b(a.mask, b, a.S);
-  // Rows of the chunk: 16 consecutive ones of the group's G x L (head, position)
+  // Rows of the chunk: R consecutive ones of the group's G x L (head, position)
   // pairs; with per-head lists, of one head's L positions.
-  const int per_head = a.bm.H > 1 ? (a.L + kRows - 1) / kRows : 0;
+  const int per_head = a.bm.H > 1 ? (a.L + R - 1) / R : 0;
   const int g0 = per_head ? rc / per_head : 0;
-  const int rho0 = (per_head ? rc % per_head : rc) * kRows;
+  const int rho0 = (per_head ? rc % per_head : rc) * R;
   const int rho_end = per_head ? a.L : a.G * a.L;
   const int bmb = a.bm.B > 1 ? b : 0;
   const int bmh = per_head ? hk * a.G + g0 : 0;
@@ -197,11 +225,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       outer = 0;
     } else if (a.page_table) {
       outer = cache_page(a.page_table, a.pages_per_seq, a.page_size, a.num_pages, a.status, b, kv);
-      row = kv % a.page_size;
+      row = kv - p.page.quotient(kv) * a.page_size;
     }
   };
   int row_c = 0, outer_c = 0, row_n = 0, outer_n = 0;  // this tile's box, and the next tile's
-  // K (u even) or V (u odd) of tile u / 2 into ring entry u % R; all lanes of warp 0
+  // K (u even) or V (u odd) of tile u / 2 into ring entry u % kRing; all lanes of warp 0
   auto issue_load = [&](int u) {
     if (lane < nbox) {
       if (u == 0) {
@@ -213,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if ((u >> 1) + 1 < nsub) box_addr((u >> 1) + 1, row_n, outer_n);
       }
     }
-    const int e = u % R;
+    const int e = u % kRing;
     if (lane == 0) mbar_expect_tx(&bars.full[e], kTileBytes);
     __syncwarp();
     if (lane < nbox)
@@ -221,10 +249,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                   outer_c);
   };
 
-  const int first_loads = min(R, 2 * nsub);
+  // the combine kernel may be set up once every CTA of this grid has started
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int first_loads = min(kRing, 2 * nsub);
   if (warp == 0) {
     if (lane == 0) {
-      for (int s = 0; s < R; ++s) {
+      for (int s = 0; s < kRing; ++s) {
         mbar_init(&bars.full[s], 1);
         mbar_init(&bars.empty[s], 1);
       }
@@ -246,8 +276,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int u = 0; u < first_loads; ++u) issue_load(u);
   }
   if (warp == 1) {
-    tmem_alloc(&bars.tmem_base, kTmemCols);
-    if (lane < kRows) {
+    tmem_alloc(&bars.tmem_base, C::kTmemCols);
+    if (lane < R) {
       const int rho = rho0 + lane;
       const bool ok = rho < rho_end;
       const int head = hk * a.G + (per_head ? g0 : min(rho / a.L, a.G - 1)), i = per_head ? rho : rho % a.L;
@@ -260,14 +290,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   if (warp >= 2) {
-    // Query rows as hi (rows 0-15) and lo (16-31) terms, 128-byte swizzled;
-    // 8 threads a row, 16 values each.
+    // Query rows as hi (rows 0 .. R-1) and lo (R .. 2R-1) terms, 128-byte
+    // swizzled; 8 threads a row, 16 values each; rows past 2 R are zero.
     const int r = (threadIdx.x - 64) >> 3, seg = threadIdx.x & 7;
     const int rho = rho0 + r;
     float q[16];
     float amax = 0.0f;
     bool finite = true;
-    const bool ok = rho < rho_end;
+    const bool ok = r < R && rho < rho_end;
     const int head = hk * a.G + (per_head ? g0 : min(rho / a.L, a.G - 1)), i = per_head ? rho : rho % a.L;
     const __nv_bfloat16* src =
         static_cast<const __nv_bfloat16*>(a.q) + b * a.q_stride[0] + head * a.q_stride[1] + i * a.q_stride[2];
@@ -300,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (!finite || amax == 0.0f) x = 0;
     const float inv = __uint_as_float(static_cast<uint32_t>(127 - x) << 23);
     // a row with an infinity or a NaN: every score, and so the output, is NaN
-    if (seg == 0) s_unit[r] = finite ? __uint_as_float(static_cast<uint32_t>(127 + x) << 23) : NAN;
+    if (seg == 0 && r < R) s_unit[r] = finite ? __uint_as_float(static_cast<uint32_t>(127 + x) << 23) : NAN;
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -310,9 +340,15 @@ __global__ void __launch_bounds__(kThreads, 2)
       hi[c] = h0 | (h1 << 16);
       lo[c] = l0 | (l1 << 16);
     }
-    const int off = (r >> 3) * 1024 + (r & 7) * 128 + ((seg ^ (r & 7)) << 4);
-    *reinterpret_cast<uint4*>(sQ + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(sQ + kRows * 128 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    auto place = [&](int row) { return (row >> 3) * 1024 + (row & 7) * 128 + ((seg ^ (row & 7)) << 4); };
+    if (r < R) {
+      *reinterpret_cast<uint4*>(sQ + place(r)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(sQ + place(r + R)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    if (R == 4 && r >= 8)  // columns that the weights leave unused, in either buffer too
+#pragma unroll
+      for (int buf = 0; buf < 3; ++buf)
+        *reinterpret_cast<uint4*>(sQ + buf * C::kOpBytes + place(r)) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
   }
   tc_fence_before();
@@ -325,16 +361,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (nsub > 0) {
       int issued = first_loads;
       for (int u = first_loads; u < 2 * nsub; ++u) {
-        const bool ok = !*abort && mbar_wait(&bars.empty[u % R], ((u / R) - 1) & 1, abort, a.status, a.wait_cycles);
+        const bool ok = !*abort && mbar_wait(&bars.empty[u % kRing], ((u / kRing) - 1) & 1, abort, a.status, a.wait_cycles);
         if (!__all_sync(0xffffffffu, ok)) break;
         issue_load(u);
         issued = u + 1;
       }
-      // every copy issued lands before this warp leaves (only the last R can
+      // every copy issued lands before this warp leaves (only the last kRing can
       // be pending: earlier entries were waited free before their reuse)
       volatile int never = 0;
-      for (int u = (issued > R ? issued - R : 0); u < issued; ++u)
-        mbar_wait(&bars.full[u % R], (u / R) & 1, &never, nullptr);
+      for (int u = (issued > kRing ? issued - kRing : 0); u < issued; ++u)
+        mbar_wait(&bars.full[u % kRing], (u / kRing) & 1, &never, nullptr);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA
@@ -348,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint64_t dp0 = umma_desc_sw128(smem_u32(sP), 16, 1024);
       const int ksteps = (a.E + 31) / 32;  // Q and K are zero past E
       auto issue_qk = [&](int j) {
-        const int e = (2 * j) % R, sb = j & 1;
+        const int e = (2 * j) % kRing, sb = j & 1;
         tc_fence_after();
         for (int kk = 0; kk < ksteps; ++kk)
           umma_e4m3(tbase + kCols * sb, dk0 + ((e * kTileBytes + kk * 32) >> 4), dq0 + ((kk * 32) >> 4), idesc_s,
@@ -357,29 +393,29 @@ __global__ void __launch_bounds__(kThreads, 2)
         umma_commit(&bars.empty[e]);
       };
       auto issue_pv = [&](int j) {
-        const int e = (2 * j + 1) % R, pb = j & 1;
+        const int e = (2 * j + 1) % kRing, pb = j & 1;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < kKeys / 32; ++kk)
           umma_e4m3(tbase + 2 * kCols, dv0 + ((e * kTileBytes + kk * 32 * 128) >> 4),
-                    dp0 + ((pb * kPBytes + kk * 32) >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+                    dp0 + ((pb * C::kOpBytes + kk * 32) >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
         umma_commit(&bars.p_free[pb]);
         umma_commit(&bars.empty[e]);
       };
       // Whichever product is ready first.  Tile jq's K entry last held K of
-      // tile jq - R / 2, whose QK was issued before, and likewise for V: a
+      // tile jq - kRing / 2, whose QK was issued before, and likewise for V: a
       // tested barrier is never two phases behind.
       int jq = 0, jp = 0;
       long long idle_from = clock64();
       while (jp < nsub) {
         bool progressed = false;
-        if (jq < nsub && mbar_test(&bars.full[(2 * jq) % R], ((2 * jq) / R) & 1) &&
+        if (jq < nsub && mbar_test(&bars.full[(2 * jq) % kRing], ((2 * jq) / kRing) & 1) &&
             (jq < 2 || mbar_test(&bars.s_free[jq & 1], ((jq - 2) >> 1) & 1))) {
           issue_qk(jq++);
           progressed = true;
         }
         if (jp < jq && mbar_test(&bars.p_full[jp & 1], (jp >> 1) & 1) &&
-            mbar_test(&bars.full[(2 * jp + 1) % R], ((2 * jp + 1) / R) & 1)) {
+            mbar_test(&bars.full[(2 * jp + 1) % kRing], ((2 * jp + 1) / kRing) & 1)) {
           issue_pv(jp++);
           progressed = true;
         }
@@ -407,10 +443,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float c_in = kCapped ? a.scale / a.score.cap : a.scale * kLog2e;
     const float c_out = kCapped ? a.score.cap * kLog2e : 1.0f;
     const bool want_max = a.max_scores != nullptr;
-    float m_run[kRows], l_part[kRows], tm[kRows], unit[kRows];
-    float sl2[kRows], sq2[kRows];  // distance bias in log2 units: slope, slope * q
+    float m_run[R], l_part[R], tm[R], unit[R];
+    float sl2[R], sq2[R];  // distance bias in log2 units: slope, slope * q
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
+    for (int r = 0; r < R; ++r) {
       m_run[r] = kNoKeyMax;
       l_part[r] = 0.0f;
       tm[r] = -INFINITY;
@@ -426,13 +462,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int kv = key_of(j);
       if (kv >= S_b) return -1;
       if (!a.page_table) return b;
-      const int pg = __ldg(a.page_table + static_cast<int64_t>(b) * a.pages_per_seq + kv / a.page_size);
+      const int pg = __ldg(a.page_table + static_cast<int64_t>(b) * a.pages_per_seq + p.page.quotient(kv));
       return min(max(pg, 0), a.num_pages - 1);  // warp 0 records an id outside the pool
     };
     auto scales_of = [&](int j, int pg, float& ks, float& vs) {
       ks = vs = 1.0f;
       if (pg < 0) return;
-      const int kv = key_of(j), at = a.page_table ? kv % a.page_size : kv;
+      const int kv = key_of(j), at = a.page_table ? kv - p.page.quotient(kv) * a.page_size : kv;
       const int64_t i = (static_cast<int64_t>(pg) * a.Hkv + hk) * qa.scales_per_outer + (at >> qa.block_log);
       ks = __ldg(qa.k_scale + i);
       vs = __ldg(qa.v_scale + i);
@@ -451,25 +487,23 @@ __global__ void __launch_bounds__(kThreads, 2)
       const float lv = log2f(vs), ivs = 1.0f / vs;
       bool ok = alive && __all_sync(0xffffffffu, mbar_wait(&bars.s_full[sb], (j >> 1) & 1, abort, a.status,
                                                            a.wait_cycles));
-      float t[kRows];  // score + log2 of the value scale
+      float t[R];  // score + log2 of the value scale
       bool grow = false;
       if (ok) {
-        uint32_t sh[kRows], sl[kRows];
+        uint32_t sr[2 * R];
         tc_fence_after();
-        tmem_ld16(tbase + lane_base + kCols * sb, sh);
-        tmem_ld16(tbase + lane_base + kCols * sb + kRows, sl);
-        tmem_wait_ld();
+        tmem_rows<R>(tbase + lane_base + kCols * sb, sr);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.s_free[sb]);
 #pragma unroll
-        for (int r = 0; r < kRows; ++r)
-          t[r] = fmaf(__uint_as_float(sl[r]), 0.0625f, __uint_as_float(sh[r])) * (unit[r] * ks);
+        for (int r = 0; r < R; ++r)
+          t[r] = fmaf(__uint_as_float(sr[R + r]), 0.0625f, __uint_as_float(sr[r])) * (unit[r] * ks);
         if constexpr (kCapped) {
-          float th[kRows];
+          float th[R];
           bool big = false;
 #pragma unroll
-          for (int i = 0; i < kRows / 2; ++i) {
+          for (int i = 0; i < R / 2; ++i) {
             float2 u2;
             const float2 v2 = tanh_poly2(make_float2(t[2 * i], t[2 * i + 1]), u2);
             th[2 * i] = v2.x;
@@ -478,21 +512,21 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           if (__any_sync(0xffffffffu, big)) {
 #pragma unroll
-            for (int r = 0; r < kRows; ++r)
+            for (int r = 0; r < R; ++r)
               if (!(fabsf(t[r]) <= kTanhPolyMax)) th[r] = tanh_large(t[r]);
           }
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) t[r] = th[r] * c_out;
+          for (int r = 0; r < R; ++r) t[r] = th[r] * c_out;
         }
         if constexpr (SCORE == FA_SCORE_ALIBI) {
           const float kvf = static_cast<float>(kv);
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) t[r] += fmaf(sl2[r], kvf, -sq2[r]);
+          for (int r = 0; r < R; ++r) t[r] += fmaf(sl2[r], kvf, -sq2[r]);
         }
         if constexpr (SCORE == FA_SCORE_CAP_THEN_BIAS) {
           const int pk = has_pos ? pos_at(a.score, b, kv, a.S) : kv;
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) {
+          for (int r = 0; r < R; ++r) {
             const int d = has_pos ? pk - s_pq[r] : kv - s_qpos[r];
             t[r] = fmaf(sl2[r], static_cast<float>(d), t[r]);
           }
@@ -500,15 +534,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         // element mask on listed-partial tiles and at the end of the sequence
         if (jt >= nfull || kv0 + kKeys > S_b) {
 #pragma unroll
-          for (int r = 0; r < kRows; ++r)
+          for (int r = 0; r < R; ++r)
             if (s_head[r] < 0 || !mask_visible(a.mask, b, s_head[r], s_qpos[r], kv, S_b, a.S)) t[r] = -INFINITY;
         }
         if (want_max) {
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) tm[r] = fmaxf(tm[r], t[r]);
+          for (int r = 0; r < R; ++r) tm[r] = fmaxf(tm[r], t[r]);
         }
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
+        for (int r = 0; r < R; ++r) {
           t[r] += lv;
           grow |= t[r] > m_run[r] + kSlack;
         }
@@ -519,12 +553,12 @@ __global__ void __launch_bounds__(kThreads, 2)
           alive = false;
           break;
         }
-        const float v = reduce_rows<true>(t, lane);
-        if ((lane & 1) == 0) s_red[0][qd][(lane >> 1) & 15] = v;
+        const float v = reduce_rows<true, R>(t, lane);
+        if (lane % (32 / R) == 0) s_red[0][qd][lane / (32 / R)] = v;
         named_bar_sync(1, 128);
-        float alpha[kRows];
+        float alpha[R];
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
+        for (int r = 0; r < R; ++r) {
           const float tmax = fmaxf(fmaxf(s_red[0][0][r], s_red[0][1][r]), fmaxf(s_red[0][2][r], s_red[0][3][r]));
           const float mn = fmaxf(m_run[r], tmax);
           alpha[r] = ex2_approx(m_run[r] - mn);
@@ -539,17 +573,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                                                     a.wait_cycles));
           if (alive) {
             tc_fence_after();
-            uint32_t o[kRows], o2[kRows];
-            tmem_ld16(tbase + lane_base + 2 * kCols, o);
-            tmem_ld16(tbase + lane_base + 2 * kCols + kRows, o2);
-            tmem_wait_ld();
+            uint32_t o[2 * R];
+            tmem_rows<R>(tbase + lane_base + 2 * kCols, o);
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-              o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r]);
-              o2[r] = __float_as_uint(__uint_as_float(o2[r]) * alpha[r]);
-            }
-            tmem_st16(tbase + lane_base + 2 * kCols, o);
-            tmem_st16(tbase + lane_base + 2 * kCols + kRows, o2);
+            for (int r = 0; r < 2 * R; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r % R]);
+#pragma unroll
+            for (int c = 0; c < 2 * R; c += 8)
+              tmem_st8(tbase + lane_base + 2 * kCols + c, *reinterpret_cast<uint32_t(*)[8]>(o + c));
             tmem_wait_st();
           }
         }
@@ -562,29 +592,28 @@ __global__ void __launch_bounds__(kThreads, 2)
       // their rows are cleared before the product reads them.
       if (alive && kv0 + kKeys > S_b) {
         const int u = 2 * j + 1;
-        alive = __all_sync(0xffffffffu, mbar_wait(&bars.full[u % R], (u / R) & 1, abort, a.status, a.wait_cycles));
+        alive = __all_sync(0xffffffffu, mbar_wait(&bars.full[u % kRing], (u / kRing) & 1, abort, a.status, a.wait_cycles));
         if (alive && kv >= S_b) {
-          uint4* vrow = reinterpret_cast<uint4*>(sKV + (u % R) * kTileBytes + kk * 128);
+          uint4* vrow = reinterpret_cast<uint4*>(sKV + (u % kRing) * kTileBytes + kk * 128);
 #pragma unroll
           for (int i = 0; i < 8; ++i) vrow[i] = make_uint4(0u, 0u, 0u, 0u);
         }
       }
       if (alive) {
-        uint8_t* pbuf = sP + sb * kPBytes + (kk & 15);
+        uint8_t* pbuf = sP + sb * C::kOpBytes + (kk & 15);
         const int ch = kk >> 4;
+        auto place = [&](int row) { return (row >> 3) * 1024 + (row & 7) * 128 + ((ch ^ (row & 7)) << 4); };
 #pragma unroll
-        for (int r = 0; r < kRows; r += 2) {
+        for (int r = 0; r < R; r += 2) {
           const float w0 = ex2_approx(t[r] - (m_run[r] - kShift)), w1 = ex2_approx(t[r + 1] - (m_run[r + 1] - kShift));
           l_part[r] = fmaf(w0, ivs, l_part[r]);
           l_part[r + 1] = fmaf(w1, ivs, l_part[r + 1]);
           uint32_t hi, lo;
           split_e4m3(w0, w1, hi, lo);
-          uint8_t* p0 = pbuf + (r >> 3) * 1024 + (r & 7) * 128 + ((ch ^ (r & 7)) << 4);
-          uint8_t* p1 = pbuf + (r >> 3) * 1024 + ((r + 1) & 7) * 128 + ((ch ^ ((r + 1) & 7)) << 4);
-          p0[0] = static_cast<uint8_t>(hi);
-          p1[0] = static_cast<uint8_t>(hi >> 8);
-          p0[kRows * 128] = static_cast<uint8_t>(lo);
-          p1[kRows * 128] = static_cast<uint8_t>(lo >> 8);
+          pbuf[place(r)] = static_cast<uint8_t>(hi);
+          pbuf[place(r + 1)] = static_cast<uint8_t>(hi >> 8);
+          pbuf[place(R + r)] = static_cast<uint8_t>(lo);
+          pbuf[place(R + r + 1)] = static_cast<uint8_t>(lo >> 8);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -599,24 +628,20 @@ __global__ void __launch_bounds__(kThreads, 2)
     fin = named_bar_and(1, 128, fin && !*abort);
     if (fin) {
       tc_fence_after();
-      uint32_t o[kRows], o2[kRows];
+      uint32_t o[2 * R];
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) o[r] = o2[r] = 0u;
-      if (nsub > 0) {
-        tmem_ld16(tbase + lane_base + 2 * kCols, o);
-        tmem_ld16(tbase + lane_base + 2 * kCols + kRows, o2);
-        tmem_wait_ld();
-      }
-      const float ls = reduce_rows<false>(l_part, lane);
-      const float lm = reduce_rows<true>(tm, lane);
-      if ((lane & 1) == 0) {
-        s_red[0][qd][(lane >> 1) & 15] = ls;
-        s_red[1][qd][(lane >> 1) & 15] = lm;
+      for (int r = 0; r < 2 * R; ++r) o[r] = 0u;
+      if (nsub > 0) tmem_rows<R>(tbase + lane_base + 2 * kCols, o);
+      const float ls = reduce_rows<false, R>(l_part, lane);
+      const float lm = reduce_rows<true, R>(tm, lane);
+      if (lane % (32 / R) == 0) {
+        s_red[0][qd][lane / (32 / R)] = ls;
+        s_red[1][qd][lane / (32 / R)] = lm;
       }
       named_bar_sync(1, 128);
       const int ev = kk;
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
+      for (int r = 0; r < R; ++r) {
         const int hq = s_head[r];
         if (hq < 0) continue;
         const float l = (s_red[0][0][r] + s_red[0][1][r]) + (s_red[0][2][r] + s_red[0][3][r]);
@@ -628,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float inv = live ? 1.0f / l : 0.0f;
         const float lse = live ? ((m_run[r] - kShift) + log2f(l)) * kLn2 : -INFINITY;
         const int64_t row_id = (static_cast<int64_t>(b) * a.Hq + hq) * a.L + s_row[r];
-        const float val = fmaf(__uint_as_float(o2[r]), 0.0625f, __uint_as_float(o[r])) * inv;
+        const float val = fmaf(__uint_as_float(o[R + r]), 0.0625f, __uint_as_float(o[r])) * inv;
         if (p.splits == 1) {
           if (ev < a.Ev) {
             const int64_t off = b * a.o_stride[0] + hq * a.o_stride[1] + s_row[r] * a.o_stride[2] + ev;
@@ -651,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tbase, kTmemCols);
+  if (warp == 1) tmem_dealloc(tbase, C::kTmemCols);
 }
 
 // One CTA per query row: merge the splits' (o_s, lse_s, max_s), with
@@ -660,6 +685,8 @@ __global__ void __launch_bounds__(128) combine_fp8_kernel(const __grid_constant_
                                                           const float* ws_o, const float* ws_lse, const float* ws_max) {
   __shared__ float s_w[kFp8MaxSplits];
   __shared__ float s_m[4], s_t[4], s_sum[4];
+  // launched while the decode kernel still runs: wait for its results
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t row_id = blockIdx.x;
   const int i = static_cast<int>(row_id % a.L), h = static_cast<int>((row_id / a.L) % a.Hq);
   const int b = static_cast<int>(row_id / (static_cast<int64_t>(a.L) * a.Hq));
@@ -789,11 +816,25 @@ __global__ void __launch_bounds__(256) restore_kernel(const __grid_constant__ Fw
 
 }  // namespace
 
+FastDiv fast_div(int d) {
+  FastDiv f{0u, 0};
+  if (d == 1) return f;
+  while ((int64_t{1} << f.shift) < d) ++f.shift;
+  f.mul = static_cast<uint32_t>(((uint64_t{1} << (31 + f.shift)) + d - 1) / d);
+  return f;
+}
+
 void plan_decode_fp8(const FwdArgs& a, int split_kv, int num_sms, Fp8Plan* p) {
-  p->row_chunks = a.bm.H > 1 ? a.G * ((a.L + kRows - 1) / kRows) : (a.G * a.L + kRows - 1) / kRows;
+  const int span = a.bm.H > 1 ? a.L : a.G * a.L;  // rows that share a list of tiles
+  p->rows = span <= 4 ? 4 : (span <= 8 ? 8 : kMaxRows);
+  p->row_chunks = (a.bm.H > 1 ? a.G : 1) * ((span + p->rows - 1) / p->rows);
+  p->page = fast_div(a.page_table ? a.page_size : 1);
   const int64_t units = static_cast<int64_t>(a.B) * a.Hkv * p->row_chunks;
+  const int slots = (p->rows <= 8 ? Cfg<8>::kCtas : Cfg<16>::kCtas) * num_sms;
   int64_t splits = split_kv;
-  if (split_kv == 0) splits = (5 * num_sms + units - 1) / units;  // about 2.5 rounds of two CTAs an SM
+  // One round of CTAs where the sequences are few; several, longest first,
+  // where many of unequal length are to be balanced.
+  if (split_kv == 0) splits = units * 4 <= slots ? slots / units : (2 * slots + units - 1) / units;
   splits = splits < 1 ? 1 : (splits > a.bm.Nb ? a.bm.Nb : splits);
   splits = splits > kFp8MaxSplits ? kFp8MaxSplits : splits;
   const int per = static_cast<int>((a.bm.Nb + splits - 1) / splits);
@@ -802,24 +843,44 @@ void plan_decode_fp8(const FwdArgs& a, int split_kv, int num_sms, Fp8Plan* p) {
       p->splits > 1 ? static_cast<size_t>(a.B) * a.Hq * a.L * p->splits * (a.Ev + 2) * sizeof(float) : 0;
 }
 
+namespace {
+template <int R>
+cudaError_t launch_rows(const FwdArgs& a, const QuantArgs& qa, const Fp8Plan& p, const CUtensorMap& map_k,
+                        const CUtensorMap& map_v, int box, float* ws_o, float* ws_lse, float* ws_max,
+                        cudaStream_t stream) {
+  auto kern = a.score.kind == FA_SCORE_NONE      ? decode_fp8_kernel<FA_SCORE_NONE, R>
+              : a.score.kind == FA_SCORE_SOFTCAP ? decode_fp8_kernel<FA_SCORE_SOFTCAP, R>
+              : a.score.kind == FA_SCORE_ALIBI   ? decode_fp8_kernel<FA_SCORE_ALIBI, R>
+                                                 : decode_fp8_kernel<FA_SCORE_CAP_THEN_BIAS, R>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<R>::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3(a.Hkv * p.row_chunks, p.splits, a.B), kThreads, Cfg<R>::kSmemBytes, stream>>>(
+      a, qa, p, map_k, map_v, box, ws_o, ws_lse, ws_max);
+  return cudaGetLastError();
+}
+}  // namespace
+
 cudaError_t launch_decode_fp8(const FwdArgs& a, const QuantArgs& qa, const Fp8Plan& p, const CUtensorMap& map_k,
                               const CUtensorMap& map_v, int box, void* workspace, cudaStream_t stream) {
   float* ws_o = static_cast<float*>(workspace);
   const int64_t rows = static_cast<int64_t>(a.B) * a.Hq * a.L;
   float* ws_lse = ws_o ? ws_o + rows * p.splits * a.Ev : nullptr;
   float* ws_max = ws_o ? ws_lse + rows * p.splits : nullptr;
-  auto kern = a.score.kind == FA_SCORE_NONE      ? decode_fp8_kernel<FA_SCORE_NONE>
-              : a.score.kind == FA_SCORE_SOFTCAP ? decode_fp8_kernel<FA_SCORE_SOFTCAP>
-              : a.score.kind == FA_SCORE_ALIBI   ? decode_fp8_kernel<FA_SCORE_ALIBI>
-                                                 : decode_fp8_kernel<FA_SCORE_CAP_THEN_BIAS>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e != cudaSuccess) return e;
-  kern<<<dim3(a.Hkv * p.row_chunks, p.splits, a.B), kThreads, kSmemBytes, stream>>>(a, qa, p, map_k, map_v, box, ws_o,
-                                                                                 ws_lse, ws_max);
-  e = cudaGetLastError();
+  cudaError_t e = p.rows == 4   ? launch_rows<4>(a, qa, p, map_k, map_v, box, ws_o, ws_lse, ws_max, stream)
+                  : p.rows == 8 ? launch_rows<8>(a, qa, p, map_k, map_v, box, ws_o, ws_lse, ws_max, stream)
+                                : launch_rows<16>(a, qa, p, map_k, map_v, box, ws_o, ws_lse, ws_max, stream);
   if (e != cudaSuccess || p.splits == 1) return e;
-  combine_fp8_kernel<<<static_cast<unsigned>(rows), 128, 0, stream>>>(a, p.splits, ws_o, ws_lse, ws_max);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(rows));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_fp8_kernel, a, p.splits, static_cast<const float*>(ws_o),
+                            static_cast<const float*>(ws_lse), static_cast<const float*>(ws_max));
 }
 
 cudaError_t launch_restore(const FwdArgs& a, const QuantArgs& qa, const RestoreArgs& k, const RestoreArgs& v,

@@ -193,8 +193,23 @@ struct QuantArgs {
   int block_log;                   // log2 of the slots per scale
   int scales_per_outer;
 };
+// Quotients by a fixed divisor of values below 2^31: with s = ceil(log2 d) and
+// mul = ceil(2^(31 + s) / d) < 2^32, x / d = (x mul) >> (31 + s) (the error of
+// mul is below 2^s / 2^(31 + s) of it, less than 1 / (d x)).
+struct FastDiv {
+  uint32_t mul;  // 0: d = 1
+  int shift;
+#ifdef __CUDACC__
+  __device__ __forceinline__ int quotient(int x) const {
+    return mul == 0 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x) << 1, mul) >> shift);
+  }
+#endif
+};
+FastDiv fast_div(int d);
 struct Fp8Plan {
-  int row_chunks;   // CTAs that share one KV head's cache: 16 query rows each
+  int rows;         // query rows of a CTA: 4, 8 or 16
+  int row_chunks;   // CTAs that share one KV head's cache
+  FastDiv page;     // slots to pages
   int splits;       // KV splits per (sequence, KV head, row chunk)
   size_t workspace_bytes;
 };
