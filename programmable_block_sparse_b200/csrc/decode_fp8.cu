@@ -34,7 +34,7 @@
 //   warp 0      TMA: one box per page piece, a lane each.
 //   warp 1      TMEM allocation; one thread issues the MMAs, whichever product
 //               is ready first.
-//   warps 2-5   softmax (warp % 4 is the TMEM lane quadrant), epilogue.
+//   warps 2-    softmax (warp % 4 is the TMEM lane quadrant), epilogue.
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -46,7 +46,6 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 192;
 constexpr int kKeys = 128;        // keys per tile: the M side
 constexpr int kMaxRows = 16;      // query rows per CTA
 constexpr int kTileBytes = kKeys * 128;
@@ -61,10 +60,15 @@ constexpr float kShift = 6.0f;
 
 // A CTA of R = 4, 8 or 16 query rows: the softmax works on R scores a key, so
 // fewer rows are that much less work (one query of a group of 4 heads on 16
-// rows: 330 us, on 4: see the launcher).  CTAs of up to 8 rows leave registers
-// for three an SM, with rings of 4 tiles (192 KB in flight an SM either way).
+// rows took 330 us where 4 rows take 232).  Sixteen rows go to two sets of four
+// softmax warps, 8 rows each, which share the tiles but nothing else.  CTAs of
+// up to 8 rows leave registers for three an SM, with rings of 4 tiles (192 KB
+// in flight an SM either way).
 template <int R>
 struct Cfg {
+  static constexpr int kSets = R == 16 ? 2 : 1;          // sets of softmax warps
+  static constexpr int kOwn = R / kSets;                 // rows of a set
+  static constexpr int kThreads = 64 + 128 * kSets;
   static constexpr int kCols = 2 * R < 16 ? 16 : 2 * R;  // N: hi at 0, lo at R (M = 128 takes N in 16s)
   static constexpr int kCtas = R <= 8 ? 3 : 2;
   static constexpr int kRing = R <= 8 ? 4 : 6;           // K or V tiles of 16 KB in flight
@@ -133,14 +137,15 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
-// The hi and lo columns of a thread's TMEM lane: 2 R values.
-template <int R>
-__device__ __forceinline__ void tmem_rows(uint32_t taddr, uint32_t (&r)[2 * R]) {
+// The hi columns (from taddr on) and lo columns (from taddr + R on) of N rows
+// of a thread's TMEM lane.  Four rows lie side by side: one load of 8.
+template <int N, int R>
+__device__ __forceinline__ void tmem_rows(uint32_t taddr, uint32_t (&r)[2 * N]) {
 #pragma unroll
-  for (int c = 0; c < 2 * R; c += 8) tmem_ld8(taddr + c, r + c);
+  for (int c = 0; c < 2 * N; c += 8) tmem_ld8(taddr + (c < N ? c : c - N + R), r + c);
   tmem_wait_ld();
 #pragma unroll
-  for (int c = 0; c < 2 * R; ++c) asm volatile("" : "+r"(r[c]));  // no use is scheduled before the wait
+  for (int c = 0; c < 2 * N; ++c) asm volatile("" : "+r"(r[c]));  // no use is scheduled before the wait
 }
 
 // The sequence of the given rank by length of its list of tiles, longest first
@@ -173,7 +178,7 @@ __device__ __forceinline__ float tanh_large(float y) {
 }
 
 template <int SCORE, int R>
-__global__ void __launch_bounds__(kThreads, Cfg<R>::kCtas)
+__global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
     decode_fp8_kernel(const __grid_constant__ FwdArgs a, const __grid_constant__ QuantArgs qa, const Fp8Plan p,
                       const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, int box,
                       float* ws_o, float* ws_lse, float* ws_max) {
@@ -260,8 +265,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<R>::kCtas)
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&bars.s_full[i], 1);
-        mbar_init(&bars.s_free[i], 4);
-        mbar_init(&bars.p_full[i], 4);
+        mbar_init(&bars.s_free[i], 4 * C::kSets);
+        mbar_init(&bars.p_full[i], 4 * C::kSets);
         mbar_init(&bars.p_free[i], 1);
       }
       mbar_init(&bars.o_final, 1);
@@ -289,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R>::kCtas)
       s_pq[lane] = has_pos ? pos_at(a.score, b, s_qpos[lane], a.S) : 0;
     }
   }
-  if (warp >= 2) {
+  if (warp >= 2 && warp < 6) {
     // Query rows as hi (rows 0 .. R-1) and lo (R .. 2R-1) terms, 128-byte
     // swizzled; 8 threads a row, 16 values each; rows past 2 R are zero.
     const int r = (threadIdx.x - 64) >> 3, seg = threadIdx.x & 7;
@@ -436,23 +441,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<R>::kCtas)
     }
   } else {
     // -------------------------------------------------------------- softmax
+    constexpr int N = C::kOwn;
     const int qd = warp & 3;
+    const int set = (warp - 2) >> 2, row0 = set * N;  // this set's rows: row0 .. row0 + N - 1
+    const int bar = 1 + set;
     const int kk = qd * 32 + lane;  // this thread's key of a tile; its TMEM lane
     const uint32_t lane_base = static_cast<uint32_t>(qd * 32) << 16;
     constexpr bool kCapped = SCORE == FA_SCORE_SOFTCAP || SCORE == FA_SCORE_CAP_THEN_BIAS;
     const float c_in = kCapped ? a.scale / a.score.cap : a.scale * kLog2e;
     const float c_out = kCapped ? a.score.cap * kLog2e : 1.0f;
     const bool want_max = a.max_scores != nullptr;
-    float m_run[R], l_part[R], tm[R], unit[R];
-    float sl2[R], sq2[R];  // distance bias in log2 units: slope, slope * q
+    float m_run[N], l_part[N], tm[N], unit[N];
+    float sl2[N], sq2[N];  // distance bias in log2 units: slope, slope * q
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < N; ++r) {
       m_run[r] = kNoKeyMax;
       l_part[r] = 0.0f;
       tm[r] = -INFINITY;
-      unit[r] = s_unit[r] * c_in;
-      sl2[r] = s_slope[r] * kLog2e;
-      sq2[r] = sl2[r] * static_cast<float>(s_qpos[r]);
+      unit[r] = s_unit[row0 + r] * c_in;
+      sl2[r] = s_slope[row0 + r] * kLog2e;
+      sq2[r] = sl2[r] * static_cast<float>(s_qpos[row0 + r]);
     }
     // This key's scales, loaded a tile ahead, its page two tiles ahead (the
     // two loads depend on one another).
@@ -487,23 +495,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<R>::kCtas)
       const float lv = log2f(vs), ivs = 1.0f / vs;
       bool ok = alive && __all_sync(0xffffffffu, mbar_wait(&bars.s_full[sb], (j >> 1) & 1, abort, a.status,
                                                            a.wait_cycles));
-      float t[R];  // score + log2 of the value scale
+      float t[N];  // score + log2 of the value scale
       bool grow = false;
       if (ok) {
-        uint32_t sr[2 * R];
+        uint32_t sr[2 * N];
         tc_fence_after();
-        tmem_rows<R>(tbase + lane_base + kCols * sb, sr);
+        tmem_rows<N, R>(tbase + lane_base + kCols * sb + row0, sr);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.s_free[sb]);
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-          t[r] = fmaf(__uint_as_float(sr[R + r]), 0.0625f, __uint_as_float(sr[r])) * (unit[r] * ks);
+        for (int r = 0; r < N; ++r)
+          t[r] = fmaf(__uint_as_float(sr[N + r]), 0.0625f, __uint_as_float(sr[r])) * (unit[r] * ks);
         if constexpr (kCapped) {
-          float th[R];
+          float th[N];
           bool big = false;
 #pragma unroll
-          for (int i = 0; i < R / 2; ++i) {
+          for (int i = 0; i < N / 2; ++i) {
             float2 u2;
             const float2 v2 = tanh_poly2(make_float2(t[2 * i], t[2 * i + 1]), u2);
             th[2 * i] = v2.x;
@@ -512,60 +520,60 @@ __global__ void __launch_bounds__(kThreads, Cfg<R>::kCtas)
           }
           if (__any_sync(0xffffffffu, big)) {
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+            for (int r = 0; r < N; ++r)
               if (!(fabsf(t[r]) <= kTanhPolyMax)) th[r] = tanh_large(t[r]);
           }
 #pragma unroll
-          for (int r = 0; r < R; ++r) t[r] = th[r] * c_out;
+          for (int r = 0; r < N; ++r) t[r] = th[r] * c_out;
         }
         if constexpr (SCORE == FA_SCORE_ALIBI) {
           const float kvf = static_cast<float>(kv);
 #pragma unroll
-          for (int r = 0; r < R; ++r) t[r] += fmaf(sl2[r], kvf, -sq2[r]);
+          for (int r = 0; r < N; ++r) t[r] += fmaf(sl2[r], kvf, -sq2[r]);
         }
         if constexpr (SCORE == FA_SCORE_CAP_THEN_BIAS) {
           const int pk = has_pos ? pos_at(a.score, b, kv, a.S) : kv;
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const int d = has_pos ? pk - s_pq[r] : kv - s_qpos[r];
+          for (int r = 0; r < N; ++r) {
+            const int d = has_pos ? pk - s_pq[row0 + r] : kv - s_qpos[row0 + r];
             t[r] = fmaf(sl2[r], static_cast<float>(d), t[r]);
           }
         }
         // element mask on listed-partial tiles and at the end of the sequence
         if (jt >= nfull || kv0 + kKeys > S_b) {
 #pragma unroll
-          for (int r = 0; r < R; ++r)
-            if (s_head[r] < 0 || !mask_visible(a.mask, b, s_head[r], s_qpos[r], kv, S_b, a.S)) t[r] = -INFINITY;
+          for (int r = 0; r < N; ++r)
+            if (s_head[row0 + r] < 0 || !mask_visible(a.mask, b, s_head[row0 + r], s_qpos[row0 + r], kv, S_b, a.S)) t[r] = -INFINITY;
         }
         if (want_max) {
 #pragma unroll
-          for (int r = 0; r < R; ++r) tm[r] = fmaxf(tm[r], t[r]);
+          for (int r = 0; r < N; ++r) tm[r] = fmaxf(tm[r], t[r]);
         }
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
+        for (int r = 0; r < N; ++r) {
           t[r] += lv;
           grow |= t[r] > m_run[r] + kSlack;
         }
       }
       // one vote per tile: as usual, or a wait gave up, or a maximum moves
-      if (named_bar_or(1, 128, !ok || grow)) {
-        if (named_bar_or(1, 128, !ok)) {
+      if (named_bar_or(bar, 128, !ok || grow)) {
+        if (named_bar_or(bar, 128, !ok)) {
           alive = false;
           break;
         }
-        const float v = reduce_rows<true, R>(t, lane);
-        if (lane % (32 / R) == 0) s_red[0][qd][lane / (32 / R)] = v;
-        named_bar_sync(1, 128);
-        float alpha[R];
+        const float v = reduce_rows<true, N>(t, lane);
+        if (lane % (32 / N) == 0) s_red[0][qd][row0 + lane / (32 / N)] = v;
+        named_bar_sync(bar, 128);
+        float alpha[N];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float tmax = fmaxf(fmaxf(s_red[0][0][r], s_red[0][1][r]), fmaxf(s_red[0][2][r], s_red[0][3][r]));
+        for (int r = 0; r < N; ++r) {
+          const float tmax = fmaxf(fmaxf(s_red[0][0][row0 + r], s_red[0][1][row0 + r]), fmaxf(s_red[0][2][row0 + r], s_red[0][3][row0 + r]));
           const float mn = fmaxf(m_run[r], tmax);
           alpha[r] = ex2_approx(m_run[r] - mn);
           m_run[r] = mn;
           l_part[r] *= alpha[r];
         }
-        named_bar_sync(1, 128);  // s_red is read by all before its next use
+        named_bar_sync(bar, 128);  // s_red is read by all before its next use
         if (j > 0) {
           // O^T holds tiles 0 .. j-1: once the last of them is in, rescale
           const int jp = j - 1;
@@ -573,13 +581,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<R>::kCtas)
                                                     a.wait_cycles));
           if (alive) {
             tc_fence_after();
-            uint32_t o[2 * R];
-            tmem_rows<R>(tbase + lane_base + 2 * kCols, o);
+            const uint32_t ot = tbase + lane_base + 2 * kCols + row0;
+            uint32_t o[2 * N];
+            tmem_rows<N, R>(ot, o);
 #pragma unroll
-            for (int r = 0; r < 2 * R; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r % R]);
+            for (int r = 0; r < 2 * N; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r % N]);
 #pragma unroll
-            for (int c = 0; c < 2 * R; c += 8)
-              tmem_st8(tbase + lane_base + 2 * kCols + c, *reinterpret_cast<uint32_t(*)[8]>(o + c));
+            for (int c = 0; c < 2 * N; c += 8)
+              tmem_st8(ot + (c < N ? c : c - N + R), *reinterpret_cast<uint32_t(*)[8]>(o + c));
             tmem_wait_st();
           }
         }
@@ -593,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<R>::kCtas)
       if (alive && kv0 + kKeys > S_b) {
         const int u = 2 * j + 1;
         alive = __all_sync(0xffffffffu, mbar_wait(&bars.full[u % kRing], (u / kRing) & 1, abort, a.status, a.wait_cycles));
-        if (alive && kv >= S_b) {
+        if (alive && set == 0 && kv >= S_b) {
           uint4* vrow = reinterpret_cast<uint4*>(sKV + (u % kRing) * kTileBytes + kk * 128);
 #pragma unroll
           for (int i = 0; i < 8; ++i) vrow[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -604,16 +613,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<R>::kCtas)
         const int ch = kk >> 4;
         auto place = [&](int row) { return (row >> 3) * 1024 + (row & 7) * 128 + ((ch ^ (row & 7)) << 4); };
 #pragma unroll
-        for (int r = 0; r < R; r += 2) {
+        for (int r = 0; r < N; r += 2) {
+          const int row = row0 + r;
           const float w0 = ex2_approx(t[r] - (m_run[r] - kShift)), w1 = ex2_approx(t[r + 1] - (m_run[r + 1] - kShift));
           l_part[r] = fmaf(w0, ivs, l_part[r]);
           l_part[r + 1] = fmaf(w1, ivs, l_part[r + 1]);
           uint32_t hi, lo;
           split_e4m3(w0, w1, hi, lo);
-          pbuf[place(r)] = static_cast<uint8_t>(hi);
-          pbuf[place(r + 1)] = static_cast<uint8_t>(hi >> 8);
-          pbuf[place(R + r)] = static_cast<uint8_t>(lo);
-          pbuf[place(R + r + 1)] = static_cast<uint8_t>(lo >> 8);
+          pbuf[place(row)] = static_cast<uint8_t>(hi);
+          pbuf[place(row + 1)] = static_cast<uint8_t>(hi >> 8);
+          pbuf[place(R + row)] = static_cast<uint8_t>(lo);
+          pbuf[place(R + row + 1)] = static_cast<uint8_t>(lo >> 8);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -625,38 +635,38 @@ __global__ void __launch_bounds__(kThreads, Cfg<R>::kCtas)
     // through the vote, or at its end)
     bool fin = alive;
     if (fin && nsub > 0) fin = mbar_wait(&bars.o_final, 0, abort, a.status, a.wait_cycles);
-    fin = named_bar_and(1, 128, fin && !*abort);
+    fin = named_bar_and(bar, 128, fin && !*abort);
     if (fin) {
       tc_fence_after();
-      uint32_t o[2 * R];
+      uint32_t o[2 * N];
 #pragma unroll
-      for (int r = 0; r < 2 * R; ++r) o[r] = 0u;
-      if (nsub > 0) tmem_rows<R>(tbase + lane_base + 2 * kCols, o);
-      const float ls = reduce_rows<false, R>(l_part, lane);
-      const float lm = reduce_rows<true, R>(tm, lane);
-      if (lane % (32 / R) == 0) {
-        s_red[0][qd][lane / (32 / R)] = ls;
-        s_red[1][qd][lane / (32 / R)] = lm;
+      for (int r = 0; r < 2 * N; ++r) o[r] = 0u;
+      if (nsub > 0) tmem_rows<N, R>(tbase + lane_base + 2 * kCols + row0, o);
+      const float ls = reduce_rows<false, N>(l_part, lane);
+      const float lm = reduce_rows<true, N>(tm, lane);
+      if (lane % (32 / N) == 0) {
+        s_red[0][qd][row0 + lane / (32 / N)] = ls;
+        s_red[1][qd][row0 + lane / (32 / N)] = lm;
       }
-      named_bar_sync(1, 128);
+      named_bar_sync(bar, 128);
       const int ev = kk;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int hq = s_head[r];
+      for (int r = 0; r < N; ++r) {
+        const int hq = s_head[row0 + r];
         if (hq < 0) continue;
-        const float l = (s_red[0][0][r] + s_red[0][1][r]) + (s_red[0][2][r] + s_red[0][3][r]);
-        const float top = fmaxf(fmaxf(s_red[1][0][r], s_red[1][1][r]), fmaxf(s_red[1][2][r], s_red[1][3][r]));
+        const float l = (s_red[0][0][row0 + r] + s_red[0][1][row0 + r]) + (s_red[0][2][row0 + r] + s_red[0][3][row0 + r]);
+        const float top = fmaxf(fmaxf(s_red[1][0][row0 + r], s_red[1][1][row0 + r]), fmaxf(s_red[1][2][row0 + r], s_red[1][3][row0 + r]));
         // a row without a visible key (in this split) has l = 0: out 0 and lse
         // -inf, unless the caller promised there is none and there is one
         // split; NaN stays NaN
         const bool live = (a.rows_safe && p.splits == 1) || !(l == 0.0f);
         const float inv = live ? 1.0f / l : 0.0f;
         const float lse = live ? ((m_run[r] - kShift) + log2f(l)) * kLn2 : -INFINITY;
-        const int64_t row_id = (static_cast<int64_t>(b) * a.Hq + hq) * a.L + s_row[r];
-        const float val = fmaf(__uint_as_float(o[R + r]), 0.0625f, __uint_as_float(o[r])) * inv;
+        const int64_t row_id = (static_cast<int64_t>(b) * a.Hq + hq) * a.L + s_row[row0 + r];
+        const float val = fmaf(__uint_as_float(o[N + r]), 0.0625f, __uint_as_float(o[r])) * inv;
         if (p.splits == 1) {
           if (ev < a.Ev) {
-            const int64_t off = b * a.o_stride[0] + hq * a.o_stride[1] + s_row[r] * a.o_stride[2] + ev;
+            const int64_t off = b * a.o_stride[0] + hq * a.o_stride[1] + s_row[row0 + r] * a.o_stride[2] + ev;
             if (a.out_f32)
               static_cast<float*>(a.out)[off] = val;
             else
@@ -680,20 +690,33 @@ __global__ void __launch_bounds__(kThreads, Cfg<R>::kCtas)
 }
 
 // One CTA per query row: merge the splits' (o_s, lse_s, max_s), with
-// lse = ln sum e^(lse_s), o = sum e^(lse_s - lse) o_s.
-__global__ void __launch_bounds__(128) combine_fp8_kernel(const __grid_constant__ FwdArgs a, int splits,
-                                                          const float* ws_o, const float* ws_lse, const float* ws_max) {
+// lse = ln sum e^(lse_s), o = sum e^(lse_s - lse) o_s.  A warp takes every 8th
+// split, a lane four columns.
+constexpr int kCombineWarps = 8;
+__global__ void __launch_bounds__(32 * kCombineWarps)
+    combine_fp8_kernel(const __grid_constant__ FwdArgs a, int splits, const float* ws_o, const float* ws_lse,
+                       const float* ws_max) {
   __shared__ float s_w[kFp8MaxSplits];
-  __shared__ float s_m[4], s_t[4], s_sum[4];
-  // launched while the decode kernel still runs: wait for its results
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float s_m[kCombineWarps], s_t[kCombineWarps], s_sum[kCombineWarps];
+  __shared__ __align__(16) float s_o[kCombineWarps][128];
   const int64_t row_id = blockIdx.x;
   const int i = static_cast<int>(row_id % a.L), h = static_cast<int>((row_id / a.L) % a.Hq);
   const int b = static_cast<int>(row_id / (static_cast<int64_t>(a.L) * a.Hq));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // launched while the decode kernel still runs: wait for its results
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the first splits' outputs come with their weights still unknown
+  constexpr int kAhead = 4;
+  const float* src = ws_o + row_id * splits * a.Ev + 4 * lane;
+  float4 o[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    const int s = warp + u * kCombineWarps;
+    if (s < splits && 4 * lane < a.Ev) o[u] = *reinterpret_cast<const float4*>(src + static_cast<int64_t>(s) * a.Ev);
+  }
   float m = -INFINITY, top = -INFINITY;
   bool nan = false;
-  for (int s = threadIdx.x; s < splits; s += 128) {
+  for (int s = threadIdx.x; s < splits; s += 32 * kCombineWarps) {
     const float v = ws_lse[row_id * splits + s];
     s_w[s] = v;
     nan = nan || v != v;
@@ -701,36 +724,59 @@ __global__ void __launch_bounds__(128) combine_fp8_kernel(const __grid_constant_
     top = fmaxf(top, ws_max[row_id * splits + s]);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  for (int d = 16; d > 0; d >>= 1) {
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   }
   if (lane == 0) {
     s_m[warp] = m;
     s_t[warp] = top;
   }
   nan = __syncthreads_or(nan);
-  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  top = fmaxf(fmaxf(s_t[0], s_t[1]), fmaxf(s_t[2], s_t[3]));
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w) {
+    m = fmaxf(m, s_m[w]);
+    top = fmaxf(top, s_t[w]);
+  }
   const bool live = a.rows_safe || nan || m != -INFINITY;
   float sum = 0.0f;
-  for (int s = threadIdx.x; s < splits; s += 128) {
+  for (int s = threadIdx.x; s < splits; s += 32 * kCombineWarps) {
     const float w = live ? expf(s_w[s] - m) : 0.0f;
     s_w[s] = w;
     sum += w;
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
   if (lane == 0) s_sum[warp] = sum;
   __syncthreads();
-  sum = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+  sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kCombineWarps; ++w) sum += s_sum[w];
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto add = [&](const float4& v, float w) {
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
+  };
+  if (4 * lane < a.Ev) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int s = warp + u * kCombineWarps;
+      if (s < splits) add(o[u], s_w[s]);
+    }
+#pragma unroll 4
+    for (int s = warp + kAhead * kCombineWarps; s < splits; s += kCombineWarps)
+      add(*reinterpret_cast<const float4*>(src + static_cast<int64_t>(s) * a.Ev), s_w[s]);
+    *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = acc;
+  }
+  __syncthreads();
   const int ev = threadIdx.x;
   if (ev < a.Ev) {
-    const float* src = ws_o + row_id * splits * a.Ev + ev;
-    float acc = 0.0f;
-#pragma unroll 8
-    for (int s = 0; s < splits; ++s) acc = fmaf(s_w[s], src[static_cast<int64_t>(s) * a.Ev], acc);
-    const float val = live ? acc / sum : 0.0f;
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kCombineWarps; ++w) v += s_o[w][ev];
+    const float val = live ? v / sum : 0.0f;
     const int64_t off = b * a.o_stride[0] + h * a.o_stride[1] + i * a.o_stride[2] + ev;
     if (a.out_f32)
       static_cast<float*>(a.out)[off] = val;
@@ -854,7 +900,7 @@ cudaError_t launch_rows(const FwdArgs& a, const QuantArgs& qa, const Fp8Plan& p,
                                                  : decode_fp8_kernel<FA_SCORE_CAP_THEN_BIAS, R>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<R>::kSmemBytes);
   if (e != cudaSuccess) return e;
-  kern<<<dim3(a.Hkv * p.row_chunks, p.splits, a.B), kThreads, Cfg<R>::kSmemBytes, stream>>>(
+  kern<<<dim3(a.Hkv * p.row_chunks, p.splits, a.B), Cfg<R>::kThreads, Cfg<R>::kSmemBytes, stream>>>(
       a, qa, p, map_k, map_v, box, ws_o, ws_lse, ws_max);
   return cudaGetLastError();
 }
@@ -872,7 +918,7 @@ cudaError_t launch_decode_fp8(const FwdArgs& a, const QuantArgs& qa, const Fp8Pl
   if (e != cudaSuccess || p.splits == 1) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(rows));
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(32 * kCombineWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
