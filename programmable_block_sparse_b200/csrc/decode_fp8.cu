@@ -90,6 +90,9 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
 
+__device__ __forceinline__ void put_byte(uint32_t saddr, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
+}
 // Two values as (hi, lo) e4m3 pairs: v = hi + lo / 16.
 __device__ __forceinline__ void split_e4m3(float v0, float v1, uint32_t& hi, uint32_t& lo) {
   hi = __nv_cvt_float2_to_fp8x2(make_float2(v0, v1), __NV_SATFINITE, __NV_E4M3);
@@ -451,52 +454,64 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
     const float c_in = kCapped ? a.scale / a.score.cap : a.scale * kLog2e;
     const float c_out = kCapped ? a.score.cap * kLog2e : 1.0f;
     const bool want_max = a.max_scores != nullptr;
-    float m_run[N], l_part[N], tm[N], unit[N];
-    float sl2[N], sq2[N];  // distance bias in log2 units: slope, slope * q
+    // nms: kShift less the running maximum of t + log2 s^v, so that the weight
+    // of a key is 2^(t + log2 s^v + nms)
+    float2 nms[N / 2];
+    float tm[N];
+    float2 l_part[N / 2], unit[N / 2], sl2[N / 2], sq2[N / 2];  // distance bias in log2 units: slope, slope * q
 #pragma unroll
-    for (int r = 0; r < N; ++r) {
-      m_run[r] = kNoKeyMax;
-      l_part[r] = 0.0f;
-      tm[r] = -INFINITY;
-      unit[r] = s_unit[row0 + r] * c_in;
-      sl2[r] = s_slope[row0 + r] * kLog2e;
-      sq2[r] = sl2[r] * static_cast<float>(s_qpos[row0 + r]);
+    for (int r = 0; r < N; ++r) tm[r] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const int r = row0 + 2 * i;
+      nms[i] = splat2(-kNoKeyMax);
+      l_part[i] = make_float2(0.0f, 0.0f);
+      unit[i] = make_float2(s_unit[r] * c_in, s_unit[r + 1] * c_in);
+      sl2[i] = make_float2(s_slope[r] * kLog2e, s_slope[r + 1] * kLog2e);
+      sq2[i] = make_float2(-sl2[i].x * static_cast<float>(s_qpos[r]), -sl2[i].y * static_cast<float>(s_qpos[r + 1]));
     }
-    // This key's scales, loaded a tile ahead, its page two tiles ahead (the
-    // two loads depend on one another).
-    auto key_of = [&](int j) { return listed_tile(a, brow, nfull, t0 + j) * kKeys + kk; };
-    auto page_of = [&](int j) {  // -1 past the sequence's end
-      if (j >= nsub) return -1;
-      const int kv = key_of(j);
+    // where this key's weights go, by row of an 8-row group (row 4 of 4 rows is
+    // the first lo row)
+    uint32_t wx[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+      wx[r] = smem_u32(sP) + (row0 >> 3) * 1024 + r * 128 + (((kk >> 4) ^ r) << 4) + (kk & 15);
+    // What the next tiles need comes ahead, a stage an iteration, since each
+    // load depends on the one before: tile index, page, scales.
+    auto page_of = [&](int kv) {  // -1 past the sequence's end
       if (kv >= S_b) return -1;
       if (!a.page_table) return b;
       const int pg = __ldg(a.page_table + static_cast<int64_t>(b) * a.pages_per_seq + p.page.quotient(kv));
       return min(max(pg, 0), a.num_pages - 1);  // warp 0 records an id outside the pool
     };
-    auto scales_of = [&](int j, int pg, float& ks, float& vs) {
+    auto scales_of = [&](int kv, int pg, float& ks, float& vs) {
       ks = vs = 1.0f;
       if (pg < 0) return;
-      const int kv = key_of(j), at = a.page_table ? kv - p.page.quotient(kv) * a.page_size : kv;
+      const int at = a.page_table ? kv - p.page.quotient(kv) * a.page_size : kv;
       const int64_t i = (static_cast<int64_t>(pg) * a.Hkv + hk) * qa.scales_per_outer + (at >> qa.block_log);
       ks = __ldg(qa.k_scale + i);
       vs = __ldg(qa.v_scale + i);
     };
-    float ks_n, vs_n;
-    scales_of(0, page_of(0), ks_n, vs_n);
-    int pg_n = page_of(1);
+    auto first_key = [&](int j) { return j < nsub ? listed_tile(a, brow, nfull, t0 + j) * kKeys : 0; };
+    int kv0 = first_key(0), kv0_1 = first_key(1), kv0_2 = first_key(2);
+    float ks, vs, ks_1 = 1.0f, vs_1 = 1.0f;
+    scales_of(kv0 + kk, nsub > 0 ? page_of(kv0 + kk) : -1, ks, vs);
+    int pg_1 = nsub > 1 ? page_of(kv0_1 + kk) : -1;
     bool alive = true;
     for (int j = 0; j < nsub; ++j) {
       const int sb = j & 1;
-      const int jt = t0 + j;
-      const int kv0 = listed_tile(a, brow, nfull, jt) * kKeys, kv = kv0 + kk;
-      const float ks = ks_n, vs = fmaxf(vs_n, 7.888609052210118e-31f);  // 2^-100: a block of zeros has scale 0
-      scales_of(j + 1, pg_n, ks_n, vs_n);
-      pg_n = page_of(j + 2);
-      const float lv = log2f(vs), ivs = 1.0f / vs;
+      const int kv = kv0 + kk;
+      if (j + 1 < nsub) scales_of(kv0_1 + kk, pg_1, ks_1, vs_1);
+      const int pg_2 = j + 2 < nsub ? page_of(kv0_2 + kk) : -1;
+      const int kv0_3 = first_key(j + 3);
+      vs = fmaxf(vs, 7.888609052210118e-31f);  // 2^-100: a block of zeros has scale 0
+      float lv, ivs;  // exact for powers of two; other errors, 2^-21, cancel but between blocks
+      asm("lg2.approx.f32 %0, %1;" : "=f"(lv) : "f"(vs));
+      asm("rcp.approx.f32 %0, %1;" : "=f"(ivs) : "f"(vs));
       bool ok = alive && __all_sync(0xffffffffu, mbar_wait(&bars.s_full[sb], (j >> 1) & 1, abort, a.status,
                                                            a.wait_cycles));
-      float t[N];  // score + log2 of the value scale
-      bool grow = false;
+      float2 t[N / 2];  // score + log2 s^v
+      float top = -INFINITY;  // of the weights' exponents
       if (ok) {
         uint32_t sr[2 * N];
         tc_fence_after();
@@ -504,75 +519,98 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.s_free[sb]);
+        const float2 kfac = splat2(ks), lv2 = splat2(lv);
+        const float kvf = static_cast<float>(kv);
+        const int pk = has_pos ? pos_at(a.score, b, kv, a.S) : kv;
 #pragma unroll
-        for (int r = 0; r < N; ++r)
-          t[r] = fmaf(__uint_as_float(sr[N + r]), 0.0625f, __uint_as_float(sr[r])) * (unit[r] * ks);
+        for (int i = 0; i < N / 2; ++i) {
+          const float2 hi = make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]));
+          const float2 lo = make_float2(__uint_as_float(sr[N + 2 * i]), __uint_as_float(sr[N + 2 * i + 1]));
+          const float2 x = fma2(lo, splat2(0.0625f), hi), f = mul2(unit[i], kfac);
+          if constexpr (SCORE == FA_SCORE_NONE)
+            t[i] = fma2(x, f, lv2);
+          else if constexpr (SCORE == FA_SCORE_ALIBI)
+            t[i] = add2(fma2(x, f, fma2(sl2[i], splat2(kvf), sq2[i])), lv2);
+          else
+            t[i] = mul2(x, f);
+        }
         if constexpr (kCapped) {
-          float th[N];
-          bool big = false;
+          float2 th[N / 2];
+          float big = 0.0f;
+          bool nan = false;
 #pragma unroll
           for (int i = 0; i < N / 2; ++i) {
             float2 u2;
-            const float2 v2 = tanh_poly2(make_float2(t[2 * i], t[2 * i + 1]), u2);
-            th[2 * i] = v2.x;
-            th[2 * i + 1] = v2.y;
-            big |= !(fmaxf(u2.x, u2.y) <= kTanhPolyMax * kTanhPolyMax);
+            th[i] = tanh_poly2(t[i], u2);
+            big = max3f(big, u2.x, u2.y);
+            nan = nan || !(u2.x + u2.y == u2.x + u2.y);
           }
-          if (__any_sync(0xffffffffu, big)) {
+          if (__any_sync(0xffffffffu, nan || big > kTanhPolyMax * kTanhPolyMax)) {
 #pragma unroll
-            for (int r = 0; r < N; ++r)
-              if (!(fabsf(t[r]) <= kTanhPolyMax)) th[r] = tanh_large(t[r]);
+            for (int i = 0; i < N / 2; ++i) {
+              if (!(fabsf(t[i].x) <= kTanhPolyMax)) th[i].x = tanh_large(t[i].x);
+              if (!(fabsf(t[i].y) <= kTanhPolyMax)) th[i].y = tanh_large(t[i].y);
+            }
           }
 #pragma unroll
-          for (int r = 0; r < N; ++r) t[r] = th[r] * c_out;
-        }
-        if constexpr (SCORE == FA_SCORE_ALIBI) {
-          const float kvf = static_cast<float>(kv);
-#pragma unroll
-          for (int r = 0; r < N; ++r) t[r] += fmaf(sl2[r], kvf, -sq2[r]);
-        }
-        if constexpr (SCORE == FA_SCORE_CAP_THEN_BIAS) {
-          const int pk = has_pos ? pos_at(a.score, b, kv, a.S) : kv;
-#pragma unroll
-          for (int r = 0; r < N; ++r) {
-            const int d = has_pos ? pk - s_pq[row0 + r] : kv - s_qpos[row0 + r];
-            t[r] = fmaf(sl2[r], static_cast<float>(d), t[r]);
+          for (int i = 0; i < N / 2; ++i) {
+            t[i] = fma2(th[i], splat2(c_out), lv2);
+            if constexpr (SCORE == FA_SCORE_CAP_THEN_BIAS) {
+              const int r = row0 + 2 * i;
+              const int d0 = has_pos ? pk - s_pq[r] : kv - s_qpos[r], d1 = has_pos ? pk - s_pq[r + 1] : kv - s_qpos[r + 1];
+              t[i] = fma2(sl2[i], make_float2(static_cast<float>(d0), static_cast<float>(d1)), t[i]);
+            }
           }
         }
         // element mask on listed-partial tiles and at the end of the sequence
-        if (jt >= nfull || kv0 + kKeys > S_b) {
+        if (t0 + j >= nfull || kv0 + kKeys > S_b) {
 #pragma unroll
           for (int r = 0; r < N; ++r)
-            if (s_head[row0 + r] < 0 || !mask_visible(a.mask, b, s_head[row0 + r], s_qpos[row0 + r], kv, S_b, a.S)) t[r] = -INFINITY;
+            if (s_head[row0 + r] < 0 ||
+                !mask_visible(a.mask, b, s_head[row0 + r], s_qpos[row0 + r], kv, S_b, a.S)) {
+              if (r & 1)
+                t[r >> 1].y = -INFINITY;
+              else
+                t[r >> 1].x = -INFINITY;
+            }
         }
-        if (want_max) {
 #pragma unroll
-          for (int r = 0; r < N; ++r) tm[r] = fmaxf(tm[r], t[r]);
-        }
-#pragma unroll
-        for (int r = 0; r < N; ++r) {
-          t[r] += lv;
-          grow |= t[r] > m_run[r] + kSlack;
+        for (int i = 0; i < N / 2; ++i) {
+          if (want_max) {
+            tm[2 * i] = fmaxf(tm[2 * i], t[i].x - lv);
+            tm[2 * i + 1] = fmaxf(tm[2 * i + 1], t[i].y - lv);
+          }
+          const float2 d = add2(t[i], nms[i]);
+          top = max3f(top, d.x, d.y);
         }
       }
       // one vote per tile: as usual, or a wait gave up, or a maximum moves
-      if (named_bar_or(bar, 128, !ok || grow)) {
+      if (named_bar_or(bar, 128, !ok || top > kSlack + kShift)) {
         if (named_bar_or(bar, 128, !ok)) {
           alive = false;
           break;
         }
-        const float v = reduce_rows<true, N>(t, lane);
+        float tv[N];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+          tv[2 * i] = t[i].x;
+          tv[2 * i + 1] = t[i].y;
+        }
+        const float v = reduce_rows<true, N>(tv, lane);
         if (lane % (32 / N) == 0) s_red[0][qd][row0 + lane / (32 / N)] = v;
         named_bar_sync(bar, 128);
         float alpha[N];
 #pragma unroll
         for (int r = 0; r < N; ++r) {
-          const float tmax = fmaxf(fmaxf(s_red[0][0][row0 + r], s_red[0][1][row0 + r]), fmaxf(s_red[0][2][row0 + r], s_red[0][3][row0 + r]));
-          const float mn = fmaxf(m_run[r], tmax);
-          alpha[r] = ex2_approx(m_run[r] - mn);
-          m_run[r] = mn;
-          l_part[r] *= alpha[r];
+          const float tmax = fmaxf(fmaxf(s_red[0][0][row0 + r], s_red[0][1][row0 + r]),
+                                   fmaxf(s_red[0][2][row0 + r], s_red[0][3][row0 + r]));
+          float& mine = (r & 1) ? nms[r >> 1].y : nms[r >> 1].x;
+          const float now = fminf(mine, kShift - tmax);
+          alpha[r] = ex2_approx(now - mine);
+          mine = now;
         }
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) l_part[i] = mul2(l_part[i], make_float2(alpha[2 * i], alpha[2 * i + 1]));
         named_bar_sync(bar, 128);  // s_red is read by all before its next use
         if (j > 0) {
           // O^T holds tiles 0 .. j-1: once the last of them is in, rescale
@@ -609,27 +647,31 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
         }
       }
       if (alive) {
-        uint8_t* pbuf = sP + sb * C::kOpBytes + (kk & 15);
-        const int ch = kk >> 4;
-        auto place = [&](int row) { return (row >> 3) * 1024 + (row & 7) * 128 + ((ch ^ (row & 7)) << 4); };
+        // 4 rows: hi and lo share an 8-row group; else lo is R rows further on
+        constexpr int kLoBytes = R == 4 ? 0 : R * 128, kLoRow = R == 4 ? 4 : 0;
 #pragma unroll
-        for (int r = 0; r < N; r += 2) {
-          const int row = row0 + r;
-          const float w0 = ex2_approx(t[r] - (m_run[r] - kShift)), w1 = ex2_approx(t[r + 1] - (m_run[r + 1] - kShift));
-          l_part[r] = fmaf(w0, ivs, l_part[r]);
-          l_part[r + 1] = fmaf(w1, ivs, l_part[r + 1]);
+        for (int i = 0; i < N / 2; ++i) {
+          const float2 d = add2(t[i], nms[i]);
+          const float2 w = make_float2(ex2_approx(d.x), ex2_approx(d.y));
+          l_part[i] = fma2(w, splat2(ivs), l_part[i]);
           uint32_t hi, lo;
-          split_e4m3(w0, w1, hi, lo);
-          pbuf[place(row)] = static_cast<uint8_t>(hi);
-          pbuf[place(row + 1)] = static_cast<uint8_t>(hi >> 8);
-          pbuf[place(R + row)] = static_cast<uint8_t>(lo);
-          pbuf[place(R + row + 1)] = static_cast<uint8_t>(lo >> 8);
+          split_e4m3(w.x, w.y, hi, lo);
+          put_byte(wx[2 * i] + sb * C::kOpBytes, hi);
+          put_byte(wx[2 * i + 1] + sb * C::kOpBytes, hi >> 8);
+          put_byte(wx[2 * i + kLoRow] + sb * C::kOpBytes + kLoBytes, lo);
+          put_byte(wx[2 * i + 1 + kLoRow] + sb * C::kOpBytes + kLoBytes, lo >> 8);
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_full[sb]);
       }
+      kv0 = kv0_1;
+      kv0_1 = kv0_2;
+      kv0_2 = kv0_3;
+      ks = ks_1;
+      vs = vs_1;
+      pg_1 = pg_2;
     }
     // every softmax thread arrives here together (the loop is left only
     // through the vote, or at its end)
@@ -642,7 +684,13 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
 #pragma unroll
       for (int r = 0; r < 2 * N; ++r) o[r] = 0u;
       if (nsub > 0) tmem_rows<N, R>(tbase + lane_base + 2 * kCols + row0, o);
-      const float ls = reduce_rows<false, N>(l_part, lane);
+      float lp[N];
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        lp[2 * i] = l_part[i].x;
+        lp[2 * i + 1] = l_part[i].y;
+      }
+      const float ls = reduce_rows<false, N>(lp, lane);
       const float lm = reduce_rows<true, N>(tm, lane);
       if (lane % (32 / N) == 0) {
         s_red[0][qd][row0 + lane / (32 / N)] = ls;
@@ -661,7 +709,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
         // split; NaN stays NaN
         const bool live = (a.rows_safe && p.splits == 1) || !(l == 0.0f);
         const float inv = live ? 1.0f / l : 0.0f;
-        const float lse = live ? ((m_run[r] - kShift) + log2f(l)) * kLn2 : -INFINITY;
+        const float lse = live ? (log2f(l) - ((r & 1) ? nms[r >> 1].y : nms[r >> 1].x)) * kLn2 : -INFINITY;
         const int64_t row_id = (static_cast<int64_t>(b) * a.Hq + hq) * a.L + s_row[row0 + r];
         const float val = fmaf(__uint_as_float(o[N + r]), 0.0625f, __uint_as_float(o[r])) * inv;
         if (p.splits == 1) {
