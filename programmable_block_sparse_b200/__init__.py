@@ -457,35 +457,52 @@ def flexattn_backward(q, k, v, out, dout, lse, block_mask, q_side=None, score_mo
 # ---------------------------------------------------------------------------
 # Query / key preparation, cache writes and attention over an e4m3 cache
 # ---------------------------------------------------------------------------
-# These calls are made once a layer and token, so their structs are packed in
-# one go (a ctypes constructor takes three times as long).
+# These calls are made once a layer and token, and some of their kernels take
+# less time than a Python function that builds ctypes structs one by one: all
+# structs of a call are packed into one buffer, at fixed places.
+_PACK_TENSOR = struct.Struct("Qii4q4q").pack_into
+_PACK_NORM = struct.Struct("Qif").pack_into
+_PACK_ROPE = struct.Struct("QQiiii").pack_into
+_PACK_QUANT = struct.Struct("QQii").pack_into
+_PACK_CACHE = struct.Struct("5Qii").pack_into
+_PACK_MASK = struct.Struct("8i4Q").pack_into
+_PACK_OPTIONS = struct.Struct("QqiiQii").pack_into
+_TENSOR, _NORM, _ROPE, _QUANT = 80, 16, 32, 24  # bytes
+_addressof = C.addressof
 _DTYPES = {}
-_PACK_TENSOR = struct.Struct("Qii4q4q").pack
-_PACK_NORM = struct.Struct("Qif").pack
-_PACK_ROPE = struct.Struct("QQiiii").pack
-_PACK_QUANT = struct.Struct("QQii").pack
-_byref = C.byref
+_torch = None
 
 
-def _dtype_codes():
-    if not _DTYPES:
+def _load_torch():
+    """torch, with the element types' codes known."""
+    global _torch
+    if _torch is None:
         import torch
         _DTYPES.update({torch.bfloat16: _abi.FA_DTYPE_BF16, torch.float32: _abi.FA_DTYPE_F32,
                         torch.float8_e4m3fn: _abi.FA_DTYPE_E4M3})
-    return _DTYPES
+        _torch = torch
+    return _torch
 
 
-def _device_tensor(t, name, device):
-    """``t`` as an fa_tensor; it has to be 4-D and on ``device``, a CUDA device."""
-    code = _dtype_codes().get(t.dtype)
+def _cuda_device(t, name):
+    if t.dtype not in _DTYPES:
+        raise FlexAttnError(6, f"{name}: unsupported dtype {t.dtype}")
+    dev = t.device
+    if dev.type != "cuda":
+        raise FlexAttnError(9, f"{name} is on {dev}, expected a CUDA device")
+    return dev
+
+
+def _pack_tensor(buf, at, t, name, device):
+    """``t`` as the fa_tensor at byte ``at`` of ``buf``; it has to be 4-D and on ``device``."""
+    code = _DTYPES.get(t.dtype)
     if code is None:
         raise FlexAttnError(6, f"{name}: unsupported dtype {t.dtype}")
-    shape = t.shape
-    if len(shape) != 4:
-        raise FlexAttnError(2, f"{name}: expected a 4-D tensor, got shape {tuple(shape)}")
-    if t.device != device or not t.is_cuda:
-        raise FlexAttnError(9, f"{name} is on {t.device}, expected {device if device.type == 'cuda' else 'a CUDA device'}")
-    return _abi.fa_tensor.from_buffer_copy(_PACK_TENSOR(t.data_ptr(), code, 0, *shape, *t.stride()))
+    if t.device != device:
+        raise FlexAttnError(9, f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 4:
+        raise FlexAttnError(2, f"{name}: expected a 4-D tensor, got shape {tuple(t.shape)}")
+    _PACK_TENSOR(buf, at, t.data_ptr(), code, 0, *t.shape, *t.stride())
 
 
 def _device_array(t, name, dtype, shape, device):
@@ -502,20 +519,23 @@ def _device_array(t, name, dtype, shape, device):
     return t.data_ptr()
 
 
-def _norm_struct(spec, name, D, device):
+def _pack_norm(buf, at, spec, name, D, device):
+    """The fa_head_norm at ``at``; its address, or None without a spec."""
     if spec is None:
         return None
     w = spec.get("weight")
     if w is None:
-        return _abi.fa_head_norm(None, _abi.FA_DTYPE_F32, float(spec.get("eps", 1e-6)))
-    return _abi.fa_head_norm.from_buffer_copy(_PACK_NORM(
-        _device_array(w, name, w.dtype, (D,), device), _dtype_codes().get(w.dtype, -1), spec.get("eps", 1e-6)))
+        _PACK_NORM(buf, at, 0, _abi.FA_DTYPE_F32, spec.get("eps", 1e-6))
+    else:
+        _PACK_NORM(buf, at, _device_array(w, name, w.dtype, (D,), device), _DTYPES.get(w.dtype, -1),
+                   spec.get("eps", 1e-6))
+    return _addressof(buf) + at
 
 
-def _rope_struct(spec, B, N, device):
+def _pack_rope(buf, at, spec, B, N, device):
     if spec is None:
         return None
-    import torch
+    torch = _torch
     f = spec["inv_freq"]
     half = f.numel()
     ptr = rows = 0
@@ -525,29 +545,24 @@ def _rope_struct(spec, B, N, device):
         if rows != 1 and rows != B:
             raise FlexAttnError(4, f"rope pos: {rows} rows, expected 1 or {B}")
         ptr = _device_array(pos, "rope pos", torch.int32, (rows, N) if pos.dim() == 2 else (N,), device)
-    return _abi.fa_rope.from_buffer_copy(_PACK_ROPE(
-        _device_array(f, "inv_freq", torch.float32, (half,), device), ptr, 2 * half,
-        1 if spec.get("interleaved") else 0, rows, 0))
-
-
-def _ref(s):
-    return None if s is None else _byref(s)
+    _PACK_ROPE(buf, at, _device_array(f, "inv_freq", torch.float32, (half,), device), ptr, 2 * half,
+               1 if spec.get("interleaved") else 0, rows, 0)
+    return _addressof(buf) + at
 
 
 def _empty_like(t, dtype=None):
     """A new contiguous tensor of t's shape on its device."""
-    import torch
-    return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+    return _torch.empty_like(t, dtype=dtype, memory_format=_torch.contiguous_format)
 
 
 def _call(device, stream, fn, *args):
     """``fn(*args, stream)`` with ``device`` current; ``stream`` None is that device's current stream."""
-    import torch
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
+    cuda = _torch.cuda
+    if cuda.current_device() != device.index:
+        with cuda.device(device):
             return _call(device, stream, fn, *args)
     if stream is None:
-        handle = torch.cuda.current_stream().cuda_stream
+        handle = cuda.current_stream().cuda_stream
     else:
         handle = stream if isinstance(stream, int) else stream.cuda_stream
     status = fn(*args, handle)
@@ -555,31 +570,41 @@ def _call(device, stream, fn, *args):
         _check(status)
 
 
+_PrepBuffer = C.c_char * (4 * _TENSOR + 2 * _NORM + _ROPE)
+
+
 def flexattn_qk_norm_rope(q, k, q_norm=None, k_norm=None, rope=None, q_out=None, k_out=None, stream=None):
     """Norm (per head) and rotation of queries (B, Hq, N, D) and keys
     (B, Hkv, N, D) in one pass; returns ``(q_out, k_out)``.  Either of q, k
     may be None; the outputs may be preallocated, or the inputs themselves."""
+    _load_torch()
     x = q if q is not None else k
     if x is None:
         raise FlexAttnError(1, "q and k are both None")
-    dev = x.device
-    qs = ks = qo = ko = None
+    dev = _cuda_device(x, "q" if q is not None else "k")
+    buf = _PrepBuffer()
+    base = _addressof(buf)
+    pq = pqo = pk = pko = None
     if q is not None:
-        qs = _device_tensor(q, "q", dev)
+        _pack_tensor(buf, 0, q, "q", dev)
         if q_out is None:
             q_out = _empty_like(q)
-        qo = _device_tensor(q_out, "q_out", dev)
+        _pack_tensor(buf, 80, q_out, "q_out", dev)
+        pq, pqo = base, base + 80
     if k is not None:
-        ks = _device_tensor(k, "k", dev)
+        _pack_tensor(buf, 160, k, "k", dev)
         if k_out is None:
             k_out = _empty_like(k)
-        ko = _device_tensor(k_out, "k_out", dev)
+        _pack_tensor(buf, 240, k_out, "k_out", dev)
+        pk, pko = base + 160, base + 240
     B, _, N, D = x.shape
-    qn, kn = _norm_struct(q_norm, "q_norm", D, dev), _norm_struct(k_norm, "k_norm", D, dev)
-    rp = _rope_struct(rope, B, N, dev)
-    _call(dev, stream, load_library().flexattn_qk_norm_rope, _ref(qs), _ref(ks), _ref(qo), _ref(ko), _ref(qn),
-          _ref(kn), _ref(rp))
+    _call(dev, stream, (_LIB or load_library()).flexattn_qk_norm_rope, pq, pk, pqo, pko,
+          _pack_norm(buf, 320, q_norm, "q_norm weight", D, dev), _pack_norm(buf, 336, k_norm, "k_norm weight", D, dev),
+          _pack_rope(buf, 352, rope, B, N, dev))
     return q_out, k_out
+
+
+_PrepBwdBuffer = C.c_char * (6 * _TENSOR + 2 * _NORM + _ROPE)
 
 
 def flexattn_qk_norm_rope_backward(q, k, dq_out, dk_out, q_norm=None, k_norm=None, rope=None, dq=None, dk=None,
@@ -589,39 +614,57 @@ def flexattn_qk_norm_rope_backward(q, k, dq_out, dk_out, q_norm=None, k_norm=Non
     inputs (needed where that side has a norm).  The weight gradients are fp32
     (D,) tensors, None without a norm or with ``weight_grads=False``; dq and dk
     are allocated in ``grad_dtype`` (default: the output gradient's type)."""
-    import torch
+    torch = _load_torch()
     g = dq_out if dq_out is not None else dk_out
     if g is None:
         raise FlexAttnError(1, "dq_out and dk_out are both None")
-    dev = g.device
+    dev = _cuda_device(g, "dq_out" if dq_out is not None else "dk_out")
     B, _, N, D = g.shape
+    lib = _LIB or load_library()
+    buf = _PrepBwdBuffer()
+    base = _addressof(buf)
+    # both weight gradients lie in one allocation
+    want_q = dq_out is not None and q_norm is not None and weight_grads
+    want_k = dk_out is not None and k_norm is not None and weight_grads
+    dqw = dkw = None
+    if want_q or want_k:
+        both = torch.empty((2, D), dtype=torch.float32, device=dev)
+        dqw, dkw = both[0] if want_q else None, both[1] if want_k else None
+        if workspace is None:
+            n = C.c_size_t()
+            _check(lib.flexattn_qk_norm_rope_backward_workspace_size(D, 1, C.byref(n)))
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
 
-    def side(x, dy, dx, norm, name):
-        xs = None if x is None or norm is None else _device_tensor(x, name, dev)
-        if dy is None:
-            return xs, None, None, None, None
-        if dx is None:
-            dx = _empty_like(dy, grad_dtype)
-        dw = torch.empty(D, dtype=torch.float32, device=dev) if norm is not None and weight_grads else None
-        return xs, _device_tensor(dy, f"d{name}_out", dev), _device_tensor(dx, f"d{name}", dev), dx, dw
+    def side(at, x, dy, dx, norm, name):
+        px = pg = po = None
+        if x is not None and norm is not None:
+            _pack_tensor(buf, at, x, name, dev)
+            px = base + at
+        if dy is not None:
+            if dx is None:
+                dx = _empty_like(dy, grad_dtype)
+            _pack_tensor(buf, at + 80, dy, f"d{name}_out", dev)
+            _pack_tensor(buf, at + 160, dx, f"d{name}", dev)
+            pg, po = base + at + 80, base + at + 160
+        return px, pg, po, dx
 
-    qs, gq, oq, dq, dqw = side(q, dq_out, dq, q_norm, "q")
-    ks, gk, ok, dk, dkw = side(k, dk_out, dk, k_norm, "k")
-    qn, kn = _norm_struct(q_norm, "q_norm", D, dev), _norm_struct(k_norm, "k_norm", D, dev)
-    rp = _rope_struct(rope, B, N, dev)
-    lib = load_library()
-    if workspace is None and (dqw is not None or dkw is not None):
-        n = C.c_size_t()
-        _check(lib.flexattn_qk_norm_rope_backward_workspace_size(D, 1, C.byref(n)))
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
-    _call(dev, stream, lib.flexattn_qk_norm_rope_backward, _ref(qs), _ref(ks), _ref(gq), _ref(gk), _ref(oq), _ref(ok),
-          _ptr(dqw), _ptr(dkw), _ref(qn), _ref(kn), _ref(rp), _ptr(workspace),
-          C.c_size_t(workspace.numel() * workspace.element_size() if workspace is not None else 0))
+    pq, pgq, poq, dq = side(0, q, dq_out, dq, q_norm, "q")
+    pk, pgk, pok, dk = side(240, k, dk_out, dk, k_norm, "k")
+    _call(dev, stream, lib.flexattn_qk_norm_rope_backward, pq, pk, pgq, pgk, poq, pok,
+          None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(),
+          _pack_norm(buf, 480, q_norm, "q_norm weight", D, dev), _pack_norm(buf, 496, k_norm, "k_norm weight", D, dev),
+          _pack_rope(buf, 512, rope, B, N, dev), None if workspace is None else workspace.data_ptr(),
+          0 if workspace is None else workspace.numel() * workspace.element_size())
     return dq, dk, dqw, dkw
 
 
 def _scale_shape(pool, scale_block):
-    return (pool.shape[0], pool.shape[1], -(-pool.shape[2] // max(1, scale_block)))
+    shape = pool.shape
+    return (shape[0], shape[1], -(-shape[2] // scale_block) if scale_block > 0 else 0)
+
+
+_CACHE_BYTES = 2 * _TENSOR + 48
+_AppendBuffer = C.c_char * (_CACHE_BYTES + 4 * _TENSOR + 2 * _NORM + _ROPE)
 
 
 def flexattn_cache_append(k, v, cache, k_norm=None, rope=None, q=None, q_norm=None, q_out=None, stream=None):
@@ -629,65 +672,79 @@ def flexattn_cache_append(k, v, cache, k_norm=None, rope=None, q=None, q_norm=No
     (updated in place), keys normed and rotated on the way; with ``q``, the
     queries of the same tokens go the same way into ``q_out``, which is
     returned (None without q)."""
-    import torch
-    dev = k.device
-    ks, vs = _device_tensor(k, "k", dev), _device_tensor(v, "v", dev)
+    torch = _load_torch()
+    dev = _cuda_device(k, "k")
     B, _, N, E = k.shape
-    kp, vp = cache["k"], cache["v"]
-    c = _abi.fa_kv_cache()
-    c.k, c.v = _device_tensor(kp, "cache k", dev), _device_tensor(vp, "cache v", dev)
-    c.cache_len = _device_array(cache["cache_len"], "cache_len", torch.int32, (B,), dev)
-    if cache.get("new_len") is not None:
-        c.new_len = _device_array(cache["new_len"], "new_len", torch.int32, (B,), dev)
-    table = cache.get("page_table")
+    buf = _AppendBuffer()
+    base = _addressof(buf)
+    kp, vp, get = cache["k"], cache["v"], cache.get
+    int32 = torch.int32
+    _pack_tensor(buf, 0, kp, "cache k", dev)
+    _pack_tensor(buf, 80, vp, "cache v", dev)
+    table, new_len, ks, vs = get("page_table"), get("new_len"), get("k_scale"), get("v_scale")
+    pages = block = 0
+    ptable = pnew = pks = pvs = 0
     if table is not None:
-        c.page_table = _device_array(table, "page_table", torch.int32, (B, table.shape[-1]), dev)
-        c.pages_per_seq = table.shape[-1]
-    if cache.get("k_scale") is not None or cache.get("v_scale") is not None:
-        n = int(cache.get("scale_block", 0))
-        c.scale_block = n
-        for name, pool in (("k_scale", kp), ("v_scale", vp)):
-            if cache.get(name) is not None:
-                setattr(c, name, _device_array(cache[name], name, torch.float32, _scale_shape(pool, n), dev))
-    qs = qo = None
+        pages = table.shape[-1]
+        ptable = _device_array(table, "page_table", int32, (B, pages), dev)
+    if new_len is not None:
+        pnew = _device_array(new_len, "new_len", int32, (B,), dev)
+    if ks is not None or vs is not None:
+        block = int(get("scale_block", 0))
+        if ks is not None:
+            pks = _device_array(ks, "k_scale", torch.float32, _scale_shape(kp, block), dev)
+        if vs is not None:
+            pvs = _device_array(vs, "v_scale", torch.float32, _scale_shape(vp, block), dev)
+    _PACK_CACHE(buf, 160, ptable, _device_array(cache["cache_len"], "cache_len", int32, (B,), dev), pnew, pks, pvs,
+                pages, block)
+    _pack_tensor(buf, 208, k, "k", dev)
+    _pack_tensor(buf, 288, v, "v", dev)
+    pq = pqo = None
     if q is not None:
-        qs = _device_tensor(q, "q", dev)
+        _pack_tensor(buf, 368, q, "q", dev)
         if q_out is None:
             q_out = _empty_like(q)
-        qo = _device_tensor(q_out, "q_out", dev)
-    kn = _norm_struct(k_norm, "k_norm", E, dev)
-    qn = _norm_struct(q_norm, "q_norm", E, dev)
-    rp = _rope_struct(rope, B, N, dev)
-    _call(dev, stream, load_library().flexattn_cache_append, C.byref(ks), C.byref(vs), C.byref(c), _ref(kn), _ref(rp),
-          _ref(qs), _ref(qo), _ref(qn))
+        _pack_tensor(buf, 448, q_out, "q_out", dev)
+        pq, pqo = base + 368, base + 448
+    _call(dev, stream, (_LIB or load_library()).flexattn_cache_append, base + 208, base + 288, base,
+          _pack_norm(buf, 528, k_norm, "k_norm weight", E, dev), _pack_rope(buf, 560, rope, B, N, dev), pq, pqo,
+          _pack_norm(buf, 544, q_norm, "q_norm weight", E, dev))
     return q_out
 
 
-def _quant_struct(quant, k, v, device):
-    import torch
+_Fp8Buffer = C.c_char * (4 * _TENSOR + _QUANT + 64 + 40 + 8)
+
+
+def _pack_fp8(buf, q, k, v, block_mask, quant, paged, dev):
+    """q, k, v at 0, 80, 160, quant at 320, the block mask at 344; (page table, page size, columns)."""
+    torch = _torch
+    _pack_tensor(buf, 0, q, "q", dev)
+    _pack_tensor(buf, 80, k, "k", dev)
+    _pack_tensor(buf, 160, v, "v", dev)
     n = int(quant["scale_block"])
-    return _abi.fa_kv_quant.from_buffer_copy(_PACK_QUANT(
-        _device_array(quant["k_scale"], "k_scale", torch.float32, _scale_shape(k, n), device),
-        _device_array(quant["v_scale"], "v_scale", torch.float32, _scale_shape(v, n), device), n, 0))
-
-
-def _paged_checked(paged, B, device):
-    import torch
-    if paged is not None:
-        t = paged["page_table"]
-        _device_array(t, "page_table", torch.int32, (B, t.shape[-1]), device)
-    return paged
+    _PACK_QUANT(buf, 320, _device_array(quant["k_scale"], "k_scale", torch.float32, _scale_shape(k, n), dev),
+                _device_array(quant["v_scale"], "v_scale", torch.float32, _scale_shape(v, n), dev), n, 0)
+    m = block_mask
+    _PACK_MASK(buf, 344, m.B, m.H, m.L, m.S, m.BM, m.BN, m.Mb, m.Nb, m.kv_num_blocks.data_ptr(),
+               m.kv_indices.data_ptr(), m.full_kv_num_blocks.data_ptr(), m.full_kv_indices.data_ptr())
+    if paged is None:
+        return 0, 0, 0
+    t = paged["page_table"]
+    return (_device_array(t, "page_table", torch.int32, (q.shape[0], t.shape[-1]), dev), int(paged["page_size"]),
+            t.shape[-1])
 
 
 def flexattn_forward_fp8_workspace_size(q, k, v, block_mask, quant, split_kv=0, paged=None):
     """Workspace bytes of :func:`flexattn_forward_fp8` for these arguments (0: none)."""
-    dev = q.device
-    qs, ks, vs = _device_tensor(q, "q", dev), _device_tensor(k, "k", dev), _device_tensor(v, "v", dev)
-    qt, bm = _quant_struct(quant, k, v, dev), block_mask.as_struct()
-    opts = _options_struct(None, False, 0, _paged_checked(paged, q.shape[0], dev))
+    _load_torch()
+    dev = _cuda_device(q, "q")
+    buf = _Fp8Buffer()
+    base = _addressof(buf)
+    table = _pack_fp8(buf, q, k, v, block_mask, quant, paged, dev)
+    _PACK_OPTIONS(buf, 408, 0, 0, 0, 0, *table)
     n = C.c_size_t()
-    _check(load_library().flexattn_forward_fp8_workspace_size(C.byref(qs), C.byref(ks), C.byref(vs), C.byref(qt),
-                                                              C.byref(bm), int(split_kv), _ref(opts), C.byref(n)))
+    _check(load_library().flexattn_forward_fp8_workspace_size(base, base + 80, base + 160, base + 320, base + 344,
+                                                              int(split_kv), base + 408, C.byref(n)))
     return n.value
 
 
@@ -699,41 +756,48 @@ def flexattn_forward_fp8(q, k, v, block_mask, quant, score_mod=None, mask_mod=No
     ``quant`` is ``{"k_scale", "v_scale": fp32 (pages or B, Hkv,
     ceil(slots / scale_block)), "scale_block": n}``.  Returns ``(out, lse)``,
     or ``(out, lse, max_scores)`` when those are requested."""
-    import torch
-    dev = q.device
-    qs, ks, vs = _device_tensor(q, "q", dev), _device_tensor(k, "k", dev), _device_tensor(v, "v", dev)
+    torch = _load_torch()
+    dev = _cuda_device(q, "q")
     B, Hq, L, _ = q.shape
+    buf = _Fp8Buffer()
+    base = _addressof(buf)
+    table = _pack_fp8(buf, q, k, v, block_mask, quant, paged, dev)
     if out is None:
         out = torch.empty((B, Hq, L, v.shape[3]), dtype=out_dtype or q.dtype, device=dev)
-    os_ = _device_tensor(out, "out", dev)
+    _pack_tensor(buf, 240, out, "out", dev)
+    plse = pmax = None
     if lse is True:
         lse = torch.empty((B, Hq, L), dtype=torch.float32, device=dev)
+        plse = lse.data_ptr()
     elif lse is False or lse is None:
         lse = None
     else:
-        _device_array(lse, "lse", torch.float32, (B, Hq, L), dev)
+        plse = _device_array(lse, "lse", torch.float32, (B, Hq, L), dev)
     want_max = max_scores is not None and max_scores is not False
     if max_scores is True:
         max_scores = torch.empty((B, Hq, L), dtype=torch.float32, device=dev)
-    elif not want_max:
-        max_scores = None
-    else:
-        _device_array(max_scores, "max_scores", torch.float32, (B, Hq, L), dev)
-    qt, bm = _quant_struct(quant, k, v, dev), block_mask.as_struct()
-    opts = _options_struct(max_scores, rows_guaranteed_safe, wait_cycles, _paged_checked(paged, B, dev))
+        pmax = max_scores.data_ptr()
+    elif want_max:
+        pmax = _device_array(max_scores, "max_scores", torch.float32, (B, Hq, L), dev)
+    _PACK_OPTIONS(buf, 408, pmax or 0, int(wait_cycles or 0),
+                  _abi.FA_FLAG_ROWS_GUARANTEED_SAFE if rows_guaranteed_safe else 0, 0, *table)
     sm, mm = _score_struct(score_mod), _mask_struct(mask_mod)
     sc = 0.0 if scale is None or math.isnan(float(scale)) else float(scale)
-    lib = load_library()
+    lib = _LIB or load_library()
+    n = 0
     if workspace is None:
-        n = C.c_size_t()
-        _check(lib.flexattn_forward_fp8_workspace_size(C.byref(qs), C.byref(ks), C.byref(vs), C.byref(qt), C.byref(bm),
-                                                       int(split_kv), _ref(opts), C.byref(n)))
-        if n.value > 0:
-            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
-    _call(dev, stream, lib.flexattn_forward_fp8, C.byref(qs), C.byref(ks), C.byref(vs), C.byref(qt), C.byref(os_),
-          _ptr(lse), C.c_float(sc), int(bool(enable_gqa)), C.byref(sm), C.byref(mm), C.byref(bm), int(split_kv),
-          _ref(opts), _ptr(workspace),
-          C.c_size_t(workspace.numel() * workspace.element_size() if workspace is not None else 0))
+        status = lib.flexattn_forward_fp8_workspace_size(base, base + 80, base + 160, base + 320, base + 344,
+                                                         int(split_kv), base + 408, base + 448)
+        if status:
+            _check(status)
+        n = int.from_bytes(buf[448:456], "little")
+        if n > 0:
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    else:
+        n = workspace.numel() * workspace.element_size()
+    _call(dev, stream, lib.flexattn_forward_fp8, base, base + 80, base + 160, base + 320, base + 240, plse, sc,
+          1 if enable_gqa else 0, _addressof(sm), _addressof(mm), base + 344, int(split_kv), base + 408,
+          None if workspace is None else workspace.data_ptr(), n)
     if want_max:
         return out, lse, max_scores
     return out, lse

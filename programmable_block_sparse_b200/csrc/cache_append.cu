@@ -12,6 +12,7 @@
 // result in every order.  Angles are computed once per token of the chunk and
 // shared by the CTA's heads.
 #include "headprep.cuh"
+#include "smem_limit.h"
 
 namespace fa {
 namespace {
@@ -310,7 +311,8 @@ cudaError_t launch_append_t(const AppendArgs& a, dim3 grid, size_t smem, cudaStr
               : a.chunk == 64 ? append_kernel<T, P, kNext, kVec, 2>
                               : append_kernel<T, P, kNext, kVec, 4>;
   if (smem > 40 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static SmemLimit limit;  // only chunks of 128 slots come here
+    const cudaError_t e = limit.raise(kern, kMaxChunk * 64 * 2 * 4);
     if (e != cudaSuccess) return e;
   }
   kern<<<grid, threads_of(T), smem, st>>>(a);

@@ -42,6 +42,7 @@
 #include "fastmath.cuh"
 #include "launch.h"
 #include "mods.cuh"
+#include "smem_limit.h"
 
 namespace fa {
 namespace {
@@ -946,7 +947,8 @@ cudaError_t launch_rows(const FwdArgs& a, const QuantArgs& qa, const Fp8Plan& p,
               : a.score.kind == FA_SCORE_SOFTCAP ? decode_fp8_kernel<FA_SCORE_SOFTCAP, R>
               : a.score.kind == FA_SCORE_ALIBI   ? decode_fp8_kernel<FA_SCORE_ALIBI, R>
                                                  : decode_fp8_kernel<FA_SCORE_CAP_THEN_BIAS, R>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<R>::kSmemBytes);
+  static SmemLimit limit[4];
+  const cudaError_t e = limit[a.score.kind].raise(kern, Cfg<R>::kSmemBytes);
   if (e != cudaSuccess) return e;
   kern<<<dim3(a.Hkv * p.row_chunks, p.splits, a.B), Cfg<R>::kThreads, Cfg<R>::kSmemBytes, stream>>>(
       a, qa, p, map_k, map_v, box, ws_o, ws_lse, ws_max);

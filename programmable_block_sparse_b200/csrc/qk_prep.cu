@@ -9,6 +9,7 @@
 // keeps its token's factors in registers while it walks the heads, several
 // rows in flight.
 #include "headprep.cuh"
+#include "smem_limit.h"
 
 namespace fa {
 namespace {
@@ -272,8 +273,10 @@ __global__ void __launch_bounds__(kPrepThreads, kVec ? 3 : 1)
 template <int T, int P, bool kNext, bool kVec, bool kXF32, bool kGF32>
 cudaError_t launch_bwd_one(const PrepBwdArgs& a, int ctas, cudaStream_t st) {
   auto kern = prep_bwd_kernel<T, P, kNext, kVec, kXF32, kGF32>;
-  const int bytes = (kVec ? kBwdStages * (slot_bytes(P, kXF32) + slot_bytes(P, kGF32)) : 0) + a.tokens * a.rope.rot * 4;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  constexpr int kRing = kVec ? kBwdStages * (slot_bytes(P, kXF32) + slot_bytes(P, kGF32)) : 0;
+  const int bytes = kRing + a.tokens * a.rope.rot * 4;
+  static SmemLimit limit;  // the largest tables: a token of 128 elements for each group
+  const cudaError_t e = limit.raise(kern, kRing + kPrepThreads / T * 128 * 4);
   if (e != cudaSuccess) return e;
   kern<<<ctas, kPrepThreads, bytes, st>>>(a);
   return cudaGetLastError();
