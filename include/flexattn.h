@@ -515,8 +515,9 @@ typedef struct fa_kv_cache {
  * the way (k_norm, rope: NULL leaves it out), v as it is.  With q, the queries
  * of the same tokens are normed and rotated into q_out in the same launch (all
  * N rows of every sequence).
- *   k (B, Hkv, N, E), v (B, Hkv, N, Ev), q and q_out (B, Hq, N, E): bf16 or
- *       fp32 each, any strides with a contiguous last dimension, E, Ev <= 128.
+ *   k (B, Hkv, N, E), v (B, Hkv, N, Ev), q (B, Hq, N, E): all bf16 or all
+ *       fp32; q_out like q, bf16 or fp32.  Any strides with a contiguous last
+ *       dimension, E, Ev <= 128.
  * Token n of sequence b goes to logical slot cache_len[b] + n.  Slots that the
  * call does not name keep their bits, but for older tokens of a block whose
  * scale grows (above).  cache_len and new_len are read, not changed.

@@ -1102,6 +1102,8 @@ int flexattn_cache_append(const fa_tensor* k, const fa_tensor* v, const fa_kv_ca
   int rc;
   if ((rc = check_tensor(k, "k")) || (rc = check_tensor(v, "v"))) return rc;
   const int64_t B = k->size[0], H = k->size[1], N = k->size[2], E = k->size[3], Ev = v->size[3];
+  if (v->dtype != k->dtype || (q && q->dtype != k->dtype))
+    return fail(FA_ERR_DTYPE, "q, k and v must share one dtype");
   if (v->size[0] != B) return fail(FA_ERR_BATCH, "k and v must have the same batch size");
   if (v->size[1] != H || v->size[2] != N) return fail(FA_ERR_SHAPE, "v must be (B, Hkv, N, Ev) like k");
   if (E > 128 || Ev > 128) return fail(FA_ERR_HEADDIM, "head dims above 128 are not supported (E=%lld, Ev=%lld)", (long long)E, (long long)Ev);

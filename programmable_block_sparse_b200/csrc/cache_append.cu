@@ -67,23 +67,6 @@ __device__ __forceinline__ Span append_span(const AppendArgs& a, int b) {
   return s;
 }
 
-// The new rows of a group (n0, n0 + groups, ... below count) of one head; 0 elsewhere.
-template <int P, bool kVec, bool kF32, int kIters>
-__device__ __forceinline__ void load_rows(const RowsIn& in, int64_t off, int n0, int count, const Place& p,
-                                          Row<P> (&x)[kIters]) {
-  Raw<P, kVec, kF32> raw[kIters];
-#pragma unroll
-  for (int it = 0; it < kIters; ++it) {
-    const int n = n0 + it * kGroups;
-    if (n >= 0 && n < count)
-      load_raw(row_ptr(in.p, kF32, off + n * in.stride[2]), p, raw[it]);
-    else
-      clear_raw(raw[it]);
-  }
-#pragma unroll
-  for (int it = 0; it < kIters; ++it) x[it] = unpack(raw[it]);
-}
-
 // Queries of ntok tokens from n0 on and nh heads from hq0 on.
 template <int T, int P, bool kNext, bool kVec, bool kF32>
 __device__ __forceinline__ void append_queries(const AppendArgs& a, int b, int n0, int ntok, int hq0, int nh,
@@ -119,15 +102,145 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a, int b, int n
   }
 }
 
-// kVec: of the inputs; kCVec: rows of the cache take whole pieces.
-template <int T, int P, bool kNext, bool kVec, int kIters>
-__global__ void __launch_bounds__(threads_of(T)) append_kernel(const __grid_constant__ AppendArgs a) {
+// The new rows of heads h0 .. h1 - 1 of one chunk (keys or values): normed,
+// turned, and written; the next head's rows are loaded while this one's are
+// rounded.
+template <int T, int P, bool kNext, bool kVec, int kIters, bool kF32, bool kE4m3>
+__device__ __forceinline__ void append_rows(const AppendArgs& a, const RowsIn& in, int b, int h0, int h1, int slot0,
+                                            const Span& sp, int end, const Place& p, int D, bool turn, bool norm,
+                                            bool is_k, const float* cos_t, const float* sin_t, const float* s_w,
+                                            const int* s_outer, uint32_t (&s_amax)[2][32], float (&s_scale)[2][32],
+                                            float (&s_old)[2][32]) {
+  const int t = threadIdx.x % T, grp = threadIdx.x / T;
+  const int rot = a.rope.rot, h2 = rot >> 1;
+  const int sb_log = kE4m3 ? __ffs(a.scale_block) - 1 : 5;
+  float* scales = is_k ? a.k_scale : a.v_scale;
+  char* cache = static_cast<char*>(is_k ? a.kc : a.vc);
+  const int64_t* cs = is_k ? a.kc_stride : a.vc_stride;
+  const bool cvec = is_k ? a.kc_vec : a.vc_vec;
+  const float inv_d = 1.0f / static_cast<float>(D);
+  Raw<P, kVec, kF32> raw[kIters];
+  auto load = [&](int h) {
+    const int64_t off = b * in.stride[0] + h * in.stride[1];
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) {
+      const int n = slot0 - sp.start + grp + it * kGroups;
+      if (n >= 0 && n < sp.count)
+        load_raw(row_ptr(in.p, kF32, off + n * in.stride[2]), p, raw[it]);
+      else
+        clear_raw(raw[it]);
+    }
+  };
+  load(h0);
+  __syncthreads();  // tables, weights, pages and cleared maxima
+  Row<P> w;
+  if (norm) w = lane_weight<kVec, P>(s_w, p);
+  for (int h = h0; h < h1; ++h) {
+    const int par = (h - h0) & 1;
+    Row<P> x[kIters];
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) x[it] = unpack(raw[it]);
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) {
+      const int row = it * kGroups + grp;
+      if (norm) x[it] = product(scaled(x[it], norm_factor<T>(x[it], a.k_norm.eps, inv_d)), w);
+      if (turn)
+        x[it] = apply<kNext>(x[it], rotation<kNext, P>(cos_t + row * h2, sin_t + row * h2, t, rot, 1.0f), p, rot, D);
+      if constexpr (kE4m3) {
+        float m = 0.0f;  // of this row's finite magnitudes (rows without a new token: 0)
+        const int n = slot0 + row - sp.start;
+        if (n >= 0 && n < sp.count) {
+#pragma unroll
+          for (int i = 0; i < P; ++i) {
+            const float u = fabsf(x[it].v[i].x), v = fabsf(x[it].v[i].y);
+            m = fmaxf(m, fmaxf(u < INFINITY ? u : 0.0f, v < INFINITY ? v : 0.0f));
+          }
+        }
+#pragma unroll
+        for (int o = T / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (t == 0 && m > 0.0f) atomicMax(&s_amax[par][row >> sb_log], __float_as_uint(m));
+      }
+    }
+    if (h + 1 < h1) load(h + 1);
+    if constexpr (kE4m3) {
+      __syncthreads();
+      const int blk = threadIdx.x;
+      if (blk < 32) s_amax[1 - par][blk] = 0u;
+      if (blk < (a.chunk >> sb_log)) {
+        const int bs = slot0 + (blk << sb_log), first = max(bs, sp.start);
+        // touched by a new token, and that token's page is in the pool
+        if (first < min(bs + a.scale_block, end) && s_outer[first - slot0] >= 0) {
+          float* sc = scales + (static_cast<int64_t>(s_outer[first - slot0]) * in.H + h) * a.scales_per_outer +
+                      (bs % a.page_size) / a.scale_block;
+          const float fresh = pow2_scale(__uint_as_float(s_amax[par][blk]));
+          const bool had = bs < sp.start;
+          const float old = had ? *sc : 0.0f, now = had ? fmaxf(old, fresh) : fresh;
+          s_old[par][blk] = old;
+          s_scale[par][blk] = now;
+          if (!had || now != old) *sc = now;
+        } else {
+          s_old[par][blk] = s_scale[par][blk] = 0.0f;
+        }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int it = 0; it < kIters; ++it) {
+      const int row = it * kGroups + grp, slot = slot0 + row, outer = s_outer[row];
+      if (outer < 0) continue;
+      const int64_t off = outer * cs[0] + h * cs[1] + static_cast<int64_t>(slot % a.page_size) * cs[2];
+      if constexpr (!kE4m3) {
+        if (slot < sp.start) continue;
+        const int f32 = a.dtype == FA_DTYPE_F32;
+        if (kVec && cvec)
+          store_row<true>(row_ptr(static_cast<void*>(cache), f32, off), f32, p, x[it]);
+        else
+          store_row<false>(row_ptr(static_cast<void*>(cache), f32, off), f32, p, x[it]);
+      } else {
+      const float now = s_scale[par][row >> sb_log], inv = now > 0.0f ? 1.0f / now : 0.0f;
+      uint8_t* dst = reinterpret_cast<uint8_t*>(cache) + off;
+      Row<P> y;
+      if (slot >= sp.start) {
+        y = scaled(x[it], inv);
+      } else {
+        // an older token of a block: rounded again where its scale grew
+        const float old = s_old[par][row >> sb_log];
+        if (!(now > old)) continue;
+#pragma unroll
+        for (int i = 0; i < 2 * P; ++i)
+          put(y, i, has<P>(p, i) ? e4m3_value(dst[element<P>(p, i)]) * (old * inv) : 0.0f);
+      }
+      uint32_t code[P / 2];
+#pragma unroll
+      for (int i = 0; i < P / 2; ++i) code[i] = e4m3x4(y.v[2 * i], y.v[2 * i + 1]);
+      if (kVec && cvec) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if (!(q ? p.nb : p.na)) continue;
+          uint8_t* d = dst + (q ? p.b : p.a);
+          if constexpr (P == 8)
+            *reinterpret_cast<uint2*>(d) = make_uint2(code[2 * q], code[2 * q + 1]);
+          else
+            *reinterpret_cast<uint32_t*>(d) = code[q];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2 * P; ++i)
+          if (has<P>(p, i)) dst[element<P>(p, i)] = static_cast<uint8_t>(code[i >> 2] >> (8 * (i & 3)));
+      }
+      }
+    }
+  }
+}
+
+template <int T, int P, bool kNext, bool kVec, int kIters, bool kF32, bool kE4m3>
+__global__ void __launch_bounds__(threads_of(T), T == 8 ? 2 : 1) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kThreads = threads_of(T);
   extern __shared__ __align__(16) float tables[];  // cosines, then sines, of the chunk's tokens
   __shared__ __align__(16) float s_w[128];
   __shared__ int s_outer[kMaxChunk];
-  __shared__ uint32_t s_amax[32];
-  __shared__ float s_scale[32], s_old[32];
+  __shared__ uint32_t s_amax[2][32];  // by parity of the head: a head's maxima are
+  __shared__ float s_scale[2][32], s_old[2][32];  // cleared while the one before is rounded
   const int b = blockIdx.z, t = threadIdx.x % T, grp = threadIdx.x / T;
   const int rot = a.rope.rot, h2 = rot >> 1;
   float* cos_t = tables;
@@ -138,13 +251,48 @@ __global__ void __launch_bounds__(threads_of(T)) append_kernel(const __grid_cons
   const int* pos_row =
       a.rope.pos ? a.rope.pos + static_cast<int64_t>(a.rope.pos_batch > 1 ? b : 0) * a.N : nullptr;
   const int pos0 = __ldg(a.cache_len + b);
-  // angles of `count` tokens from n0 on into the tables from row `to` on
+  // Angles of `count` tokens from n0 on into the tables from row `to` on.
   auto fill = [&](int n0, int count, int to) {
-    for (int i = threadIdx.x; i < count * h2; i += kThreads) {
-      const int n = n0 + i / h2;
+    // Consecutive positions: one exact angle for every 8, the next ones by
+    // turning it by 1, 2 and 4 steps of the exact angle of one position (at
+    // most three products, 2^-22): an eighth of the fp64 reductions, which
+    // cost more than the rows themselves (a prompt's chunk of 64 tokens and
+    // two heads: 13 of 23 thousand warp instructions a CTA).
+    float *ct = cos_t + to * h2, *st = sin_t + to * h2;
+    const int len = pos_row ? 1 : 8, runs = (count + len - 1) / len;
+    int k = threadIdx.x / h2, f = threadIdx.x - k * h2;
+    const int dk = kThreads / h2, df = kThreads - dk * h2;
+    while (k < runs) {
+      const int first = len * k, n = n0 + first;
       const int pos =
           pos_row ? __ldg(pos_row + n) : static_cast<int>(static_cast<uint32_t>(pos0) + static_cast<uint32_t>(n));
-      angle(pos, __ldg(a.rope.inv_freq + i % h2), cos_t + to * h2 + i, sin_t + to * h2 + i);
+      const float inv = __ldg(a.rope.inv_freq + f);
+      float2 z[8];
+      z[0] = angle(pos, inv);
+      ct[first * h2 + f] = z[0].x;
+      st[first * h2 + f] = z[0].y;
+      if (len > 1 && first + 1 < count) {
+        float2 w = angle(1, inv);
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) {
+#pragma unroll
+          for (int i = 0; i < d; ++i)
+            z[d + i] = make_float2(z[i].x * w.x - z[i].y * w.y, fmaf(z[i].x, w.y, z[i].y * w.x));
+          w = make_float2(w.x * w.x - w.y * w.y, 2.0f * w.x * w.y);
+        }
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+          if (first + i < count) {
+            ct[(first + i) * h2 + f] = z[i].x;
+            st[(first + i) * h2 + f] = z[i].y;
+          }
+      }
+      k += dk;
+      f += df;
+      if (f >= h2) {
+        f -= h2;
+        ++k;
+      }
     }
   };
 
@@ -155,10 +303,7 @@ __global__ void __launch_bounds__(threads_of(T)) append_kernel(const __grid_cons
     const int hq0 = (blockIdx.y - 2 * kv_runs) * a.q_heads, nh = min(a.q_heads, a.q.H - hq0);
     if (rot) fill(n0, ntok, 0);
     if (a.q_norm.on) stage_weight(a.q_norm, a.E, 128, s_w);
-    if (a.q.f32)
-      append_queries<T, P, kNext, kVec, true>(a, b, n0, ntok, hq0, nh, cos_t, sin_t, s_w);
-    else
-      append_queries<T, P, kNext, kVec, false>(a, b, n0, ntok, hq0, nh, cos_t, sin_t, s_w);
+    append_queries<T, P, kNext, kVec, kF32>(a, b, n0, ntok, hq0, nh, cos_t, sin_t, s_w);
     return;
   }
 
@@ -195,121 +340,15 @@ __global__ void __launch_bounds__(threads_of(T)) append_kernel(const __grid_cons
     fill(from - sp.start, min(end, slot0 + a.chunk) - from, from - slot0);
   }
   if (norm) stage_weight(a.k_norm, D, 128, s_w);
-  const int e4m3 = a.dtype == FA_DTYPE_E4M3;
-  const int sb_log = e4m3 ? __ffs(a.scale_block) - 1 : 5;
-  float* scales = is_k ? a.k_scale : a.v_scale;
-  char* cache = static_cast<char*>(is_k ? a.kc : a.vc);
-  const int64_t* cs = is_k ? a.kc_stride : a.vc_stride;
-  const bool cvec = is_k ? a.kc_vec : a.vc_vec;
-
-  for (int h = run * a.k_heads; h < min((run + 1) * a.k_heads, in.H); ++h) {
-    Row<P> x[kIters];
-    const int64_t head_off = b * in.stride[0] + h * in.stride[1];
-    if (in.f32)
-      load_rows<P, kVec, true, kIters>(in, head_off, slot0 - sp.start + grp, sp.count, p, x);
-    else
-      load_rows<P, kVec, false, kIters>(in, head_off, slot0 - sp.start + grp, sp.count, p, x);
-    if (threadIdx.x < 32) s_amax[threadIdx.x] = 0u;
-    __syncthreads();  // also: the previous head's scales have been read, and the tables are filled
-#pragma unroll
-    for (int it = 0; it < kIters; ++it) {
-      const int row = it * kGroups + grp;
-      if (norm) x[it] = product(scaled(x[it], norm_factor<T>(x[it], a.k_norm.eps, 1.0f / static_cast<float>(D))),
-                                  lane_weight<kVec, P>(s_w, p));
-      if (turn)
-        x[it] = apply<kNext>(x[it], rotation<kNext, P>(cos_t + row * h2, sin_t + row * h2, t, rot, 1.0f), p, rot, D);
-      if (e4m3) {
-        float m = 0.0f;  // of this row's finite magnitudes (rows without a new token: 0)
-        const int n = slot0 + row - sp.start;
-        if (n >= 0 && n < sp.count) {
-#pragma unroll
-          for (int i = 0; i < P; ++i) {
-            const float u = fabsf(x[it].v[i].x), v = fabsf(x[it].v[i].y);
-            m = fmaxf(m, fmaxf(u < INFINITY ? u : 0.0f, v < INFINITY ? v : 0.0f));
-          }
-        }
-#pragma unroll
-        for (int o = T / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (t == 0 && m > 0.0f) atomicMax(&s_amax[row >> sb_log], __float_as_uint(m));
-      }
-    }
-    if (e4m3) {
-      __syncthreads();
-      const int blk = threadIdx.x;
-      if (blk < (a.chunk >> sb_log)) {
-        const int bs = slot0 + (blk << sb_log), first = max(bs, sp.start);
-        // touched by a new token, and that token's page is in the pool
-        if (first < min(bs + a.scale_block, end) && s_outer[first - slot0] >= 0) {
-          float* sc = scales + (static_cast<int64_t>(s_outer[first - slot0]) * in.H + h) * a.scales_per_outer +
-                      (bs % a.page_size) / a.scale_block;
-          const float fresh = pow2_scale(__uint_as_float(s_amax[blk]));
-          const bool had = bs < sp.start;
-          const float old = had ? *sc : 0.0f, now = had ? fmaxf(old, fresh) : fresh;
-          s_old[blk] = old;
-          s_scale[blk] = now;
-          if (!had || now != old) *sc = now;
-        } else {
-          s_old[blk] = s_scale[blk] = 0.0f;
-        }
-      }
-      __syncthreads();
-    }
-#pragma unroll
-    for (int it = 0; it < kIters; ++it) {
-      const int row = it * kGroups + grp, slot = slot0 + row, outer = s_outer[row];
-      if (outer < 0) continue;
-      const int64_t off = outer * cs[0] + h * cs[1] + static_cast<int64_t>(slot % a.page_size) * cs[2];
-      if (!e4m3) {
-        if (slot < sp.start) continue;
-        const int f32 = a.dtype == FA_DTYPE_F32;
-        if (kVec && cvec)
-          store_row<true>(row_ptr(static_cast<void*>(cache), f32, off), f32, p, x[it]);
-        else
-          store_row<false>(row_ptr(static_cast<void*>(cache), f32, off), f32, p, x[it]);
-        continue;
-      }
-      const float now = s_scale[row >> sb_log], inv = now > 0.0f ? 1.0f / now : 0.0f;
-      uint8_t* dst = reinterpret_cast<uint8_t*>(cache) + off;
-      Row<P> y;
-      if (slot >= sp.start) {
-        y = scaled(x[it], inv);
-      } else {
-        // an older token of a block: rounded again where its scale grew
-        const float old = s_old[row >> sb_log];
-        if (!(now > old)) continue;
-#pragma unroll
-        for (int i = 0; i < 2 * P; ++i)
-          put(y, i, has<P>(p, i) ? e4m3_value(dst[element<P>(p, i)]) * (old * inv) : 0.0f);
-      }
-      uint32_t code[P / 2];
-#pragma unroll
-      for (int i = 0; i < P / 2; ++i) code[i] = e4m3x4(y.v[2 * i], y.v[2 * i + 1]);
-      if (kVec && cvec) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (!(q ? p.nb : p.na)) continue;
-          uint8_t* d = dst + (q ? p.b : p.a);
-          if constexpr (P == 8)
-            *reinterpret_cast<uint2*>(d) = make_uint2(code[2 * q], code[2 * q + 1]);
-          else
-            *reinterpret_cast<uint32_t*>(d) = code[q];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 2 * P; ++i)
-          if (has<P>(p, i)) dst[element<P>(p, i)] = static_cast<uint8_t>(code[i >> 2] >> (8 * (i & 3)));
-      }
-    }
-    __syncthreads();  // the scales are read before the next head's maxima are cleared
-  }
+  if (threadIdx.x < 64) s_amax[threadIdx.x >> 5][threadIdx.x & 31] = 0u;
+  const int h0 = run * a.k_heads, h1 = min((run + 1) * a.k_heads, in.H);
+  append_rows<T, P, kNext, kVec, kIters, kF32, kE4m3>(a, in, b, h0, h1, slot0, sp, end, p, D, turn, norm, is_k, cos_t,
+                                                      sin_t, s_w, s_outer, s_amax, s_scale, s_old);
 }
 
-// The kernel for a row layout and a chunk.
-template <int T, int P, bool kNext, bool kVec>
-cudaError_t launch_append_t(const AppendArgs& a, dim3 grid, size_t smem, cudaStream_t st) {
-  auto kern = a.chunk == 32   ? append_kernel<T, P, kNext, kVec, 1>
-              : a.chunk == 64 ? append_kernel<T, P, kNext, kVec, 2>
-                              : append_kernel<T, P, kNext, kVec, 4>;
+template <int T, int P, bool kNext, bool kVec, int kIters, bool kF32, bool kE4m3>
+cudaError_t launch_append_one(const AppendArgs& a, dim3 grid, size_t smem, cudaStream_t st) {
+  auto kern = append_kernel<T, P, kNext, kVec, kIters, kF32, kE4m3>;
   if (smem > 40 * 1024) {
     static SmemLimit limit;  // only chunks of 128 slots come here
     const cudaError_t e = limit.raise(kern, kMaxChunk * 64 * 2 * 4);
@@ -317,6 +356,22 @@ cudaError_t launch_append_t(const AppendArgs& a, dim3 grid, size_t smem, cudaStr
   }
   kern<<<grid, threads_of(T), smem, st>>>(a);
   return cudaGetLastError();
+}
+// The kernel for a row layout, a chunk and the types.
+template <int T, int P, bool kNext, bool kVec, bool kF32>
+cudaError_t launch_append_t(const AppendArgs& a, dim3 grid, size_t smem, cudaStream_t st) {
+  if (a.dtype != FA_DTYPE_E4M3) return launch_append_one<T, P, kNext, kVec, 1, kF32, false>(a, grid, smem, st);
+  if (a.chunk == 32) return launch_append_one<T, P, kNext, kVec, 1, kF32, true>(a, grid, smem, st);
+  if (a.chunk == 64) return launch_append_one<T, P, kNext, kVec, 2, kF32, true>(a, grid, smem, st);
+  return launch_append_one<T, P, kNext, kVec, 4, kF32, true>(a, grid, smem, st);
+}
+template <int T, int P, bool kVec>
+cudaError_t launch_append_l(const AppendArgs& a, bool next, dim3 grid, size_t smem, cudaStream_t st) {
+  if (a.k.f32)
+    return next ? launch_append_t<T, P, true, kVec, true>(a, grid, smem, st)
+                : launch_append_t<T, P, false, kVec, true>(a, grid, smem, st);
+  return next ? launch_append_t<T, P, true, kVec, false>(a, grid, smem, st)
+              : launch_append_t<T, P, false, kVec, false>(a, grid, smem, st);
 }
 
 }  // namespace
@@ -338,14 +393,9 @@ cudaError_t launch_append(AppendArgs a, int num_sms, cudaStream_t st) {
   const int q_runs = a.q.p ? (a.q.H + a.q_heads - 1) / a.q_heads : 0;
   const dim3 grid(chunks, 2 * kv_runs + q_runs, a.B);
   const size_t smem = static_cast<size_t>(a.chunk) * (a.rope.rot / 2) * 2 * sizeof(float);
-  if (!l.vec)
-    return next ? launch_append_t<32, 4, true, false>(a, grid, smem, st)
-                : launch_append_t<32, 4, false, false>(a, grid, smem, st);
-  if (l.P == 8)
-    return next ? launch_append_t<8, 8, true, true>(a, grid, smem, st)
-                : launch_append_t<8, 8, false, true>(a, grid, smem, st);
-  return next ? launch_append_t<8, 4, true, true>(a, grid, smem, st)
-              : launch_append_t<8, 4, false, true>(a, grid, smem, st);
+  if (!l.vec) return launch_append_l<32, 4, false>(a, next, grid, smem, st);
+  return l.P == 8 ? launch_append_l<8, 8, true>(a, next, grid, smem, st)
+                  : launch_append_l<8, 4, true>(a, next, grid, smem, st);
 }
 
 }  // namespace fa

@@ -255,11 +255,15 @@ __device__ __forceinline__ Row<P> product(const Row<P>& x, const Row<P>& y) {
 // fp64 (pos is up to 2^31 and inv_freq a full fp32 value: in fp32 the angle of
 // a position past 10^5 would be off by a hundredth of a radian), so only the
 // remaining fraction of a turn is rounded to fp32, by 2^-25 turns at most.
-__device__ __forceinline__ void angle(int pos, float inv_freq, float* c, float* s) {
+// Not inlined: short calls wait for instructions to arrive more than for
+// anything else.
+static __device__ __noinline__ float2 angle(int pos, float inv_freq) {
   constexpr double kTurnsPerRadian = 0.15915494309189533577;
   const double turns = static_cast<double>(pos) * (static_cast<double>(inv_freq) * kTurnsPerRadian);
   const float f = static_cast<float>(turns - rint(turns));
-  sincospif(2.0f * f, s, c);
+  float2 cs;
+  sincospif(2.0f * f, &cs.y, &cs.x);
+  return cs;
 }
 
 // A linear map of a lane's pieces:

@@ -24,7 +24,9 @@ __device__ __forceinline__ void fill_tables(const RopeArgs& r, int b, int n0, in
     const int tk = i / h, n = n0 + tk;
     if (n < N) {
       const int pos = r.pos ? __ldg(r.pos + static_cast<int64_t>(r.pos_batch > 1 ? b : 0) * N + n) : n;
-      angle(pos, __ldg(r.inv_freq + (i - tk * h)), cos_t + i, sin_t + i);
+      const float2 z = angle(pos, __ldg(r.inv_freq + (i - tk * h)));
+      cos_t[i] = z.x;
+      sin_t[i] = z.y;
     }
   }
 }
