@@ -109,14 +109,14 @@ template <int T, int P, bool kNext, bool kVec, int kIters, bool kF32, bool kE4m3
 __device__ __forceinline__ void append_rows(const AppendArgs& a, const RowsIn& in, int b, int h0, int h1, int slot0,
                                             const Span& sp, int end, const Place& p, int D, bool turn, bool norm,
                                             bool is_k, const float* cos_t, const float* sin_t, const float* s_w,
-                                            const int* s_outer, uint32_t (&s_amax)[2][32], float (&s_scale)[2][32],
+                                            const int* s_outer, const int64_t* s_row, uint32_t (&s_amax)[2][32], float (&s_inv)[2][32],
                                             float (&s_old)[2][32]) {
   const int t = threadIdx.x % T, grp = threadIdx.x / T;
   const int rot = a.rope.rot, h2 = rot >> 1;
   const int sb_log = kE4m3 ? __ffs(a.scale_block) - 1 : 5;
   float* scales = is_k ? a.k_scale : a.v_scale;
   char* cache = static_cast<char*>(is_k ? a.kc : a.vc);
-  const int64_t* cs = is_k ? a.kc_stride : a.vc_stride;
+  const int64_t hstep = is_k ? a.kc_stride[1] : a.vc_stride[1];
   const bool cvec = is_k ? a.kc_vec : a.vc_vec;
   const float inv_d = 1.0f / static_cast<float>(D);
   Raw<P, kVec, kF32> raw[kIters];
@@ -147,13 +147,17 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, const RowsIn& i
       if (turn)
         x[it] = apply<kNext>(x[it], rotation<kNext, P>(cos_t + row * h2, sin_t + row * h2, t, rot, 1.0f), p, rot, D);
       if constexpr (kE4m3) {
-        float m = 0.0f;  // of this row's finite magnitudes (rows without a new token: 0)
+        // this row's largest finite magnitude (rows without a new token: 0);
+        // the maximum passes over NaN by itself, infinities are rare
+        float m = 0.0f;
         const int n = slot0 + row - sp.start;
         if (n >= 0 && n < sp.count) {
 #pragma unroll
-          for (int i = 0; i < P; ++i) {
-            const float u = fabsf(x[it].v[i].x), v = fabsf(x[it].v[i].y);
-            m = fmaxf(m, fmaxf(u < INFINITY ? u : 0.0f, v < INFINITY ? v : 0.0f));
+          for (int i = 0; i < P; ++i) m = max3f(m, fabsf(x[it].v[i].x), fabsf(x[it].v[i].y));
+          if (m == INFINITY) {
+            m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2 * P; ++i) m = fmaxf(m, fabsf(at(x[it], i)) < INFINITY ? fabsf(at(x[it], i)) : 0.0f);
           }
         }
 #pragma unroll
@@ -175,20 +179,20 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, const RowsIn& i
           const float fresh = pow2_scale(__uint_as_float(s_amax[par][blk]));
           const bool had = bs < sp.start;
           const float old = had ? *sc : 0.0f, now = had ? fmaxf(old, fresh) : fresh;
-          s_old[par][blk] = old;
-          s_scale[par][blk] = now;
+          s_inv[par][blk] = now > 0.0f ? 1.0f / now : 0.0f;
+          s_old[par][blk] = now > old ? old : -1.0f;  // -1: older codes stay as they are
           if (!had || now != old) *sc = now;
         } else {
-          s_old[par][blk] = s_scale[par][blk] = 0.0f;
+          s_old[par][blk] = -1.0f;
         }
       }
       __syncthreads();
     }
 #pragma unroll
     for (int it = 0; it < kIters; ++it) {
-      const int row = it * kGroups + grp, slot = slot0 + row, outer = s_outer[row];
-      if (outer < 0) continue;
-      const int64_t off = outer * cs[0] + h * cs[1] + static_cast<int64_t>(slot % a.page_size) * cs[2];
+      const int row = it * kGroups + grp, slot = slot0 + row;
+      if (s_row[row] < 0) continue;
+      const int64_t off = s_row[row] + h * hstep;
       if constexpr (!kE4m3) {
         if (slot < sp.start) continue;
         const int f32 = a.dtype == FA_DTYPE_F32;
@@ -197,7 +201,7 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, const RowsIn& i
         else
           store_row<false>(row_ptr(static_cast<void*>(cache), f32, off), f32, p, x[it]);
       } else {
-      const float now = s_scale[par][row >> sb_log], inv = now > 0.0f ? 1.0f / now : 0.0f;
+      const float inv = s_inv[par][row >> sb_log];
       uint8_t* dst = reinterpret_cast<uint8_t*>(cache) + off;
       Row<P> y;
       if (slot >= sp.start) {
@@ -205,7 +209,7 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, const RowsIn& i
       } else {
         // an older token of a block: rounded again where its scale grew
         const float old = s_old[par][row >> sb_log];
-        if (!(now > old)) continue;
+        if (old < 0.0f) continue;
 #pragma unroll
         for (int i = 0; i < 2 * P; ++i)
           put(y, i, has<P>(p, i) ? e4m3_value(dst[element<P>(p, i)]) * (old * inv) : 0.0f);
@@ -238,9 +242,10 @@ __global__ void __launch_bounds__(threads_of(T), T == 8 ? 2 : 1) append_kernel(c
   constexpr int kThreads = threads_of(T);
   extern __shared__ __align__(16) float tables[];  // cosines, then sines, of the chunk's tokens
   __shared__ __align__(16) float s_w[128];
+  __shared__ int64_t s_row[kMaxChunk];
   __shared__ int s_outer[kMaxChunk];
   __shared__ uint32_t s_amax[2][32];  // by parity of the head: a head's maxima are
-  __shared__ float s_scale[2][32], s_old[2][32];  // cleared while the one before is rounded
+  __shared__ float s_inv[2][32], s_old[2][32];  // cleared while the one before is rounded
   const int b = blockIdx.z, t = threadIdx.x % T, grp = threadIdx.x / T;
   const int rot = a.rope.rot, h2 = rot >> 1;
   float* cos_t = tables;
@@ -317,7 +322,9 @@ __global__ void __launch_bounds__(threads_of(T), T == 8 ? 2 : 1) append_kernel(c
   const RowsIn& in = is_k ? a.k : a.v;
   const bool turn = is_k && rot, norm = is_k && a.k_norm.on;
   const Place p = place_of<P, kNext>(t, is_k ? rot : 0, D);
-  // page (or sequence) of each slot of the chunk that the call touches; -1: none
+  // page (or sequence) of each slot of the chunk that the call touches, and the
+  // slot's offset in the cache; -1: none
+  const int64_t* cs = is_k ? a.kc_stride : a.vc_stride;
   for (int i = threadIdx.x; i < a.chunk; i += kThreads) {
     const int slot = slot0 + i;
     int outer = -1;
@@ -334,6 +341,7 @@ __global__ void __launch_bounds__(threads_of(T), T == 8 ? 2 : 1) append_kernel(c
       }
     }
     s_outer[i] = outer;
+    s_row[i] = outer < 0 ? -1 : outer * cs[0] + static_cast<int64_t>(slot % a.page_size) * cs[2];
   }
   if (turn) {
     const int from = max(slot0, sp.start);
@@ -343,7 +351,7 @@ __global__ void __launch_bounds__(threads_of(T), T == 8 ? 2 : 1) append_kernel(c
   if (threadIdx.x < 64) s_amax[threadIdx.x >> 5][threadIdx.x & 31] = 0u;
   const int h0 = run * a.k_heads, h1 = min((run + 1) * a.k_heads, in.H);
   append_rows<T, P, kNext, kVec, kIters, kF32, kE4m3>(a, in, b, h0, h1, slot0, sp, end, p, D, turn, norm, is_k, cos_t,
-                                                      sin_t, s_w, s_outer, s_amax, s_scale, s_old);
+                                                      sin_t, s_w, s_outer, s_row, s_amax, s_inv, s_old);
 }
 
 template <int T, int P, bool kNext, bool kVec, int kIters, bool kF32, bool kE4m3>
