@@ -390,11 +390,17 @@ cudaError_t launch_append(AppendArgs a, int num_sms, cudaStream_t st) {
   a.chunk = a.dtype == FA_DTYPE_E4M3 && a.scale_block > 32 ? a.scale_block : 32;
   // N tokens that start anywhere in a chunk touch this many chunks at most
   const int chunks = static_cast<int>((static_cast<int64_t>(a.N) + a.chunk - 2) / a.chunk) + 1;
-  // Heads of k share the chunk's angles: as many a CTA as leave the GPU four
-  // CTAs an SM.
-  const int64_t per_head = static_cast<int64_t>(chunks) * a.B;
+  // Heads of k share the chunk's angles, and all heads its start-up (lengths,
+  // pages), so a CTA takes several: enough to leave eight CTAs an SM, or two,
+  // which run at once, where there is little but the start-up.  Eight prompts
+  // of 2048 tokens, 8 heads: 51 us with 1 head a CTA, 37 with 2, 35 with 4 and
+  // 38 with 8; 8191 tokens into bf16 pages: 23, 14.6, 11.4, 10.7; one token of
+  // 32 sequences: 9.9, 7.8, 11.5, 18.
+  const int64_t per_head = static_cast<int64_t>(chunks) * a.B, most = (a.N >= kGroups ? 8 : 2) * num_sms;
   a.k_heads = 1;
-  while (2 * a.k_heads <= a.k.H && per_head * (a.k.H / (2 * a.k_heads)) >= 4 * num_sms) a.k_heads *= 2;
+  while (a.k_heads < a.k.H && 2 * per_head * ((a.k.H + a.k_heads - 1) / a.k_heads) > most &&
+         (a.N >= kGroups || a.k_heads < 2))
+    a.k_heads *= 2;
   const int ntok = a.N < a.chunk ? a.N : a.chunk;
   a.q_heads = ntok < kGroups ? (kGroups + ntok - 1) / ntok : 8;
   const int kv_runs = (a.k.H + a.k_heads - 1) / a.k_heads;
