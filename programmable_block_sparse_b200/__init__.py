@@ -495,14 +495,22 @@ def _cuda_device(t, name):
 
 def _pack_tensor(buf, at, t, name, device):
     """``t`` as the fa_tensor at byte ``at`` of ``buf``; it has to be 4-D and on ``device``."""
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise FlexAttnError(6, f"{name}: unsupported dtype {t.dtype}")
+    try:
+        _PACK_TENSOR(buf, at, t.data_ptr(), _DTYPES[t.dtype], 0, *t.shape, *t.stride())
+    except KeyError:
+        raise FlexAttnError(6, f"{name}: unsupported dtype {t.dtype}") from None
+    except struct.error:
+        raise FlexAttnError(2, f"{name}: expected a 4-D tensor, got shape {tuple(t.shape)}") from None
     if t.device != device:
         raise FlexAttnError(9, f"{name} is on {t.device}, expected {device}")
-    if t.dim() != 4:
-        raise FlexAttnError(2, f"{name}: expected a 4-D tensor, got shape {tuple(t.shape)}")
-    _PACK_TENSOR(buf, at, t.data_ptr(), code, 0, *t.shape, *t.stride())
+
+
+def _new_like(buf, at, x, dtype=None):
+    """A new contiguous tensor of x's shape, packed at ``at``."""
+    t = _torch.empty_like(x, dtype=dtype, memory_format=_torch.contiguous_format)
+    b, h, n, d = x.shape
+    _PACK_TENSOR(buf, at, t.data_ptr(), _DTYPES[t.dtype], 0, b, h, n, d, h * n * d, n * d, d, 1)
+    return t
 
 
 def _device_array(t, name, dtype, shape, device):
@@ -550,11 +558,6 @@ def _pack_rope(buf, at, spec, B, N, device):
     return _addressof(buf) + at
 
 
-def _empty_like(t, dtype=None):
-    """A new contiguous tensor of t's shape on its device."""
-    return _torch.empty_like(t, dtype=dtype, memory_format=_torch.contiguous_format)
-
-
 def _call(device, stream, fn, *args):
     """``fn(*args, stream)`` with ``device`` current; ``stream`` None is that device's current stream."""
     cuda = _torch.cuda
@@ -562,7 +565,8 @@ def _call(device, stream, fn, *args):
         with cuda.device(device):
             return _call(device, stream, fn, *args)
     if stream is None:
-        handle = cuda.current_stream().cuda_stream
+        # the handle itself: a Stream object takes as long to build as a small kernel runs
+        handle = _torch._C._cuda_getCurrentRawStream(device.index)
     else:
         handle = stream if isinstance(stream, int) else stream.cuda_stream
     status = fn(*args, handle)
@@ -588,14 +592,16 @@ def flexattn_qk_norm_rope(q, k, q_norm=None, k_norm=None, rope=None, q_out=None,
     if q is not None:
         _pack_tensor(buf, 0, q, "q", dev)
         if q_out is None:
-            q_out = _empty_like(q)
-        _pack_tensor(buf, 80, q_out, "q_out", dev)
+            q_out = _new_like(buf, 80, q)
+        else:
+            _pack_tensor(buf, 80, q_out, "q_out", dev)
         pq, pqo = base, base + 80
     if k is not None:
         _pack_tensor(buf, 160, k, "k", dev)
         if k_out is None:
-            k_out = _empty_like(k)
-        _pack_tensor(buf, 240, k_out, "k_out", dev)
+            k_out = _new_like(buf, 240, k)
+        else:
+            _pack_tensor(buf, 240, k_out, "k_out", dev)
         pk, pko = base + 160, base + 240
     B, _, N, D = x.shape
     _call(dev, stream, (_LIB or load_library()).flexattn_qk_norm_rope, pq, pk, pqo, pko,
@@ -641,10 +647,11 @@ def flexattn_qk_norm_rope_backward(q, k, dq_out, dk_out, q_norm=None, k_norm=Non
             _pack_tensor(buf, at, x, name, dev)
             px = base + at
         if dy is not None:
-            if dx is None:
-                dx = _empty_like(dy, grad_dtype)
             _pack_tensor(buf, at + 80, dy, f"d{name}_out", dev)
-            _pack_tensor(buf, at + 160, dx, f"d{name}", dev)
+            if dx is None:
+                dx = _new_like(buf, at + 160, dy, grad_dtype)
+            else:
+                _pack_tensor(buf, at + 160, dx, f"d{name}", dev)
             pg, po = base + at + 80, base + at + 160
         return px, pg, po, dx
 
@@ -703,8 +710,9 @@ def flexattn_cache_append(k, v, cache, k_norm=None, rope=None, q=None, q_norm=No
     if q is not None:
         _pack_tensor(buf, 368, q, "q", dev)
         if q_out is None:
-            q_out = _empty_like(q)
-        _pack_tensor(buf, 448, q_out, "q_out", dev)
+            q_out = _new_like(buf, 448, q)
+        else:
+            _pack_tensor(buf, 448, q_out, "q_out", dev)
         pq, pqo = base + 368, base + 448
     _call(dev, stream, (_LIB or load_library()).flexattn_cache_append, base + 208, base + 288, base,
           _pack_norm(buf, 528, k_norm, "k_norm weight", E, dev), _pack_rope(buf, 560, rope, B, N, dev), pq, pqo,
@@ -762,12 +770,15 @@ def flexattn_forward_fp8(q, k, v, block_mask, quant, score_mod=None, mask_mod=No
     buf = _Fp8Buffer()
     base = _addressof(buf)
     table = _pack_fp8(buf, q, k, v, block_mask, quant, paged, dev)
-    if out is None:
-        out = torch.empty((B, Hq, L, v.shape[3]), dtype=out_dtype or q.dtype, device=dev)
-    _pack_tensor(buf, 240, out, "out", dev)
+    if out is None and q.shape[3] == v.shape[3]:
+        out = _new_like(buf, 240, q, out_dtype)
+    else:
+        if out is None:
+            out = q.new_empty((B, Hq, L, v.shape[3]), dtype=out_dtype)
+        _pack_tensor(buf, 240, out, "out", dev)
     plse = pmax = None
     if lse is True:
-        lse = torch.empty((B, Hq, L), dtype=torch.float32, device=dev)
+        lse = q.new_empty((B, Hq, L), dtype=torch.float32)
         plse = lse.data_ptr()
     elif lse is False or lse is None:
         lse = None
@@ -792,7 +803,7 @@ def flexattn_forward_fp8(q, k, v, block_mask, quant, score_mod=None, mask_mod=No
             _check(status)
         n = int.from_bytes(buf[448:456], "little")
         if n > 0:
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+            workspace = q.new_empty((n,), dtype=torch.uint8)
     else:
         n = workspace.numel() * workspace.element_size()
     _call(dev, stream, lib.flexattn_forward_fp8, base, base + 80, base + 160, base + 320, base + 240, plse, sc,
