@@ -191,8 +191,9 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars<kRing> bars;
   __shared__ float s_red[2][4][R];
-  __shared__ int s_qpos[R], s_head[R], s_row[R], s_pq[R];
-  __shared__ float s_slope[R], s_unit[R];
+  __shared__ int s_qpos[R], s_head[R], s_pq[R];
+  __shared__ float s_slope[R], s_unit[R], s_inv[R];
+  __shared__ int64_t s_id[R], s_off[R];  // row of lse; where the row's output begins (-1: no row)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sKV = smem;
   uint8_t* sQ = smem + kRing * kTileBytes;
@@ -292,8 +293,12 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
       const int head = hk * a.G + (per_head ? g0 : min(rho / a.L, a.G - 1)), i = per_head ? rho : rho % a.L;
       const int Hs = a.score.slope_heads > 0 ? a.score.slope_heads : a.Hq;
       s_qpos[lane] = query_pos(i, a.L, S_b);
-      s_head[lane] = ok ? head : -1;
-      s_row[lane] = ok ? i : 0;
+      s_head[lane] = head;
+      const int64_t id = (static_cast<int64_t>(b) * a.Hq + head) * a.L + i;
+      s_id[lane] = p.splits == 1 ? id : id * p.splits + split;
+      s_off[lane] = !ok             ? -1
+                    : p.splits == 1 ? b * a.o_stride[0] + head * a.o_stride[1] + i * a.o_stride[2]
+                                    : (id * p.splits + split) * a.Ev;
       s_slope[lane] = distance_slope(head, Hs);
       s_pq[lane] = has_pos ? pos_at(a.score, b, s_qpos[lane], a.S) : 0;
     }
@@ -563,17 +568,24 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
             }
           }
         }
-        // element mask on listed-partial tiles and at the end of the sequence
+        // Element mask on listed-partial tiles and at the end of the sequence.
+        // The rule is chosen once for all rows, so that their tests overlap
+        // (rows past the CTA's are masked like any other and never written).
         if (t0 + j >= nfull || kv0 + kKeys > S_b) {
+          auto mask_rows = [&](auto visible) {
 #pragma unroll
-          for (int r = 0; r < N; ++r)
-            if (s_head[row0 + r] < 0 ||
-                !mask_visible(a.mask, b, s_head[row0 + r], s_qpos[row0 + r], kv, S_b, a.S)) {
-              if (r & 1)
-                t[r >> 1].y = -INFINITY;
-              else
-                t[r >> 1].x = -INFINITY;
+            for (int r = 0; r < N; ++r) {
+              const bool vis = kv < S_b && visible(r, s_qpos[row0 + r]);
+              float& x = (r & 1) ? t[r >> 1].y : t[r >> 1].x;
+              x = vis ? x : -INFINITY;
             }
+          };
+          if (a.mask.kind == FA_MASK_CAUSAL)
+            mask_rows([&](int, int q) { return kv <= q; });
+          else if (a.mask.kind == FA_MASK_SLIDING_WINDOW)
+            mask_rows([&](int, int q) { return kv <= q && (q - kv < a.mask.window || kv < a.mask.n_sink); });
+          else
+            mask_rows([&](int r, int q) { return mask_visible(a.mask, b, s_head[row0 + r], q, kv, S_b, a.S); });
         }
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
@@ -698,35 +710,43 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
         s_red[1][qd][row0 + lane / (32 / N)] = lm;
       }
       named_bar_sync(bar, 128);
-      const int ev = kk;
+      // one thread a row for what the row's 128 columns share
+      if (kk < N && s_off[row0 + kk] >= 0) {
+        const int rr = row0 + kk;
+        const float l = (s_red[0][0][rr] + s_red[0][1][rr]) + (s_red[0][2][rr] + s_red[0][3][rr]);
+        const float top = fmaxf(fmaxf(s_red[1][0][rr], s_red[1][1][rr]), fmaxf(s_red[1][2][rr], s_red[1][3][rr]));
+        float nm = 0.0f;
 #pragma unroll
-      for (int r = 0; r < N; ++r) {
-        const int hq = s_head[row0 + r];
-        if (hq < 0) continue;
-        const float l = (s_red[0][0][row0 + r] + s_red[0][1][row0 + r]) + (s_red[0][2][row0 + r] + s_red[0][3][row0 + r]);
-        const float top = fmaxf(fmaxf(s_red[1][0][row0 + r], s_red[1][1][row0 + r]), fmaxf(s_red[1][2][row0 + r], s_red[1][3][row0 + r]));
+        for (int r = 0; r < N; ++r)
+          if (kk == r) nm = (r & 1) ? nms[r >> 1].y : nms[r >> 1].x;
         // a row without a visible key (in this split) has l = 0: out 0 and lse
         // -inf, unless the caller promised there is none and there is one
         // split; NaN stays NaN
         const bool live = (a.rows_safe && p.splits == 1) || !(l == 0.0f);
-        const float inv = live ? 1.0f / l : 0.0f;
-        const float lse = live ? (log2f(l) - ((r & 1) ? nms[r >> 1].y : nms[r >> 1].x)) * kLn2 : -INFINITY;
-        const int64_t row_id = (static_cast<int64_t>(b) * a.Hq + hq) * a.L + s_row[row0 + r];
-        const float val = fmaf(__uint_as_float(o[N + r]), 0.0625f, __uint_as_float(o[r])) * inv;
+        s_inv[rr] = live ? 1.0f / l : 0.0f;
+        const float lse = live ? (log2f(l) - nm) * kLn2 : -INFINITY;
+        const int64_t id = s_id[rr];
         if (p.splits == 1) {
-          if (ev < a.Ev) {
-            const int64_t off = b * a.o_stride[0] + hq * a.o_stride[1] + s_row[row0 + r] * a.o_stride[2] + ev;
-            if (a.out_f32)
-              static_cast<float*>(a.out)[off] = val;
-            else
-              static_cast<__nv_bfloat16*>(a.out)[off] = __float2bfloat16_rn(val);
-          }
-          if (ev == 0 && a.lse) a.lse[row_id] = lse;
-          if (ev == 0 && a.max_scores) a.max_scores[row_id] = top * kLn2;
+          if (a.lse) a.lse[id] = lse;
+          if (a.max_scores) a.max_scores[id] = top * kLn2;
         } else {
-          if (ev < a.Ev) ws_o[(row_id * p.splits + split) * a.Ev + ev] = val;
-          if (ev == 0) ws_lse[row_id * p.splits + split] = lse;
-          if (ev == 0) ws_max[row_id * p.splits + split] = top;
+          ws_lse[id] = lse;
+          ws_max[id] = top;
+        }
+      }
+      named_bar_sync(bar, 128);
+      const int ev = kk;
+      const bool half_out = p.splits == 1 && !a.out_f32;
+      float* dst = p.splits == 1 ? static_cast<float*>(a.out) : ws_o;
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        const int64_t off = s_off[row0 + r];
+        const float val = fmaf(__uint_as_float(o[N + r]), 0.0625f, __uint_as_float(o[r])) * s_inv[row0 + r];
+        if (off >= 0 && ev < a.Ev) {
+          if (half_out)
+            static_cast<__nv_bfloat16*>(a.out)[off + ev] = __float2bfloat16_rn(val);
+          else
+            dst[off + ev] = val;
         }
       }
     }
