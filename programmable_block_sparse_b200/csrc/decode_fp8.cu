@@ -416,14 +416,16 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
         umma_commit(&bars.p_free[pb]);
         umma_commit(&bars.empty[e]);
       };
-      // Whichever product is ready first.  Tile jq's K entry last held K of
-      // tile jq - kRing / 2, whose QK was issued before, and likewise for V: a
-      // tested barrier is never two phases behind.
+      // Whichever product is ready first, but QK of tile j only after PV of
+      // tile j - 2: then the commit that hands over S_j (it covers everything
+      // issued before) also says that the weights' buffer of tile j - 2 is free.
+      // Tile jq's K entry last held K of tile jq - kRing / 2, whose QK was issued
+      // before, and likewise for V: a tested barrier is never two phases behind.
       int jq = 0, jp = 0;
       long long idle_from = clock64();
       while (jp < nsub) {
         bool progressed = false;
-        if (jq < nsub && mbar_test(&bars.full[(2 * jq) % kRing], ((2 * jq) / kRing) & 1) &&
+        if (jq < nsub && jp >= jq - 1 && mbar_test(&bars.full[(2 * jq) % kRing], ((2 * jq) / kRing) & 1) &&
             (jq < 2 || mbar_test(&bars.s_free[jq & 1], ((jq - 2) >> 1) & 1))) {
           issue_qk(jq++);
           progressed = true;
@@ -483,33 +485,49 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
     for (int r = 0; r < 8; ++r)
       wx[r] = smem_u32(sP) + (row0 >> 3) * 1024 + r * 128 + (((kk >> 4) ^ r) << 4) + (kk & 15);
     // What the next tiles need comes ahead, a stage an iteration, since each
-    // load depends on the one before: tile index, page, scales.
-    auto page_of = [&](int kv) {  // -1 past the sequence's end
-      if (kv >= S_b) return -1;
-      if (!a.page_table) return b;
-      const int pg = __ldg(a.page_table + static_cast<int64_t>(b) * a.pages_per_seq + p.page.quotient(kv));
-      return min(max(pg, 0), a.num_pages - 1);  // warp 0 records an id outside the pool
+    // load depends on the one before: tile index, page, scales.  A loaded value
+    // is first touched (scaled, clamped) an iteration later: touched at once,
+    // it held the warp for 400 of a tile's 1750 cycles.
+    auto page_at = [&](int kv) {  // raw: the id may lie outside the pool
+      return a.page_table && kv < S_b
+                 ? __ldg(a.page_table + static_cast<int64_t>(b) * a.pages_per_seq + p.page.quotient(kv))
+                 : b;
     };
-    auto scales_of = [&](int kv, int pg, float& ks, float& vs) {
+    auto scales_at = [&](int kv, int pg, float& ks, float& vs) {  // 1 past the sequence's end
       ks = vs = 1.0f;
-      if (pg < 0) return;
-      const int at = a.page_table ? kv - p.page.quotient(kv) * a.page_size : kv;
-      const int64_t i = (static_cast<int64_t>(pg) * a.Hkv + hk) * qa.scales_per_outer + (at >> qa.block_log);
-      ks = __ldg(qa.k_scale + i);
-      vs = __ldg(qa.v_scale + i);
+      if (kv < S_b) {
+        int at = kv;
+        if (a.page_table) {
+          pg = min(max(pg, 0), a.num_pages - 1);  // warp 0 records an id outside the pool
+          at = kv - p.page.quotient(kv) * a.page_size;
+        }
+        const int64_t i = (static_cast<int64_t>(pg) * a.Hkv + hk) * qa.scales_per_outer + (at >> qa.block_log);
+        ks = __ldg(qa.k_scale + i);
+        vs = __ldg(qa.v_scale + i);
+      }
     };
-    auto first_key = [&](int j) { return j < nsub ? listed_tile(a, brow, nfull, t0 + j) * kKeys : 0; };
-    int kv0 = first_key(0), kv0_1 = first_key(1), kv0_2 = first_key(2);
-    float ks, vs, ks_1 = 1.0f, vs_1 = 1.0f;
-    scales_of(kv0 + kk, nsub > 0 ? page_of(kv0 + kk) : -1, ks, vs);
-    int pg_1 = nsub > 1 ? page_of(kv0_1 + kk) : -1;
+    const int* list_full = a.bm.full_kv_indices + brow * a.bm.Nb + t0;
+    const int* list_part = a.bm.kv_indices + brow * a.bm.Nb + t0 - nfull;
+    auto tile_at = [&](int j) { return __ldg((t0 + j < nfull ? list_full : list_part) + j); };
+    int kv0 = 0, kv0_1 = 0, n_2 = 0, pg_1 = 0;
+    float ks = 1.0f, vs = 1.0f, ks_1 = 1.0f, vs_1 = 1.0f;
+    if (nsub > 0) {  // tiles past the last one repeat it
+      const int n_0 = tile_at(0), n_1 = tile_at(min(1, nsub - 1));
+      n_2 = tile_at(min(2, nsub - 1));
+      kv0 = n_0 * kKeys;
+      kv0_1 = n_1 * kKeys;
+      const int pg_0 = page_at(kv0 + kk);
+      pg_1 = page_at(kv0_1 + kk);
+      scales_at(kv0 + kk, pg_0, ks, vs);
+    }
     bool alive = true;
     for (int j = 0; j < nsub; ++j) {
       const int sb = j & 1;
       const int kv = kv0 + kk;
-      if (j + 1 < nsub) scales_of(kv0_1 + kk, pg_1, ks_1, vs_1);
-      const int pg_2 = j + 2 < nsub ? page_of(kv0_2 + kk) : -1;
-      const int kv0_3 = first_key(j + 3);
+      const int kv0_2 = n_2 * kKeys;
+      scales_at(kv0_1 + kk, pg_1, ks_1, vs_1);
+      const int pg_2 = page_at(kv0_2 + kk);
+      const int n_3 = tile_at(min(j + 3, nsub - 1));
       vs = fmaxf(vs, 7.888609052210118e-31f);  // 2^-100: a block of zeros has scale 0
       float lv, ivs;  // exact for powers of two; other errors, 2^-21, cancel but between blocks
       asm("lg2.approx.f32 %0, %1;" : "=f"(lv) : "f"(vs));
@@ -644,10 +662,6 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
           }
         }
       }
-      // weights of this tile into buffer j & 1, free once PV of tile j - 2 is done
-      if (alive && j >= 2)
-        alive = __all_sync(0xffffffffu, mbar_wait(&bars.p_free[sb], ((j - 2) >> 1) & 1, abort, a.status,
-                                                  a.wait_cycles));
       // Values past the sequence's end may hold anything (0 * NaN is NaN):
       // their rows are cleared before the product reads them.
       if (alive && kv0 + kKeys > S_b) {
@@ -681,7 +695,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
       }
       kv0 = kv0_1;
       kv0_1 = kv0_2;
-      kv0_2 = kv0_3;
+      n_2 = n_3;
       ks = ks_1;
       vs = vs_1;
       pg_1 = pg_2;
