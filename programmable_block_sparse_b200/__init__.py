@@ -634,12 +634,15 @@ def flexattn_qk_norm_rope_backward(q, k, dq_out, dk_out, q_norm=None, k_norm=Non
     want_k = dk_out is not None and k_norm is not None and weight_grads
     dqw = dkw = None
     if want_q or want_k:
-        both = torch.empty((2, D), dtype=torch.float32, device=dev)
-        dqw, dkw = both[0] if want_q else None, both[1] if want_k else None
+        dqw, dkw = g.new_empty((2, D), dtype=torch.float32).unbind()
+        if not want_q:
+            dqw = None
+        if not want_k:
+            dkw = None
         if workspace is None:
             n = C.c_size_t()
             _check(lib.flexattn_qk_norm_rope_backward_workspace_size(D, 1, C.byref(n)))
-            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+            workspace = g.new_empty((n.value,), dtype=torch.uint8)
 
     def side(at, x, dy, dx, norm, name):
         px = pg = po = None
@@ -766,6 +769,11 @@ def flexattn_forward_fp8(q, k, v, block_mask, quant, score_mod=None, mask_mod=No
     or ``(out, lse, max_scores)`` when those are requested."""
     torch = _load_torch()
     dev = _cuda_device(q, "q")
+    if torch.cuda.current_device() != dev.index:  # the plan is made for the device that runs it
+        with torch.cuda.device(dev):
+            return flexattn_forward_fp8(q, k, v, block_mask, quant, score_mod, mask_mod, scale, enable_gqa, out, lse,
+                                        split_kv, workspace, stream, out_dtype, max_scores, rows_guaranteed_safe,
+                                        wait_cycles, paged)
     B, Hq, L, _ = q.shape
     buf = _Fp8Buffer()
     base = _addressof(buf)

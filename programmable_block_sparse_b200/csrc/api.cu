@@ -661,10 +661,19 @@ struct Fp8Call {
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Up to this many 16-row chunks per KV head the decode kernel is taken: each
-// chunk reads the cache again (mostly from L2), where restoring reads it once,
-// writes it in q's type and reads that.
-constexpr int kFp8MaxRowChunks = 16;
+// Whether queries of one tile (L <= 128) run on the 8-bit decode kernel or on the
+// prefill kernel over the restored cache.  The decode kernel takes 1.2 us for
+// each 128 keys of a row chunk and SM, every chunk reading the cache again
+// (mostly from L2); the prefill kernel about 2.7 us for each 128 keys of a
+// round of heads, one an SM.  Measured (us, decode / restored): 2 sequences of
+// 8k keys, 32 heads on 8: L = 64 130 / 174, L = 96 183 / 174; 8 of 4k, 16 on 4:
+// L = 32 84 / 103, L = 48 114 / 105; 1 of 32k: L = 128 405 / 543.  Head dims
+// without a tensor-core prefill stay on the decode kernel.
+bool prefer_decode(const FwdArgs& a, const Fp8Plan& plan) {
+  if (a.E != a.Ev || (a.E != 64 && a.E != 128)) return true;
+  const int64_t sms = sm_count(), rounds = (static_cast<int64_t>(a.B) * a.Hq + sms - 1) / sms;
+  return static_cast<int64_t>(a.B) * a.Hkv * plan.row_chunks <= 2 * sms * rounds;
+}
 
 int prepare_fp8(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const fa_kv_quant* quant,
                 const fa_tensor* out, float scale, int32_t enable_gqa, const fa_score_mod* score,
@@ -697,8 +706,7 @@ int prepare_fp8(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, cons
     while (opt->page_size % c->box) c->box /= 2;
   plan_decode_fp8(a, split_kv, sm_count(), &c->plan);
   c->decode = q->dtype == FA_DTYPE_BF16 && bm->Mb == 1 && bm->BN == 128 && c->box >= 8 && aligned16(q) &&
-              codes_aligned16(k) && codes_aligned16(v) && c->plan.row_chunks <= kFp8MaxRowChunks &&
-              static_cast<int64_t>(a.Hkv) * c->plan.row_chunks * a.B < (int64_t{1} << 30);
+              codes_aligned16(k) && codes_aligned16(v) && prefer_decode(a, c->plan);
   if (c->decode) {
     c->bytes = c->plan.workspace_bytes;
     return FA_OK;
