@@ -258,40 +258,19 @@ __global__ void __launch_bounds__(threads_of(T), T == 8 ? 2 : 1) append_kernel(c
   const int pos0 = __ldg(a.cache_len + b);
   // Angles of `count` tokens from n0 on into the tables from row `to` on.
   auto fill = [&](int n0, int count, int to) {
-    // Consecutive positions: one exact angle for every 8, the next ones by
-    // turning it by 1, 2 and 4 steps of the exact angle of one position (at
-    // most three products, 2^-22): an eighth of the fp64 reductions, which
-    // cost more than the rows themselves (a prompt's chunk of 64 tokens and
-    // two heads: 13 of 23 thousand warp instructions a CTA).
+    // (Every eighth angle and products of complex numbers between them saved
+    // 4 of 39 us on the prompt below, but moved 2.5 times as many codes across
+    // a tie.)
     float *ct = cos_t + to * h2, *st = sin_t + to * h2;
-    const int len = pos_row ? 1 : 8, runs = (count + len - 1) / len;
-    int k = threadIdx.x / h2, f = threadIdx.x - k * h2;
+    int k = threadIdx.x / h2, f = threadIdx.x - k * h2;  // stepped without divisions
     const int dk = kThreads / h2, df = kThreads - dk * h2;
-    while (k < runs) {
-      const int first = len * k, n = n0 + first;
+    while (k < count) {
+      const int n = n0 + k;
       const int pos =
           pos_row ? __ldg(pos_row + n) : static_cast<int>(static_cast<uint32_t>(pos0) + static_cast<uint32_t>(n));
-      const float inv = __ldg(a.rope.inv_freq + f);
-      float2 z[8];
-      z[0] = angle(pos, inv);
-      ct[first * h2 + f] = z[0].x;
-      st[first * h2 + f] = z[0].y;
-      if (len > 1 && first + 1 < count) {
-        float2 w = angle(1, inv);
-#pragma unroll
-        for (int d = 1; d < 8; d <<= 1) {
-#pragma unroll
-          for (int i = 0; i < d; ++i)
-            z[d + i] = make_float2(z[i].x * w.x - z[i].y * w.y, fmaf(z[i].x, w.y, z[i].y * w.x));
-          w = make_float2(w.x * w.x - w.y * w.y, 2.0f * w.x * w.y);
-        }
-#pragma unroll
-        for (int i = 1; i < 8; ++i)
-          if (first + i < count) {
-            ct[(first + i) * h2 + f] = z[i].x;
-            st[(first + i) * h2 + f] = z[i].y;
-          }
-      }
+      const float2 z = angle(pos, __ldg(a.rope.inv_freq + f));
+      ct[k * h2 + f] = z.x;
+      st[k * h2 + f] = z.y;
       k += dk;
       f += df;
       if (f >= h2) {

@@ -253,17 +253,23 @@ __device__ __forceinline__ Row<P> product(const Row<P>& x, const Row<P>& y) {
 
 // cos and sin of pos * inv_freq.  The angle is taken in turns and reduced in
 // fp64 (pos is up to 2^31 and inv_freq a full fp32 value: in fp32 the angle of
-// a position past 10^5 would be off by a hundredth of a radian), so only the
-// remaining fraction of a turn is rounded to fp32, by 2^-25 turns at most.
+// a position past 10^5 would be off by a hundredth of a radian).  The fraction
+// left is rounded to fp32 for sincospif, and what that rounding drops (2^-25
+// turns at most) turns the result by its own small angle, so that the two are
+// good to their last place: keys that are rounded to e4m3 afterwards land on
+// another code than the exact ones where the fp32 error crosses a tie.
 // Not inlined: short calls wait for instructions to arrive more than for
 // anything else.
 static __device__ __noinline__ float2 angle(int pos, float inv_freq) {
   constexpr double kTurnsPerRadian = 0.15915494309189533577;
+  constexpr float kTwoPi = 6.2831853f;
   const double turns = static_cast<double>(pos) * (static_cast<double>(inv_freq) * kTurnsPerRadian);
-  const float f = static_cast<float>(turns - rint(turns));
-  float2 cs;
-  sincospif(2.0f * f, &cs.y, &cs.x);
-  return cs;
+  const double frac = turns - rint(turns);
+  const float f = static_cast<float>(frac);
+  const float rest = kTwoPi * static_cast<float>(frac - static_cast<double>(f));
+  float c, s;
+  sincospif(2.0f * f, &s, &c);
+  return make_float2(fmaf(-s, rest, c), fmaf(c, rest, s));
 }
 
 // A linear map of a lane's pieces:
