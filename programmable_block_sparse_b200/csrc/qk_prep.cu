@@ -127,12 +127,21 @@ __device__ __forceinline__ Walk walk_of(const RowsIn& in, const Place& p, int b,
 constexpr int slot_bytes(int P, bool f32) { return kPrepThreads * 2 * P * (f32 ? 4 : 2); }
 
 // One row's gradient: y, the output gradient turned back, becomes the input
-// gradient, and dw takes its share of the weight gradient.
+// gradient, and dw takes its share of the weight gradient.  Single fp32
+// operations: the factors r and k would have to be copied into register pairs
+// for packed ones (203 us with those, 184 without; the forward pass is the
+// other way round, 122 and 132).
 template <int T, int P>
 __device__ __forceinline__ void norm_gradient(Row<P>& y, const Row<P>& x, const Row<P>& w, float eps, float inv_d,
                                               Row<P>& dw) {
-  const Row<P> yw = product(y, w);
-  float ss = dot(x, x), sd = dot(yw, x);
+  Row<P> yw;
+  float ss = 0.0f, sd = 0.0f;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    yw.v[i] = make_float2(y.v[i].x * w.v[i].x, y.v[i].y * w.v[i].y);
+    ss = fmaf(x.v[i].y, x.v[i].y, fmaf(x.v[i].x, x.v[i].x, ss));
+    sd = fmaf(yw.v[i].y, x.v[i].y, fmaf(yw.v[i].x, x.v[i].x, sd));
+  }
 #pragma unroll
   for (int o = T / 2; o > 0; o >>= 1) {
     ss += __shfl_xor_sync(0xffffffffu, ss, o);
@@ -141,9 +150,11 @@ __device__ __forceinline__ void norm_gradient(Row<P>& y, const Row<P>& x, const 
   const float r = rsqrtf(ss * inv_d + eps), k = sd * inv_d * r * r;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const float2 xr = mul2(x.v[i], splat2(r));
-    dw.v[i] = fma2(y.v[i], xr, dw.v[i]);
-    y.v[i] = fma2(splat2(-k), xr, mul2(yw.v[i], splat2(r)));
+    const float2 xr = make_float2(x.v[i].x * r, x.v[i].y * r);
+    dw.v[i].x = fmaf(y.v[i].x, xr.x, dw.v[i].x);
+    dw.v[i].y = fmaf(y.v[i].y, xr.y, dw.v[i].y);
+    y.v[i].x = fmaf(-k, xr.x, yw.v[i].x * r);
+    y.v[i].y = fmaf(-k, xr.y, yw.v[i].y * r);
   }
 }
 
