@@ -23,10 +23,9 @@
  *   - Every call returns an int status: FA_OK (0) or one of FA_ERR_*.  No call
  *     throws or aborts.  flexattn_last_error() gives a message for the last
  *     failing call on the calling thread.
- *   - flexattn_build_block_mask, flexattn_forward and
- *     flexattn_forward_decode_noalloc only enqueue kernels, so a stream
- *     capture of them (CUDA graphs, relaxed capture mode) replays the same
- *     work; flexattn_poll_device_status synchronises and must stay outside a
+ *   - Every entry point that takes a stream only enqueues kernels, so a stream
+ *     capture of it (CUDA graphs, relaxed capture mode) replays the same work;
+ *     flexattn_poll_device_status alone synchronises and must stay outside a
  *     capture.
  *   - Integers on the device are int32; the host-side struct sizes are int32.
  */
@@ -524,8 +523,10 @@ typedef struct fa_kv_cache {
  * Nothing outside the cache is written: a token past the cache's end, a page id
  * outside the pool, a negative cache_len or a new_len outside 0..N records
  * FA_ERR_PARAM in the device status word, and the tokens concerned are left
- * out (new_len is clamped).  Two sequences of one call must not share the
- * pages they write to.
+ * out (new_len is clamped).  No two tokens of one call may go to one slot,
+ * and no two sequences to one scale block (pages written by two sequences, or
+ * more tokens than a circular table has slots): what such slots hold is
+ * unspecified.
  * Errors: FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_HEADS, FA_ERR_BATCH, FA_ERR_DTYPE,
  * FA_ERR_HEADDIM, FA_ERR_ALIGN, FA_ERR_PARAM, FA_ERR_CUDA. */
 int flexattn_cache_append(const fa_tensor* k, const fa_tensor* v, const fa_kv_cache* cache,
@@ -553,16 +554,20 @@ int flexattn_forward_fp8_workspace_size(const fa_tensor* q, const fa_tensor* k, 
  * options and outputs, with k_j = code * scale and v_j = code * scale.
  *   q: bf16 or fp32; k, v: e4m3, dense (B, Hkv, S, E / Ev) or page pools
  *       (options->page_table).
- *   Short queries (bf16 q, one query tile, 128-key tiles, E and Ev multiples of
- *       16, 16-byte aligned codes and strides, pages of a multiple of 8 keys)
- *       run on the 8-bit decode kernel, which reads every code once and keeps
- *       q exactly (two e4m3 terms a value); the softmax weights are rounded to
- *       two e4m3 terms, at most 2^-8 of each.  Other calls restore
+ *   Short queries (bf16 q on 16-byte boundaries, one query tile, 128-key tiles, E
+ *       and Ev multiples of 16, 16-byte aligned codes and strides, pages of a
+ *       multiple of 8 keys; up to 16 rows always, more while it is the faster
+ *       way) run on the 8-bit decode kernel, which keeps q exactly (two e4m3
+ *       terms a value); the softmax weights are rounded to two e4m3 terms, at
+ *       most 2^-8 of each.  Other calls restore
  *       the visible part of the cache to q's type in the workspace (exact in
  *       bf16 for power-of-two scales, else rounded, 2^-8 of each value at
  *       most) and run flexattn_forward on it.
- *   Slots at or beyond kv_len[b] are not read as numbers (NaN there is
- *       harmless), nor are page ids past the last page in use.
+ *   Slots at or beyond kv_len[b] are not read as numbers (NaN there, in codes or
+ *       scales, is harmless), nor are page ids past the last page in use; slots
+ *       below it that a rule hides hold finite values (a weight of 0 times NaN
+ *       is NaN).  Value scales below 2^-100 count as 2^-100.  A query row with
+ *       an infinity or NaN gives NaN, in its own row only.
  *   split_kv: as in flexattn_forward, for the decode kernel.
  * Errors: those of flexattn_forward. */
 int flexattn_forward_fp8(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const fa_kv_quant* quant,

@@ -736,6 +736,8 @@ def _pack_fp8(buf, q, k, v, block_mask, quant, paged, dev):
     _PACK_QUANT(buf, 320, _device_array(quant["k_scale"], "k_scale", torch.float32, _scale_shape(k, n), dev),
                 _device_array(quant["v_scale"], "v_scale", torch.float32, _scale_shape(v, n), dev), n, 0)
     m = block_mask
+    if m.kv_num_blocks.device != dev:
+        raise FlexAttnError(9, f"the block mask is on {m.kv_num_blocks.device}, expected {dev}")
     _PACK_MASK(buf, 344, m.B, m.H, m.L, m.S, m.BM, m.BN, m.Mb, m.Nb, m.kv_num_blocks.data_ptr(),
                m.kv_indices.data_ptr(), m.full_kv_num_blocks.data_ptr(), m.full_kv_indices.data_ptr())
     if paged is None:
@@ -743,6 +745,18 @@ def _pack_fp8(buf, q, k, v, block_mask, quant, paged, dev):
     t = paged["page_table"]
     return (_device_array(t, "page_table", torch.int32, (q.shape[0], t.shape[-1]), dev), int(paged["page_size"]),
             t.shape[-1])
+
+
+def _check_rule(spec, B, S, dev):
+    """The tensors of a mask or score rule: int32, of a known extent, on ``dev``."""
+    for name, shapes in (("kv_len", ((B,),)), ("doc_id", ((S,), (1, S), (B, S))), ("pos", ((S,), (1, S), (B, S)))):
+        t = spec.get(name)
+        if t is not None and not isinstance(t, str):
+            _device_array(t, name, _torch.int32, tuple(t.shape) if tuple(t.shape) in shapes else shapes[0], dev)
+    for sub in spec.get("masks", ()):
+        _check_rule(sub, B, S, dev)
+    if "mask" in spec:
+        _check_rule(spec["mask"], B, S, dev)
 
 
 def flexattn_forward_fp8_workspace_size(q, k, v, block_mask, quant, split_kv=0, paged=None):
@@ -800,6 +814,9 @@ def flexattn_forward_fp8(q, k, v, block_mask, quant, score_mod=None, mask_mod=No
         pmax = _device_array(max_scores, "max_scores", torch.float32, (B, Hq, L), dev)
     _PACK_OPTIONS(buf, 408, pmax or 0, int(wait_cycles or 0),
                   _abi.FA_FLAG_ROWS_GUARANTEED_SAFE if rows_guaranteed_safe else 0, 0, *table)
+    for rule in (mask_mod, score_mod):
+        if rule:
+            _check_rule(rule, B, block_mask.S, dev)
     sm, mm = _score_struct(score_mod), _mask_struct(mask_mod)
     sc = 0.0 if scale is None or math.isnan(float(scale)) else float(scale)
     lib = _LIB or load_library()

@@ -747,7 +747,7 @@ using namespace fa;
 
 extern "C" {
 
-int flexattn_version(void) { return 100; }
+int flexattn_version(void) { return 200; }
 
 const char* flexattn_last_error(void) { return t_last_error.c_str(); }
 

@@ -133,7 +133,7 @@ constexpr int slot_bytes(int P, bool f32) { return kPrepThreads * 2 * P * (f32 ?
 // other way round, 122 and 132).
 template <int T, int P>
 __device__ __forceinline__ void norm_gradient(Row<P>& y, const Row<P>& x, const Row<P>& w, float eps, float inv_d,
-                                              Row<P>& dw) {
+                                              bool ok, Row<P>& dw) {
   Row<P> yw;
   float ss = 0.0f, sd = 0.0f;
 #pragma unroll
@@ -147,7 +147,8 @@ __device__ __forceinline__ void norm_gradient(Row<P>& y, const Row<P>& x, const 
     ss += __shfl_xor_sync(0xffffffffu, ss, o);
     sd += __shfl_xor_sync(0xffffffffu, sd, o);
   }
-  const float r = rsqrtf(ss * inv_d + eps), k = sd * inv_d * r * r;
+  // rows that are not there count for nothing, with eps = 0 too
+  const float r = ok ? rsqrtf(ss * inv_d + eps) : 0.0f, k = sd * inv_d * r * r;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     const float2 xr = make_float2(x.v[i].x * r, x.v[i].y * r);
@@ -165,7 +166,7 @@ __device__ __forceinline__ void norm_gradient(Row<P>& y, const Row<P>& x, const 
 // A row takes two reads, so the walk over q's heads and then k's keeps
 // kStages - 1 rows a lane in flight through shared memory (copy_raw).  Rows
 // that are read one element at a time go without.
-constexpr int kBwdStages = 4;
+constexpr int kBwdStages = 3;  // 182 us; 4: 183, 5 (two CTAs an SM): 206
 
 template <int T, int P, bool kNext, bool kVec, bool kXF32, bool kGF32>
 __global__ void __launch_bounds__(kPrepThreads, kVec ? 3 : 1)
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(kPrepThreads, kVec ? 3 : 1)
           }
         }
         Row<P> y = apply<kNext>(unpack(graw), f, p, rot, a.D);
-        if (norm) norm_gradient<T>(y, unpack(xraw), w, eps, inv_d, dw);
+        if (norm) norm_gradient<T>(y, unpack(xraw), w, eps, inv_d, head < heads, dw);
         if (head < heads) store_row<kVec>(op, dx.f32, p, y);
         op += ostep;
         head += per;

@@ -309,6 +309,50 @@ def test_streams_graphs_and_repeats():
     assert fa.flexattn_poll_device_status() == 0
 
 
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace of its own, do not touch one another."""
+    import programmable_block_sparse_b200 as fa
+    cases = [Fp8Case(4, 8, 2, 1, 4096, 128, block=64, page=64, kv_len=[4096, 3000, 64, 2000], seed=s) for s in (1, 2)]
+    want = [c.run(split_kv=7) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    bms = [c.block_mask() for c in cases]
+    qs = [c.q.cuda() for c in cases]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(5):
+        for i, c in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                got[i] = fa.flexattn_forward_fp8(qs[i], c.dev[0], c.dev[1], bms[i], c.quant, score_mod=c.dev_score,
+                                                 mask_mod=c.dev_mask, enable_gqa=True, paged=c.paged, split_kv=7)
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+def test_python_refusals():
+    """Rule tensors, scales and tables of other types, extents or devices."""
+    import programmable_block_sparse_b200 as fa
+    c = Fp8Case(2, 4, 2, 1, 256, 64, block=16, page=64, kv_len=[256, 100], seed=1)
+    bm = c.block_mask()
+
+    def status(quant=c.quant, mask=c.dev_mask, paged=c.paged, **kw):
+        with pytest.raises(fa.FlexAttnError) as e:
+            fa.flexattn_forward_fp8(c.q.cuda(), c.dev[0], c.dev[1], bm, quant, mask_mod=mask, enable_gqa=True,
+                                    paged=paged, **kw)
+        return e.value.status
+
+    assert status(mask=dict(c.dev_mask, kv_len=c.dev_mask["kv_len"].long())) == 6
+    assert status(mask=dict(c.dev_mask, kv_len=c.dev_mask["kv_len"][:1])) == 2
+    assert status(mask=dict(c.dev_mask, kv_len=c.dev_mask["kv_len"].cpu())) == 9
+    assert status(quant=dict(c.quant, k_scale=c.quant["k_scale"][:-1])) == 2
+    assert status(quant=dict(c.quant, v_scale=c.quant["v_scale"].double())) == 6
+    assert status(quant=dict(c.quant, scale_block=32)) == 2
+    assert status(paged=dict(c.paged, page_table=c.paged["page_table"][:1])) == 2
+    assert status(paged=dict(c.paged, page_table=c.paged["page_table"].t().contiguous().t())) == 8
+    assert status(lse=torch.empty(2, 4, 2, device="cuda")) == 2
+    assert status(score_mod={"kind": "cap_then_bias", "cap": 5.0, "pos": torch.zeros(7, dtype=torch.int32).cuda()}) == 2
+
+
 def test_bad_page_ids_are_reported():
     """An id outside the pool in a page that is in use: nothing outside the
     pool is read and the status word says so, on both paths."""

@@ -183,6 +183,18 @@ def test_backward_of_shared_and_broadcast_inputs():
                    True, None, pos, f, False)
 
 
+@pytest.mark.parametrize("N,H,D", [(5, 3, 64), (33, 5, 128), (1, 1, 80)])
+def test_backward_without_eps(N, H, D):
+    """eps = 0: places that a block of tokens or heads leaves empty add nothing."""
+    import programmable_block_sparse_b200 as fa
+    x, g = randn(1, 2, H, N, D).cuda(), randn(2, 2, H, N, D).cuda()
+    f = inv_freq(D).cuda()
+    dx, _, dw, _ = fa.flexattn_qk_norm_rope_backward(x, None, g, None, q_norm={"eps": 0.0}, rope={"inv_freq": f})
+    rx, rw = co.norm_rope_backward(np64(x), np64(g), np.arange(N)[None], np64(f), False, True, None, 0.0)
+    assert np.linalg.norm(np64(dx) - rx) <= 2.0 ** -8 * np.linalg.norm(rx)
+    assert np.linalg.norm(np64(dw) - rw) <= 2.0 ** -17 * np.abs(np64(g) * np64(x)).sum()
+
+
 def test_gradient_against_differences():
     """Central differences of the kernel's own fp32 forward: a step of 2^-7
     leaves a rounding of 2^-20 / 2^-7 and a third-order term of 2^-14 a value."""
