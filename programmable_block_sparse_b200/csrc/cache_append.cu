@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(threads_of(T), T == 8 ? 2 : 1) append_kernel(c
   const int rot = a.rope.rot, h2 = rot >> 1;
   float* cos_t = tables;
   float* sin_t = tables + a.chunk * h2;
-  const int k_runs = (a.k.H + a.k_heads - 1) / a.k_heads, v_runs = (a.k.H + a.v_heads - 1) / a.v_heads;
+  const int kv_runs = (a.k.H + a.k_heads - 1) / a.k_heads;
   const Span sp = append_span(a, b);
   if (sp.bad && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) record_error(a.status, FA_ERR_PARAM);
   const int* pos_row =
@@ -280,11 +280,11 @@ __global__ void __launch_bounds__(threads_of(T), T == 8 ? 2 : 1) append_kernel(c
     }
   };
 
-  if (static_cast<int>(blockIdx.y) >= k_runs + v_runs) {
+  if (static_cast<int>(blockIdx.y) >= 2 * kv_runs) {
     // ------------------------------------------------------------- queries
     const int n0 = blockIdx.x * a.chunk, ntok = min(a.chunk, a.N - n0);
     if (ntok <= 0) return;
-    const int hq0 = (static_cast<int>(blockIdx.y) - k_runs - v_runs) * a.q_heads, nh = min(a.q_heads, a.q.H - hq0);
+    const int hq0 = (blockIdx.y - 2 * kv_runs) * a.q_heads, nh = min(a.q_heads, a.q.H - hq0);
     if (rot) fill(n0, ntok, 0);
     if (a.q_norm.on) stage_weight(a.q_norm, a.E, 128, s_w);
     append_queries<T, P, kNext, kVec, kF32>(a, b, n0, ntok, hq0, nh, cos_t, sin_t, s_w);
@@ -292,9 +292,8 @@ __global__ void __launch_bounds__(threads_of(T), T == 8 ? 2 : 1) append_kernel(c
   }
 
   // ------------------------------------------------------- keys or values
-  const bool is_k = static_cast<int>(blockIdx.y) < k_runs;
-  const int heads = is_k ? a.k_heads : a.v_heads;
-  const int h0 = (is_k ? blockIdx.y : blockIdx.y - k_runs) * heads;
+  const bool is_k = static_cast<int>(blockIdx.y) < kv_runs;
+  const int h0 = (is_k ? blockIdx.y : blockIdx.y - kv_runs) * a.k_heads;
   const int slot0 = (sp.start / a.chunk + static_cast<int>(blockIdx.x)) * a.chunk;
   const int end = sp.start + sp.count;  // past the last new slot
   if (sp.count == 0 || slot0 >= end) return;
@@ -329,7 +328,7 @@ __global__ void __launch_bounds__(threads_of(T), T == 8 ? 2 : 1) append_kernel(c
   }
   if (norm) stage_weight(a.k_norm, D, 128, s_w);
   if (threadIdx.x < 64) s_amax[threadIdx.x >> 5][threadIdx.x & 31] = 0u;
-  const int h1 = min(h0 + heads, in.H);
+  const int h1 = min(h0 + a.k_heads, in.H);
   append_rows<T, P, kNext, kVec, kIters, kF32, kE4m3>(a, in, b, h0, h1, slot0, sp, end, p, D, turn, norm, is_k, cos_t,
                                                       sin_t, s_w, s_outer, s_row, s_amax, s_inv, s_old);
 }
@@ -373,9 +372,9 @@ cudaError_t launch_append(AppendArgs a, int num_sms, cudaStream_t st) {
   // Heads of k share the chunk's angles, and all heads its start-up (lengths,
   // pages), so a CTA takes several: enough to leave eight CTAs an SM, or two,
   // which run at once, where there is little but the start-up.  Eight prompts
-  // of 2048 tokens, 8 heads: 44 us with 2 heads a CTA, 39 with 4 and 41 with 8;
-  // 8191 tokens into bf16 pages: 16, 11.9 and 11; one token of 32 sequences:
-  // 9.9 with 1, 8 with 2, 11.5 with 4.
+  // of 2048 tokens, 8 heads, inputs not in L2: 72 us with 1 head a CTA, 52 with
+  // 2, 43 with 4 and 44 with 8; 8191 tokens into bf16 pages: 30, 20.5, 17.3 and
+  // 16.4; one token of 32 sequences (graph replay): 9.9, 8, 11.5, 18.
   const int64_t per_head = static_cast<int64_t>(chunks) * a.B, most = (a.N >= kGroups ? 8 : 2) * num_sms;
   a.k_heads = 1;
   while (a.k_heads < a.k.H && 2 * per_head * ((a.k.H + a.k_heads - 1) / a.k_heads) > most &&
@@ -383,12 +382,9 @@ cudaError_t launch_append(AppendArgs a, int num_sms, cudaStream_t st) {
     a.k_heads *= 2;
   const int ntok = a.N < a.chunk ? a.N : a.chunk;
   a.q_heads = ntok < kGroups ? (kGroups + ntok - 1) / ntok : 8;
-  // Heads of v come without angles, so a CTA takes twice as many of them where
-  // there are rows to speak of (prompts: 39 -> 33 us).
-  a.v_heads = a.N >= kGroups && 2 * a.k_heads <= a.k.H ? 2 * a.k_heads : a.k_heads;
-  const int kv_runs = (a.k.H + a.k_heads - 1) / a.k_heads + (a.k.H + a.v_heads - 1) / a.v_heads;
+  const int kv_runs = (a.k.H + a.k_heads - 1) / a.k_heads;
   const int q_runs = a.q.p ? (a.q.H + a.q_heads - 1) / a.q_heads : 0;
-  const dim3 grid(chunks, kv_runs + q_runs, a.B);
+  const dim3 grid(chunks, 2 * kv_runs + q_runs, a.B);
   const size_t smem = static_cast<size_t>(a.chunk) * (a.rope.rot / 2) * 2 * sizeof(float);
   if (!l.vec) return launch_append_l<32, 4, false>(a, next, grid, smem, st);
   return l.P == 8 ? launch_append_l<8, 8, true>(a, next, grid, smem, st)

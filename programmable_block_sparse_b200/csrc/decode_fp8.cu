@@ -17,8 +17,8 @@
 //     a rounding to bf16, and a third of that in the mean square.
 //
 // hi and lo are columns of the small N side: 16 query rows make N = 32, 4 or 8
-// rows N = 16.  With s^k_j, s^v_j the
-// scales of key j, c_j the codes, in log2 units:
+// rows N = 16.  With s^k_j, s^v_j the scales of key j, c_j the codes, in log2
+// units:
 //   t_rj  = rule(s_r s^k_j scale (hi_r + lo_r / 16) . c^k_j)
 //   w_rj  = 2^(t_rj + log2 s^v_j - m_r + 6),  m_r the running maximum of
 //           t + log2 s^v, moved when some key passes it by more than 2, so
@@ -35,6 +35,10 @@
 //   warp 1      TMEM allocation; one thread issues the MMAs, whichever product
 //               is ready first.
 //   warps 2-    softmax (warp % 4 is the TMEM lane quadrant), epilogue.
+// Measured: 32 sequences of 4k..32k keys, 32 heads on 8, head dim 128: one query
+// 223 us for 1.44 GB of codes and scales (6.47 TB/s, the copy rate), four
+// queries 294 us, where the softmax of 16 rows a key is the bound; one sequence
+// of 32k keys 17.7 us, of which about 7 are a CTA's start, one tile and its end.
 #include <cuda_fp8.h>
 #include <math.h>
 

@@ -11,7 +11,7 @@
 // D <= 64, P = 4 and T = 8; above, P = 4 and T = 16, or P = 8 and T = 8 (the
 // cache append, which holds rows in registers anyway and gains from fewer
 // lanes a row: 61 -> 49 us for 8 prompts of 2048 tokens; the preparation does
-// not: 121 -> 141 us forward, 203 -> 197 us backward, and 10 -> 15 us for a
+// not: 122 -> 124 us forward, 203 -> 197 us backward, and 10 -> 15 us for a
 // short batch).  Other rows are read one element at a time by a whole warp
 // (P = 4, T = 32).
 // What a row costs beside its arithmetic decides, so shuffles are left to the

@@ -182,7 +182,7 @@ struct AppendArgs {
   const int* page_table;
   const int *cache_len, *new_len;
   int page_size, pages_per_seq, num_outer;
-  int chunk, k_heads, v_heads, q_heads;  // tokens and heads per CTA (set by the launcher)
+  int chunk, k_heads, q_heads;  // tokens and heads per CTA (set by the launcher)
 };
 cudaError_t launch_append(AppendArgs a, int num_sms, cudaStream_t stream);
 

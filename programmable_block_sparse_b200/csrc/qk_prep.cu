@@ -7,7 +7,10 @@
 // a token's angles are the same for every head, so their fp64 reduction and
 // sincos are paid once a token, into shared memory, and each group of T lanes
 // keeps its token's factors in registers while it walks the heads, several
-// rows in flight.
+// rows in flight.  Measured at 32 + 8 heads of 128 over 32768 tokens in bf16:
+// forward 122 us for 671 MB (5.5 TB/s), 146 instructions for two rows of a
+// warp and 68% of the issue slots; backward 184 us for 1007 MB (5.5 TB/s), 74%
+// of the issue slots.
 #include "headprep.cuh"
 #include "smem_limit.h"
 
