@@ -109,8 +109,8 @@ template <int T, int P, bool kNext, bool kVec, int kIters, bool kF32, bool kE4m3
 __device__ __forceinline__ void append_rows(const AppendArgs& a, const RowsIn& in, int b, int h0, int h1, int slot0,
                                             const Span& sp, int end, const Place& p, int D, bool turn, bool norm,
                                             bool is_k, const float* cos_t, const float* sin_t, const float* s_w,
-                                            const int* s_outer, const int64_t* s_row, uint32_t (&s_amax)[2][32], float (&s_inv)[2][32],
-                                            float (&s_old)[2][32]) {
+                                            const int* s_outer, const int64_t* s_row, uint32_t (&s_amax)[2][32],
+                                            float (&s_inv)[2][32], float (&s_old)[2][32]) {
   const int t = threadIdx.x % T, grp = threadIdx.x / T;
   const int rot = a.rope.rot, h2 = rot >> 1;
   const int sb_log = kE4m3 ? __ffs(a.scale_block) - 1 : 5;
@@ -201,37 +201,37 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, const RowsIn& i
         else
           store_row<false>(row_ptr(static_cast<void*>(cache), f32, off), f32, p, x[it]);
       } else {
-      const float inv = s_inv[par][row >> sb_log];
-      uint8_t* dst = reinterpret_cast<uint8_t*>(cache) + off;
-      Row<P> y;
-      if (slot >= sp.start) {
-        y = scaled(x[it], inv);
-      } else {
-        // an older token of a block: rounded again where its scale grew
-        const float old = s_old[par][row >> sb_log];
-        if (old < 0.0f) continue;
+        const float inv = s_inv[par][row >> sb_log];
+        uint8_t* dst = reinterpret_cast<uint8_t*>(cache) + off;
+        Row<P> y;
+        if (slot >= sp.start) {
+          y = scaled(x[it], inv);
+        } else {
+          // an older token of a block: rounded again where its scale grew
+          const float old = s_old[par][row >> sb_log];
+          if (old < 0.0f) continue;
 #pragma unroll
-        for (int i = 0; i < 2 * P; ++i)
-          put(y, i, has<P>(p, i) ? e4m3_value(dst[element<P>(p, i)]) * (old * inv) : 0.0f);
-      }
-      uint32_t code[P / 2];
-#pragma unroll
-      for (int i = 0; i < P / 2; ++i) code[i] = e4m3x4(y.v[2 * i], y.v[2 * i + 1]);
-      if (kVec && cvec) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (!(q ? p.nb : p.na)) continue;
-          uint8_t* d = dst + (q ? p.b : p.a);
-          if constexpr (P == 8)
-            *reinterpret_cast<uint2*>(d) = make_uint2(code[2 * q], code[2 * q + 1]);
-          else
-            *reinterpret_cast<uint32_t*>(d) = code[q];
+          for (int i = 0; i < 2 * P; ++i)
+            put(y, i, has<P>(p, i) ? e4m3_value(dst[element<P>(p, i)]) * (old * inv) : 0.0f);
         }
-      } else {
+        uint32_t code[P / 2];
 #pragma unroll
-        for (int i = 0; i < 2 * P; ++i)
-          if (has<P>(p, i)) dst[element<P>(p, i)] = static_cast<uint8_t>(code[i >> 2] >> (8 * (i & 3)));
-      }
+        for (int i = 0; i < P / 2; ++i) code[i] = e4m3x4(y.v[2 * i], y.v[2 * i + 1]);
+        if (kVec && cvec) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            if (!(q ? p.nb : p.na)) continue;
+            uint8_t* d = dst + (q ? p.b : p.a);
+            if constexpr (P == 8)
+              *reinterpret_cast<uint2*>(d) = make_uint2(code[2 * q], code[2 * q + 1]);
+            else
+              *reinterpret_cast<uint32_t*>(d) = code[q];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2 * P; ++i)
+            if (has<P>(p, i)) dst[element<P>(p, i)] = static_cast<uint8_t>(code[i >> 2] >> (8 * (i & 3)));
+        }
       }
     }
   }
@@ -294,9 +294,10 @@ __global__ void __launch_bounds__(threads_of(T), T == 8 ? 2 : 1) append_kernel(c
   // ------------------------------------------------------- keys or values
   const bool is_k = static_cast<int>(blockIdx.y) < kv_runs;
   const int h0 = (is_k ? blockIdx.y : blockIdx.y - kv_runs) * a.k_heads;
-  const int slot0 = (sp.start / a.chunk + static_cast<int>(blockIdx.x)) * a.chunk;
   const int end = sp.start + sp.count;  // past the last new slot
-  if (sp.count == 0 || slot0 >= end) return;
+  const int64_t first_slot = (static_cast<int64_t>(sp.start / a.chunk) + blockIdx.x) * a.chunk;
+  if (sp.count == 0 || first_slot >= end) return;
+  const int slot0 = static_cast<int>(first_slot);
   const int D = is_k ? a.E : a.Ev;
   const RowsIn& in = is_k ? a.k : a.v;
   const bool turn = is_k && rot, norm = is_k && a.k_norm.on;

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
     if (lane < R) {
       const int rho = rho0 + lane;
       const bool ok = rho < rho_end;
-      const int head = hk * a.G + (per_head ? g0 : min(rho / a.L, a.G - 1)), i = per_head ? rho : rho % a.L;
+      const int head = hk * a.G + (per_head ? g0 : min(rho / a.L, a.G - 1)), i = per_head ? min(rho, a.L - 1) : rho % a.L;
       const int Hs = a.score.slope_heads > 0 ? a.score.slope_heads : a.Hq;
       s_qpos[lane] = query_pos(i, a.L, S_b);
       s_head[lane] = head;
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
     float amax = 0.0f;
     bool finite = true;
     const bool ok = r < R && rho < rho_end;
-    const int head = hk * a.G + (per_head ? g0 : min(rho / a.L, a.G - 1)), i = per_head ? rho : rho % a.L;
+    const int head = hk * a.G + (per_head ? g0 : min(rho / a.L, a.G - 1)), i = per_head ? min(rho, a.L - 1) : rho % a.L;
     const __nv_bfloat16* src =
         static_cast<const __nv_bfloat16*>(a.q) + b * a.q_stride[0] + head * a.q_stride[1] + i * a.q_stride[2];
 #pragma unroll
@@ -592,7 +592,8 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
         }
         // Element mask on listed-partial tiles and at the end of the sequence.
         // The rule is chosen once for all rows, so that their tests overlap
-        // (rows past the CTA's are masked like any other and never written).
+        // (rows past the CTA's stand at a valid position, are masked like any
+        // other and never written).
         if (t0 + j >= nfull || kv0 + kKeys > S_b) {
           auto mask_rows = [&](auto visible) {
 #pragma unroll

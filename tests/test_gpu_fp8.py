@@ -208,6 +208,13 @@ def test_head_dependent_rule():
         c.check(c.run(c.block_mask(heads=8)))
 
 
+def test_document_rule_with_lists_per_head():
+    """Fixed rules may come with per-head lists: the last chunk of 20 rows a
+    head is not full, and its empty rows read no document id."""
+    c = Fp8Case(2, 4, 2, 20, 384, 64, mask={"kind": "document"}, kv_len=[384, 384], seed=5)
+    c.check(c.run(c.block_mask(heads=4)))
+
+
 @pytest.mark.parametrize("kv_len", [[64, 700, 1500, 129, 700], [(37 * i) % 900 + 40 for i in range(40)]],
                          ids=["ties", "forty_sequences"])
 def test_sequence_order(kv_len):
