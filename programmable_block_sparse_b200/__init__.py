@@ -1,8 +1,9 @@
 """B200 (sm_100a) FlexAttention forward: Python binding of ``libflexattn_b200.so``.
 
 The functions here carry the C entry points' names and only marshal
-arguments: torch tensors become device pointers, sizes and strides; mask and
-score specifications (plain dicts) become the C structs.  Every step of the
+arguments (the per-token calls through a compiled binding): torch tensors become
+device pointers, sizes and strides; mask and score specifications (plain dicts)
+become the C structs.  Every step of the
 computation runs in the CUDA library; there is no CPU fallback -- importing
 works without the library, but any call raises if it is not built.
 
@@ -35,7 +36,6 @@ from __future__ import annotations
 import ctypes as C
 import math
 import os
-import struct
 from dataclasses import dataclass
 
 from . import _abi
@@ -458,159 +458,31 @@ def flexattn_backward(q, k, v, out, dout, lse, block_mask, q_side=None, score_mo
 # Query / key preparation, cache writes and attention over an e4m3 cache
 # ---------------------------------------------------------------------------
 # These calls are made once a layer and token, and some of their kernels take
-# less time than a Python function that builds ctypes structs one by one: all
-# structs of a call are packed into one buffer, at fixed places.
-_PACK_TENSOR = struct.Struct("Qii4q4q").pack_into
-_PACK_NORM = struct.Struct("Qif").pack_into
-_PACK_ROPE = struct.Struct("QQiiii").pack_into
-_PACK_QUANT = struct.Struct("QQii").pack_into
-_PACK_CACHE = struct.Struct("5Qii").pack_into
-_PACK_MASK = struct.Struct("8i4Q").pack_into
-_PACK_OPTIONS = struct.Struct("QqiiQii").pack_into
-_TENSOR, _NORM, _ROPE, _QUANT = 80, 16, 32, 24  # bytes
-_addressof = C.addressof
-_DTYPES = {}
-_torch = None
+# less time than a Python function that packs structs: csrc/binding.cpp does the
+# marshalling (and the checks of tensors whose extent the library cannot know).
+_BINDING = None
 
 
-def _load_torch():
-    """torch, with the element types' codes known."""
-    global _torch
-    if _torch is None:
-        import torch
-        _DTYPES.update({torch.bfloat16: _abi.FA_DTYPE_BF16, torch.float32: _abi.FA_DTYPE_F32,
-                        torch.float8_e4m3fn: _abi.FA_DTYPE_E4M3})
-        _torch = torch
-    return _torch
-
-
-def _cuda_device(t, name):
-    if t.dtype not in _DTYPES:
-        raise FlexAttnError(6, f"{name}: unsupported dtype {t.dtype}")
-    dev = t.device
-    if dev.type != "cuda":
-        raise FlexAttnError(9, f"{name} is on {dev}, expected a CUDA device")
-    return dev
-
-
-def _pack_tensor(buf, at, t, name, device):
-    """``t`` as the fa_tensor at byte ``at`` of ``buf``; it has to be 4-D and on ``device``."""
-    try:
-        _PACK_TENSOR(buf, at, t.data_ptr(), _DTYPES[t.dtype], 0, *t.shape, *t.stride())
-    except KeyError:
-        raise FlexAttnError(6, f"{name}: unsupported dtype {t.dtype}") from None
-    except struct.error:
-        raise FlexAttnError(2, f"{name}: expected a 4-D tensor, got shape {tuple(t.shape)}") from None
-    if t.device != device:
-        raise FlexAttnError(9, f"{name} is on {t.device}, expected {device}")
-
-
-def _new_like(buf, at, x, dtype=None):
-    """A new contiguous tensor of x's shape, packed at ``at``."""
-    t = _torch.empty_like(x, dtype=dtype, memory_format=_torch.contiguous_format)
-    b, h, n, d = x.shape
-    _PACK_TENSOR(buf, at, t.data_ptr(), _DTYPES[t.dtype], 0, b, h, n, d, h * n * d, n * d, d, 1)
-    return t
-
-
-def _device_array(t, name, dtype, shape, device):
-    """Address of a contiguous ``dtype`` tensor of the given shape on ``device``
-    (the library reads it without knowing its extent)."""
-    if t.dtype != dtype:
-        raise FlexAttnError(6, f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise FlexAttnError(2, f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise FlexAttnError(9, f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise FlexAttnError(8, f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _pack_norm(buf, at, spec, name, D, device):
-    """The fa_head_norm at ``at``; its address, or None without a spec."""
-    if spec is None:
-        return None
-    w = spec.get("weight")
-    if w is None:
-        _PACK_NORM(buf, at, 0, _abi.FA_DTYPE_F32, spec.get("eps", 1e-6))
-    else:
-        _PACK_NORM(buf, at, _device_array(w, name, w.dtype, (D,), device), _DTYPES.get(w.dtype, -1),
-                   spec.get("eps", 1e-6))
-    return _addressof(buf) + at
-
-
-def _pack_rope(buf, at, spec, B, N, device):
-    if spec is None:
-        return None
-    torch = _torch
-    f = spec["inv_freq"]
-    half = f.numel()
-    ptr = rows = 0
-    pos = spec.get("pos")
-    if pos is not None:
-        rows = pos.shape[0] if pos.dim() == 2 else 1
-        if rows != 1 and rows != B:
-            raise FlexAttnError(4, f"rope pos: {rows} rows, expected 1 or {B}")
-        ptr = _device_array(pos, "rope pos", torch.int32, (rows, N) if pos.dim() == 2 else (N,), device)
-    _PACK_ROPE(buf, at, _device_array(f, "inv_freq", torch.float32, (half,), device), ptr, 2 * half,
-               1 if spec.get("interleaved") else 0, rows, 0)
-    return _addressof(buf) + at
-
-
-def _call(device, stream, fn, *args):
-    """``fn(*args, stream)`` with ``device`` current; ``stream`` None is that device's current stream."""
-    cuda = _torch.cuda
-    if cuda.current_device() != device.index:
-        with cuda.device(device):
-            return _call(device, stream, fn, *args)
-    if stream is None:
-        # the handle itself: a Stream object takes as long to build as a small kernel runs
-        handle = _torch._C._cuda_getCurrentRawStream(device.index)
-    else:
-        handle = stream if isinstance(stream, int) else stream.cuda_stream
-    status = fn(*args, handle)
-    if status:
-        _check(status)
-
-
-_PrepBuffer = C.c_char * (4 * _TENSOR + 2 * _NORM + _ROPE)
+def _native():
+    """The compiled binding of the calls below; raise if it is missing."""
+    global _BINDING
+    if _BINDING is None:
+        import torch  # noqa: F401  (its libraries come first)
+        load_library()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("the compiled binding is not built: run "
+                               "`python -m programmable_block_sparse_b200.build`") from e
+        _BINDING = _binding
+    return _BINDING
 
 
 def flexattn_qk_norm_rope(q, k, q_norm=None, k_norm=None, rope=None, q_out=None, k_out=None, stream=None):
     """Norm (per head) and rotation of queries (B, Hq, N, D) and keys
     (B, Hkv, N, D) in one pass; returns ``(q_out, k_out)``.  Either of q, k
     may be None; the outputs may be preallocated, or the inputs themselves."""
-    _load_torch()
-    x = q if q is not None else k
-    if x is None:
-        raise FlexAttnError(1, "q and k are both None")
-    dev = _cuda_device(x, "q" if q is not None else "k")
-    buf = _PrepBuffer()
-    base = _addressof(buf)
-    pq = pqo = pk = pko = None
-    if q is not None:
-        _pack_tensor(buf, 0, q, "q", dev)
-        if q_out is None:
-            q_out = _new_like(buf, 80, q)
-        else:
-            _pack_tensor(buf, 80, q_out, "q_out", dev)
-        pq, pqo = base, base + 80
-    if k is not None:
-        _pack_tensor(buf, 160, k, "k", dev)
-        if k_out is None:
-            k_out = _new_like(buf, 240, k)
-        else:
-            _pack_tensor(buf, 240, k_out, "k_out", dev)
-        pk, pko = base + 160, base + 240
-    B, _, N, D = x.shape
-    _call(dev, stream, (_LIB or load_library()).flexattn_qk_norm_rope, pq, pk, pqo, pko,
-          _pack_norm(buf, 320, q_norm, "q_norm weight", D, dev), _pack_norm(buf, 336, k_norm, "k_norm weight", D, dev),
-          _pack_rope(buf, 352, rope, B, N, dev))
-    return q_out, k_out
-
-
-_PrepBwdBuffer = C.c_char * (6 * _TENSOR + 2 * _NORM + _ROPE)
+    return (_BINDING or _native()).qk_norm_rope(q, k, q_norm, k_norm, rope, q_out, k_out, stream)
 
 
 def flexattn_qk_norm_rope_backward(q, k, dq_out, dk_out, q_norm=None, k_norm=None, rope=None, dq=None, dk=None,
@@ -620,61 +492,8 @@ def flexattn_qk_norm_rope_backward(q, k, dq_out, dk_out, q_norm=None, k_norm=Non
     inputs (needed where that side has a norm).  The weight gradients are fp32
     (D,) tensors, None without a norm or with ``weight_grads=False``; dq and dk
     are allocated in ``grad_dtype`` (default: the output gradient's type)."""
-    torch = _load_torch()
-    g = dq_out if dq_out is not None else dk_out
-    if g is None:
-        raise FlexAttnError(1, "dq_out and dk_out are both None")
-    dev = _cuda_device(g, "dq_out" if dq_out is not None else "dk_out")
-    B, _, N, D = g.shape
-    lib = _LIB or load_library()
-    buf = _PrepBwdBuffer()
-    base = _addressof(buf)
-    # both weight gradients lie in one allocation
-    want_q = dq_out is not None and q_norm is not None and weight_grads
-    want_k = dk_out is not None and k_norm is not None and weight_grads
-    dqw = dkw = None
-    if want_q or want_k:
-        dqw, dkw = g.new_empty((2, D), dtype=torch.float32).unbind()
-        if not want_q:
-            dqw = None
-        if not want_k:
-            dkw = None
-        if workspace is None:
-            n = C.c_size_t()
-            _check(lib.flexattn_qk_norm_rope_backward_workspace_size(D, 1, C.byref(n)))
-            workspace = g.new_empty((n.value,), dtype=torch.uint8)
-
-    def side(at, x, dy, dx, norm, name):
-        px = pg = po = None
-        if x is not None and norm is not None:
-            _pack_tensor(buf, at, x, name, dev)
-            px = base + at
-        if dy is not None:
-            _pack_tensor(buf, at + 80, dy, f"d{name}_out", dev)
-            if dx is None:
-                dx = _new_like(buf, at + 160, dy, grad_dtype)
-            else:
-                _pack_tensor(buf, at + 160, dx, f"d{name}", dev)
-            pg, po = base + at + 80, base + at + 160
-        return px, pg, po, dx
-
-    pq, pgq, poq, dq = side(0, q, dq_out, dq, q_norm, "q")
-    pk, pgk, pok, dk = side(240, k, dk_out, dk, k_norm, "k")
-    _call(dev, stream, lib.flexattn_qk_norm_rope_backward, pq, pk, pgq, pgk, poq, pok,
-          None if dqw is None else dqw.data_ptr(), None if dkw is None else dkw.data_ptr(),
-          _pack_norm(buf, 480, q_norm, "q_norm weight", D, dev), _pack_norm(buf, 496, k_norm, "k_norm weight", D, dev),
-          _pack_rope(buf, 512, rope, B, N, dev), None if workspace is None else workspace.data_ptr(),
-          0 if workspace is None else workspace.numel() * workspace.element_size())
-    return dq, dk, dqw, dkw
-
-
-def _scale_shape(pool, scale_block):
-    shape = pool.shape
-    return (shape[0], shape[1], -(-shape[2] // scale_block) if scale_block > 0 else 0)
-
-
-_CACHE_BYTES = 2 * _TENSOR + 48
-_AppendBuffer = C.c_char * (_CACHE_BYTES + 4 * _TENSOR + 2 * _NORM + _ROPE)
+    return (_BINDING or _native()).qk_norm_rope_backward(q, k, dq_out, dk_out, q_norm, k_norm, rope, dq, dk,
+                                                         grad_dtype, weight_grads, workspace, stream)
 
 
 def flexattn_cache_append(k, v, cache, k_norm=None, rope=None, q=None, q_norm=None, q_out=None, stream=None):
@@ -682,77 +501,24 @@ def flexattn_cache_append(k, v, cache, k_norm=None, rope=None, q=None, q_norm=No
     (updated in place), keys normed and rotated on the way; with ``q``, the
     queries of the same tokens go the same way into ``q_out``, which is
     returned (None without q)."""
-    torch = _load_torch()
-    dev = _cuda_device(k, "k")
-    B, _, N, E = k.shape
-    buf = _AppendBuffer()
-    base = _addressof(buf)
-    kp, vp, get = cache["k"], cache["v"], cache.get
-    int32 = torch.int32
-    _pack_tensor(buf, 0, kp, "cache k", dev)
-    _pack_tensor(buf, 80, vp, "cache v", dev)
-    table, new_len, ks, vs = get("page_table"), get("new_len"), get("k_scale"), get("v_scale")
-    pages = block = 0
-    ptable = pnew = pks = pvs = 0
-    if table is not None:
-        pages = table.shape[-1]
-        ptable = _device_array(table, "page_table", int32, (B, pages), dev)
-    if new_len is not None:
-        pnew = _device_array(new_len, "new_len", int32, (B,), dev)
-    if ks is not None or vs is not None:
-        block = int(get("scale_block", 0))
-        if ks is not None:
-            pks = _device_array(ks, "k_scale", torch.float32, _scale_shape(kp, block), dev)
-        if vs is not None:
-            pvs = _device_array(vs, "v_scale", torch.float32, _scale_shape(vp, block), dev)
-    _PACK_CACHE(buf, 160, ptable, _device_array(cache["cache_len"], "cache_len", int32, (B,), dev), pnew, pks, pvs,
-                pages, block)
-    _pack_tensor(buf, 208, k, "k", dev)
-    _pack_tensor(buf, 288, v, "v", dev)
-    pq = pqo = None
-    if q is not None:
-        _pack_tensor(buf, 368, q, "q", dev)
-        if q_out is None:
-            q_out = _new_like(buf, 448, q)
-        else:
-            _pack_tensor(buf, 448, q_out, "q_out", dev)
-        pq, pqo = base + 368, base + 448
-    _call(dev, stream, (_LIB or load_library()).flexattn_cache_append, base + 208, base + 288, base,
-          _pack_norm(buf, 528, k_norm, "k_norm weight", E, dev), _pack_rope(buf, 560, rope, B, N, dev), pq, pqo,
-          _pack_norm(buf, 544, q_norm, "q_norm weight", E, dev))
-    return q_out
-
-
-_Fp8Buffer = C.c_char * (4 * _TENSOR + _QUANT + 64 + 40 + 8)
-
-
-def _pack_fp8(buf, q, k, v, block_mask, quant, paged, dev):
-    """q, k, v at 0, 80, 160, quant at 320, the block mask at 344; (page table, page size, columns)."""
-    torch = _torch
-    _pack_tensor(buf, 0, q, "q", dev)
-    _pack_tensor(buf, 80, k, "k", dev)
-    _pack_tensor(buf, 160, v, "v", dev)
-    n = int(quant["scale_block"])
-    _PACK_QUANT(buf, 320, _device_array(quant["k_scale"], "k_scale", torch.float32, _scale_shape(k, n), dev),
-                _device_array(quant["v_scale"], "v_scale", torch.float32, _scale_shape(v, n), dev), n, 0)
-    m = block_mask
-    if m.kv_num_blocks.device != dev:
-        raise FlexAttnError(9, f"the block mask is on {m.kv_num_blocks.device}, expected {dev}")
-    _PACK_MASK(buf, 344, m.B, m.H, m.L, m.S, m.BM, m.BN, m.Mb, m.Nb, m.kv_num_blocks.data_ptr(),
-               m.kv_indices.data_ptr(), m.full_kv_num_blocks.data_ptr(), m.full_kv_indices.data_ptr())
-    if paged is None:
-        return 0, 0, 0
-    t = paged["page_table"]
-    return (_device_array(t, "page_table", torch.int32, (q.shape[0], t.shape[-1]), dev), int(paged["page_size"]),
-            t.shape[-1])
+    return (_BINDING or _native()).cache_append(k, v, cache, k_norm, rope, q, q_norm, q_out, stream)
 
 
 def _check_rule(spec, B, S, dev):
-    """The tensors of a mask or score rule: int32, of a known extent, on ``dev``."""
+    """The tensors of a mask or score rule: contiguous int32, of a known extent, on ``dev``."""
+    import torch
     for name, shapes in (("kv_len", ((B,),)), ("doc_id", ((S,), (1, S), (B, S))), ("pos", ((S,), (1, S), (B, S)))):
         t = spec.get(name)
-        if t is not None and not isinstance(t, str):
-            _device_array(t, name, _torch.int32, tuple(t.shape) if tuple(t.shape) in shapes else shapes[0], dev)
+        if t is None or isinstance(t, str):
+            continue
+        if t.dtype != torch.int32:
+            raise FlexAttnError(6, f"{name}: expected torch.int32, got {t.dtype}")
+        if t.shape not in shapes:
+            raise FlexAttnError(2, f"{name}: expected shape {shapes[-1]}, got {tuple(t.shape)}")
+        if t.device != dev:
+            raise FlexAttnError(9, f"{name} is on {t.device}, expected {dev}")
+        if not t.is_contiguous():
+            raise FlexAttnError(8, f"{name} must be contiguous")
     for sub in spec.get("masks", ()):
         _check_rule(sub, B, S, dev)
     if "mask" in spec:
@@ -761,16 +527,7 @@ def _check_rule(spec, B, S, dev):
 
 def flexattn_forward_fp8_workspace_size(q, k, v, block_mask, quant, split_kv=0, paged=None):
     """Workspace bytes of :func:`flexattn_forward_fp8` for these arguments (0: none)."""
-    _load_torch()
-    dev = _cuda_device(q, "q")
-    buf = _Fp8Buffer()
-    base = _addressof(buf)
-    table = _pack_fp8(buf, q, k, v, block_mask, quant, paged, dev)
-    _PACK_OPTIONS(buf, 408, 0, 0, 0, 0, *table)
-    n = C.c_size_t()
-    _check(load_library().flexattn_forward_fp8_workspace_size(base, base + 80, base + 160, base + 320, base + 344,
-                                                              int(split_kv), base + 408, C.byref(n)))
-    return n.value
+    return (_BINDING or _native()).forward_fp8_workspace_size(q, k, v, block_mask, quant, split_kv, paged)
 
 
 def flexattn_forward_fp8(q, k, v, block_mask, quant, score_mod=None, mask_mod=None, scale=None, enable_gqa=False,
@@ -781,59 +538,12 @@ def flexattn_forward_fp8(q, k, v, block_mask, quant, score_mod=None, mask_mod=No
     ``quant`` is ``{"k_scale", "v_scale": fp32 (pages or B, Hkv,
     ceil(slots / scale_block)), "scale_block": n}``.  Returns ``(out, lse)``,
     or ``(out, lse, max_scores)`` when those are requested."""
-    torch = _load_torch()
-    dev = _cuda_device(q, "q")
-    if torch.cuda.current_device() != dev.index:  # the plan is made for the device that runs it
-        with torch.cuda.device(dev):
-            return flexattn_forward_fp8(q, k, v, block_mask, quant, score_mod, mask_mod, scale, enable_gqa, out, lse,
-                                        split_kv, workspace, stream, out_dtype, max_scores, rows_guaranteed_safe,
-                                        wait_cycles, paged)
-    B, Hq, L, _ = q.shape
-    buf = _Fp8Buffer()
-    base = _addressof(buf)
-    table = _pack_fp8(buf, q, k, v, block_mask, quant, paged, dev)
-    if out is None and q.shape[3] == v.shape[3]:
-        out = _new_like(buf, 240, q, out_dtype)
-    else:
-        if out is None:
-            out = q.new_empty((B, Hq, L, v.shape[3]), dtype=out_dtype)
-        _pack_tensor(buf, 240, out, "out", dev)
-    plse = pmax = None
-    if lse is True:
-        lse = q.new_empty((B, Hq, L), dtype=torch.float32)
-        plse = lse.data_ptr()
-    elif lse is False or lse is None:
-        lse = None
-    else:
-        plse = _device_array(lse, "lse", torch.float32, (B, Hq, L), dev)
-    want_max = max_scores is not None and max_scores is not False
-    if max_scores is True:
-        max_scores = torch.empty((B, Hq, L), dtype=torch.float32, device=dev)
-        pmax = max_scores.data_ptr()
-    elif want_max:
-        pmax = _device_array(max_scores, "max_scores", torch.float32, (B, Hq, L), dev)
-    _PACK_OPTIONS(buf, 408, pmax or 0, int(wait_cycles or 0),
-                  _abi.FA_FLAG_ROWS_GUARANTEED_SAFE if rows_guaranteed_safe else 0, 0, *table)
+    native = _BINDING or _native()
     for rule in (mask_mod, score_mod):
         if rule:
-            _check_rule(rule, B, block_mask.S, dev)
+            _check_rule(rule, q.shape[0], block_mask.S, q.device)
     sm, mm = _score_struct(score_mod), _mask_struct(mask_mod)
     sc = 0.0 if scale is None or math.isnan(float(scale)) else float(scale)
-    lib = _LIB or load_library()
-    n = 0
-    if workspace is None:
-        status = lib.flexattn_forward_fp8_workspace_size(base, base + 80, base + 160, base + 320, base + 344,
-                                                         int(split_kv), base + 408, base + 448)
-        if status:
-            _check(status)
-        n = int.from_bytes(buf[448:456], "little")
-        if n > 0:
-            workspace = q.new_empty((n,), dtype=torch.uint8)
-    else:
-        n = workspace.numel() * workspace.element_size()
-    _call(dev, stream, lib.flexattn_forward_fp8, base, base + 80, base + 160, base + 320, base + 240, plse, sc,
-          1 if enable_gqa else 0, _addressof(sm), _addressof(mm), base + 344, int(split_kv), base + 408,
-          None if workspace is None else workspace.data_ptr(), n)
-    if want_max:
-        return out, lse, max_scores
-    return out, lse
+    return native.forward_fp8(q, k, v, block_mask, quant, C.addressof(sm), C.addressof(mm), sc, bool(enable_gqa), out,
+                              lse, split_kv, workspace, stream, out_dtype, max_scores, bool(rows_guaranteed_safe),
+                              int(wait_cycles or 0), paged)

@@ -127,7 +127,7 @@ PROTOTYPES = [
       C.c_void_p, C.POINTER(fa_tensor), C.POINTER(fa_tensor), C.POINTER(fa_tensor), C.c_float, C.c_int32,
       C.POINTER(fa_score_mod), C.POINTER(fa_mask_mod), C.POINTER(fa_block_mask), C.POINTER(fa_block_mask_q),
       C.c_void_p, C.c_size_t, C.c_void_p]),
-    # struct pointers as plain addresses: the binding packs all structs of a call into one buffer
+    # called through csrc/binding.cpp; structs as plain addresses
     ("flexattn_qk_norm_rope", C.c_int, [C.c_void_p] * 8),
     ("flexattn_qk_norm_rope_backward_workspace_size", C.c_int, [C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
     ("flexattn_qk_norm_rope_backward", C.c_int, [C.c_void_p] * 12 + [C.c_size_t, C.c_void_p]),

@@ -3,7 +3,8 @@
 Every ``csrc/*.cu`` is compiled to an object under ``_build/`` at the repo
 root and linked into ``programmable_block_sparse_b200/libflexattn_b200.so``.
 Objects are rebuilt when their source, or any header under ``csrc/`` or
-``include/``, is newer.  Usage: ``python -m programmable_block_sparse_b200.build``.
+``include/``, is newer.  ``csrc/binding.cpp`` is compiled with g++ against
+torch's headers into ``_binding.so`` beside the library.  Usage: ``python -m programmable_block_sparse_b200.build``.
 """
 
 from __future__ import annotations
@@ -22,6 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libflexattn_b200.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH_FLAGS + [
@@ -53,6 +56,26 @@ def _compile(nvcc, src, obj, verbose):
     return r.stderr if verbose else ""
 
 
+def _build_binding():
+    """csrc/binding.cpp -> _binding.so, next to the library it calls."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    includes = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"), sysconfig.get_paths()["include"]]
+    tmp = BINDING_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-DTORCH_EXTENSION_NAME=_binding",
+           "-DTORCH_API_INCLUDE_EXTENSION_H", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += ["-I" + d for d in includes] + [BINDING_SRC, "-o", tmp, "-L" + PKG_DIR, "-lflexattn_b200",
+                                           "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+                                           "-ltorch_cuda", "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(force=False, verbose=False, jobs=None):
     """Compile and link; returns the path of the shared library."""
     nvcc = _nvcc()
@@ -76,6 +99,9 @@ def build(force=False, verbose=False, jobs=None):
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB_PATH)
+    newest = max(os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.join(INCLUDE, "flexattn.h")))
+    if force or not os.path.exists(BINDING_PATH) or os.path.getmtime(BINDING_PATH) < newest:
+        _build_binding()
     if verbose:
         for log in logs:
             sys.stderr.write(log)
