@@ -85,6 +85,7 @@ void* array(const Tensor& t, const char* name, at::ScalarType type, at::IntArray
 // Entries of a specification dict: a borrowed reference, or null where the key
 // is absent or its value is None.
 PyObject* entry(const py::handle& spec, const char* key) {
+  if (!PyDict_Check(spec.ptr())) raise(FA_ERR_PARAM, std::string("expected a dict with ") + key);
   PyObject* v = PyDict_GetItemString(spec.ptr(), key);
   return v == nullptr || v == Py_None ? nullptr : v;
 }
@@ -135,10 +136,32 @@ const fa_rope* rope_of(const py::object& spec, int64_t B, int64_t N, c10::Device
   return r;
 }
 
-void* stream_of(const py::object& stream, c10::Device dev) {
-  if (!given(stream)) return at::cuda::getCurrentCUDAStream(dev.index()).stream();
-  const py::object handle = PyLong_Check(stream.ptr()) ? stream : py::object(stream.attr("cuda_stream"));
-  return reinterpret_cast<void*>(handle.cast<uintptr_t>());
+// A call's device and stream, current for as long as this lives: a stream that
+// the caller names is also the one that new outputs and workspaces belong to, so
+// that a workspace freed on return is not handed to other work before the
+// kernels on that stream are done with it.
+class Launch {
+ public:
+  Launch(c10::Device dev, const py::object& stream) : guard_(dev) {
+    if (!given(stream)) return;
+    const py::object handle = PyLong_Check(stream.ptr()) ? stream : py::object(stream.attr("cuda_stream"));
+    const auto raw = reinterpret_cast<cudaStream_t>(handle.cast<uintptr_t>());
+    on_.reset_stream(raw ? at::cuda::getStreamFromExternal(raw, dev.index())
+                         : at::cuda::getDefaultCUDAStream(dev.index()));
+  }
+  void* stream(c10::Device dev) const { return at::cuda::getCurrentCUDAStream(dev.index()).stream(); }
+
+ private:
+  c10::cuda::CUDAGuard guard_;
+  c10::cuda::OptionalCUDAStreamGuard on_;
+};
+
+// A workspace that the caller gave: contiguous, on the call's device.
+Tensor workspace_of(const py::object& o, c10::Device dev) {
+  Tensor t = tensor(o.ptr(), "workspace");
+  if (t.device() != dev) raise(FA_ERR_PARAM, "workspace is on " + t.device().str() + ", expected " + dev.str());
+  if (!t.is_contiguous()) raise(FA_ERR_ALIGN, "workspace must be contiguous");
+  return t;
 }
 
 Tensor like(const Tensor& x, at::ScalarType type) { return at::empty(x.sizes(), x.options().dtype(type)); }
@@ -169,7 +192,7 @@ py::tuple qk_norm_rope(const py::object& q, const py::object& k, const py::objec
   if (!given(q) && !given(k)) raise(FA_ERR_NULL, "q and k are both None");
   const Tensor x = given(q) ? tensor(q.ptr(), "q") : tensor(k.ptr(), "k");
   const c10::Device dev = cuda_device(x, given(q) ? "q" : "k");
-  const c10::cuda::CUDAGuard guard(dev);
+  const Launch launch(dev, stream);
   Given in[2], out[2];
   in[0].take(q, "q", dev);
   in[1].take(k, "k", dev);
@@ -181,7 +204,7 @@ py::tuple qk_norm_rope(const py::object& q, const py::object& k, const py::objec
   const fa_head_norm* pq = norm_of(q_norm, "q_norm weight", x.size(3), dev, &qn);
   const fa_head_norm* pk = norm_of(k_norm, "k_norm weight", x.size(3), dev, &kn);
   const fa_rope* pr = rope_of(rope, x.size(0), x.size(2), dev, &rp);
-  void* st = stream_of(stream, dev);
+  void* st = launch.stream(dev);
   int status;
   {
     py::gil_scoped_release nogil;
@@ -199,7 +222,7 @@ py::tuple qk_norm_rope_backward(const py::object& q, const py::object& k, const 
   if (!given(dq_out) && !given(dk_out)) raise(FA_ERR_NULL, "dq_out and dk_out are both None");
   const Tensor g = given(dq_out) ? tensor(dq_out.ptr(), "dq_out") : tensor(dk_out.ptr(), "dk_out");
   const c10::Device dev = cuda_device(g, given(dq_out) ? "dq_out" : "dk_out");
-  const c10::cuda::CUDAGuard guard(dev);
+  const Launch launch(dev, stream);
   if (g.dim() != 4) raise(FA_ERR_SHAPE, "expected 4-D tensors");
   const int64_t D = g.size(3);
   const py::object *xs[2] = {&q, &k}, *dys[2] = {&dq_out, &dk_out}, *dxs[2] = {&dq, &dk}, *norms[2] = {&q_norm, &k_norm};
@@ -221,19 +244,18 @@ py::tuple qk_norm_rope_backward(const py::object& q, const py::object& k, const 
   Tensor ws;
   size_t bytes = 0;
   if (given(workspace)) {
-    ws = tensor(workspace.ptr(), "workspace");
+    ws = workspace_of(workspace, dev);
     bytes = ws.nbytes();
   } else if (sums) {
     check(flexattn_qk_norm_rope_backward_workspace_size(static_cast<int32_t>(D), 1, &bytes));
     ws = at::empty({static_cast<int64_t>(bytes)}, g.options().dtype(at::kByte));
   }
-  if (ws.defined() && ws.device() != dev) raise(FA_ERR_PARAM, "workspace is on " + ws.device().str() + ", expected " + dev.str());
   fa_head_norm qn, kn;
   fa_rope rp;
   const fa_head_norm* pq = norm_of(q_norm, "q_norm weight", D, dev, &qn);
   const fa_head_norm* pk = norm_of(k_norm, "k_norm weight", D, dev, &kn);
   const fa_rope* pr = rope_of(rope, g.size(0), g.size(2), dev, &rp);
-  void* st = stream_of(stream, dev);
+  void* st = launch.stream(dev);
   float* pw[2];
   for (int i = 0; i < 2; ++i) pw[i] = dw[i].defined() ? dw[i].data_ptr<float>() : nullptr;
   void* pws = ws.defined() ? ws.data_ptr() : nullptr;
@@ -257,7 +279,7 @@ py::object cache_append(const Tensor& k, const Tensor& v, const py::dict& cache,
                         const py::object& rope, const py::object& q, const py::object& q_norm, const py::object& q_out,
                         const py::object& stream) {
   const c10::Device dev = cuda_device(k, "k");
-  const c10::cuda::CUDAGuard guard(dev);
+  const Launch launch(dev, stream);
   const fa_tensor ks = view(k, "k", dev), vs = view(v, "v", dev);
   const int64_t B = k.size(0), N = k.size(2), E = k.size(3);
   const Tensor kp = required(cache, "k"), vp = required(cache, "v");
@@ -287,7 +309,7 @@ py::object cache_append(const Tensor& k, const Tensor& v, const py::dict& cache,
   const fa_head_norm* pk = norm_of(k_norm, "k_norm weight", E, dev, &kn);
   const fa_head_norm* pq = norm_of(q_norm, "q_norm weight", E, dev, &qn);
   const fa_rope* pr = rope_of(rope, B, N, dev, &rp);
-  void* st = stream_of(stream, dev);
+  void* st = launch.stream(dev);
   int status;
   {
     py::gil_scoped_release nogil;
@@ -356,7 +378,7 @@ py::tuple forward_fp8(const Tensor& q, const Tensor& k, const Tensor& v, const p
                       const py::object& stream, const py::object& out_dtype, const py::object& max_scores,
                       bool rows_safe, int64_t wait_cycles, const py::object& paged) {
   Fp8Args a(q, k, v, block_mask, quant, paged);
-  const c10::cuda::CUDAGuard guard(a.dev);
+  const Launch launch(a.dev, stream);
   const int64_t B = q.size(0), Hq = q.size(1), L = q.size(2), Ev = v.size(3);
   const at::ScalarType type = given(out_dtype) ? out_dtype.cast<at::ScalarType>() : q.scalar_type();
   const Tensor o = given(out) ? tensor(out.ptr(), "out") : at::empty({B, Hq, L, Ev}, q.options().dtype(type));
@@ -376,14 +398,13 @@ py::tuple forward_fp8(const Tensor& q, const Tensor& k, const Tensor& v, const p
   Tensor ws;
   size_t bytes = 0;
   if (given(workspace)) {
-    ws = tensor(workspace.ptr(), "workspace");
+    ws = workspace_of(workspace, a.dev);
     bytes = ws.nbytes();
-    if (ws.device() != a.dev) raise(FA_ERR_PARAM, "workspace is on " + ws.device().str() + ", expected " + a.dev.str());
   } else {
     check(flexattn_forward_fp8_workspace_size(&a.q, &a.k, &a.v, &a.quant, &a.bm, split_kv, &a.opt, &bytes));
     if (bytes) ws = at::empty({static_cast<int64_t>(bytes)}, q.options().dtype(at::kByte));
   }
-  void* st = stream_of(stream, a.dev);
+  void* st = launch.stream(a.dev);
   float* pl = tl.defined() ? tl.data_ptr<float>() : nullptr;
   void* pws = ws.defined() ? ws.data_ptr() : nullptr;
   int status;

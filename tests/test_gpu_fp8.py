@@ -336,6 +336,39 @@ def test_two_calls_at_once():
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
 
 
+def test_workspace_of_a_named_stream():
+    """A call on a stream that is still busy, its workspace allocated inside:
+    work that the current stream is given meanwhile does not get that memory."""
+    import programmable_block_sparse_b200 as fa
+    c = Fp8Case(4, 8, 2, 1, 4096, 128, block=64, page=64, kv_len=[4096, 3000, 64, 2000], seed=3)
+    want = c.run(split_kv=7, max_scores=None)
+    bm, q = c.block_mask(), c.q.cuda()
+    size = fa.flexattn_forward_fp8_workspace_size(q, c.dev[0], c.dev[1], bm, c.quant, 7, c.paged)
+    side = torch.cuda.Stream()
+
+    def call():
+        return fa.flexattn_forward_fp8(q, c.dev[0], c.dev[1], bm, c.quant, mask_mod=c.dev_mask, enable_gqa=True,
+                                       paged=c.paged, split_kv=7, stream=side)
+
+    # The first allocations reach the driver, which may wait for the device:
+    # both streams' pools hold what is needed before the stream is made busy.
+    torch.cuda.synchronize()
+    kept = [call(), [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]]
+    torch.cuda.synchronize()
+    side_done = torch.cuda.Event()
+    side_done.record(side)
+    kept.clear()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)  # tens of milliseconds
+    out, lse = call()
+    side_done.record(side)
+    junk = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    busy = not side_done.query()
+    torch.cuda.synchronize()
+    assert len(junk) == 8 and busy
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 def test_python_refusals():
     """Rule tensors, scales and tables of other types, extents or devices."""
     import programmable_block_sparse_b200 as fa
@@ -357,6 +390,13 @@ def test_python_refusals():
     assert status(paged=dict(c.paged, page_table=c.paged["page_table"][:1])) == 2
     assert status(paged=dict(c.paged, page_table=c.paged["page_table"].t().contiguous().t())) == 8
     assert status(lse=torch.empty(2, 4, 2, device="cuda")) == 2
+    assert status(paged=[c.paged["page_table"]]) == 9
+    assert status(split_kv=2, workspace=torch.empty(1 << 20, dtype=torch.uint8)) == 9
+    assert status(split_kv=2, workspace=torch.empty((1 << 10, 2), device="cuda")[:, 0]) == 8
+    host = fa.BlockMask(**{k: v.cpu() if torch.is_tensor(v) else v for k, v in vars(bm).items()})
+    with pytest.raises(fa.FlexAttnError):
+        fa.flexattn_forward_fp8(c.q.cuda(), c.dev[0], c.dev[1], host, c.quant, mask_mod=c.dev_mask, enable_gqa=True,
+                                paged=c.paged)
     assert status(score_mod={"kind": "cap_then_bias", "cap": 5.0, "pos": torch.zeros(7, dtype=torch.int32).cuda()}) == 2
 
 
