@@ -359,7 +359,7 @@ def test_workspace_of_a_named_stream():
     side_done.record(side)
     kept.clear()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(100_000_000)  # tens of milliseconds
+        torch.cuda._sleep(400_000_000)  # about 0.2 s
     out, lse = call()
     side_done.record(side)
     junk = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
@@ -367,6 +367,35 @@ def test_workspace_of_a_named_stream():
     torch.cuda.synchronize()
     assert len(junk) == 8 and busy
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_threads():
+    """Calls from several host threads at once, each on its own stream; a call
+    that is refused in between tells its own thread only."""
+    from concurrent.futures import ThreadPoolExecutor
+    import programmable_block_sparse_b200 as fa
+    cases = [Fp8Case(2, 8, 2, 1 + i, 1024, 128, block=64, page=64, kv_len=[1024, 700 + i], seed=20 + i)
+             for i in range(4)]
+    wants = [c.run(split_kv=0, max_scores=None) for c in cases]
+    args = [(c.q.cuda(), c.dev[0], c.dev[1], c.block_mask()) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+
+    def work(i):
+        q, k, v, bm = args[i]
+        outs = []
+        for _ in range(20):
+            outs.append(fa.flexattn_forward_fp8(q, k, v, bm, cases[i].quant, mask_mod=cases[i].dev_mask,
+                                                enable_gqa=True, paged=cases[i].paged, stream=streams[i]))
+            with pytest.raises(fa.FlexAttnError):
+                fa.flexattn_forward_fp8(q, k, v, bm, cases[i].quant, enable_gqa=True, paged=[], stream=streams[i])
+        streams[i].synchronize()
+        return outs
+
+    with ThreadPoolExecutor(len(cases)) as pool:
+        results = list(pool.map(work, range(len(cases))))
+    for want, outs in zip(wants, results):
+        assert all(torch.equal(o, want[0]) and torch.equal(l, want[1]) for o, l in outs)
 
 
 def test_python_refusals():
