@@ -539,7 +539,8 @@ int flexattn_cache_append(const fa_tensor* k, const fa_tensor* v, const fa_kv_ca
 
 typedef struct fa_kv_quant {
   const float* k_scale;  /* device fp32 [num_pages or B, Hkv, ceil(size / scale_block)], as in
-                            fa_kv_cache; any finite values >= 0 (not only powers of two)     */
+                            fa_kv_cache; any finite values >= 0 (not only powers of two; what
+                            the decode kernel makes of far ones: flexattn_forward_fp8)      */
   const float* v_scale;
   int32_t scale_block;   /* as in fa_kv_cache                                                */
   int32_t reserved;      /* must be 0                                                        */
@@ -566,8 +567,10 @@ int flexattn_forward_fp8_workspace_size(const fa_tensor* q, const fa_tensor* k, 
  *   Slots at or beyond kv_len[b] are not read as numbers (NaN there, in codes or
  *       scales, is harmless), nor are page ids past the last page in use; slots
  *       below it that a rule hides hold finite values (a weight of 0 times NaN
- *       is NaN).  Value scales below 2^-100 count as 2^-100.  A query row with
- *       an infinity or NaN gives NaN, in its own row only.
+ *       is NaN).  The decode kernel counts value scales below 2^-80 as 2^-80,
+ *       and a key adds nothing to out and lse once its softmax weight times
+ *       value scale is below 2^-130 of the row's largest such product.  A query
+ *       row with an infinity or NaN gives NaN, in its own row only.
  *   split_kv: as in flexattn_forward, for the decode kernel.
  * Errors: those of flexattn_forward. */
 int flexattn_forward_fp8(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const fa_kv_quant* quant,

@@ -62,6 +62,11 @@ constexpr float kNoKeyMax = -1.0e30f;
 // 2^kShift, so they stay below 2^(kSlack + kShift) = 256 < 448.
 constexpr float kSlack = 2.0f;
 constexpr float kShift = 6.0f;
+// Value scales below this one, 2^-80, count as it.  A weight's exponent carries
+// its key's value scale, so the smaller it may be, the sooner the key's share of
+// the softmax leaves fp32 beside a large scale; and the share is the weight
+// divided by the scale, 2^(8 + 80) at most, of which 2^30 keys still add up.
+constexpr float kLeastScale = 8.271806125530277e-25f;
 
 // A CTA of R = 4, 8 or 16 query rows: the softmax works on R scores a key, so
 // fewer rows are that much less work (one query of a group of 4 heads on 16
@@ -532,7 +537,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
       scales_at(kv0_1 + kk, pg_1, ks_1, vs_1);
       const int pg_2 = page_at(kv0_2 + kk);
       const int n_3 = tile_at(min(j + 3, nsub - 1));
-      vs = fmaxf(vs, 7.888609052210118e-31f);  // 2^-100: a block of zeros has scale 0
+      vs = fmaxf(vs, kLeastScale);  // a block of zeros has scale 0
       float lv, ivs;  // exact for powers of two; other errors, 2^-21, cancel but between blocks
       asm("lg2.approx.f32 %0, %1;" : "=f"(lv) : "f"(vs));
       asm("rcp.approx.f32 %0, %1;" : "=f"(ivs) : "f"(vs));

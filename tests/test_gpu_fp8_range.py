@@ -1,0 +1,86 @@
+"""Attention over an e4m3 cache where its numbers lie far apart: keys that take
+most of the weight, value scales far from one another, far positions, lists that
+reach past a sequence's end.
+
+Tolerances are those of test_gpu_fp8.py: with A_i = sum_j p_ij |v_j|, 2^-8 + 2^-12
+of A_i for out (a weight is good to 2^-8 of itself while it is above 2^-27 of its
+row's largest, and to 2^-34 of that one below: 2^-14 of A over 2^20 such keys),
+half a bf16 step of the result, and 1e-3 for lse and max_scores.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_fp8 import BF, E4, F32, Fp8Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from programmable_block_sparse_b200 import build
+    build.build()
+
+
+def finish(c, page=0, seed=0):
+    """The case's values, pools and device tensors after its codes or scales were changed."""
+    for i in range(2):
+        s = c.scales[i].double().repeat_interleave(c.block, -1)[..., :c.S, None]
+        c.vals[i] = c.codes[i].double().numpy() * s.numpy()
+        if c.kv_len is not None:
+            for b, n in enumerate(c.kv_len):
+                c.vals[i][b, :, n:] = 0
+    if page:
+        c.page = page
+        c._page(torch.Generator().manual_seed(seed))
+    c.dev = [t.cuda() for t in c.codes]
+    c.quant = {"k_scale": c.scales[0].cuda(), "v_scale": c.scales[1].cuda(), "scale_block": c.block}
+    return c
+
+
+def sink_case(L, S, code, tail, page=0, E=128, B=1, seed=0):
+    """The first key's score is (64 / sqrt(E)) * code * 2^-7 for every query, its
+    value 0; the other keys' scores are N(0, 0.9) or all 0, their values 0.5 on
+    average."""
+    c = Fp8Case(B, 8, 2, L, S, E, block=64, seed=seed)
+    g = torch.Generator().manual_seed(seed + 1)
+    c.q[..., 0] = 64
+    k = c.codes[0].float()
+    if tail == "equal":
+        k.zero_()
+    k[..., 0] = 0
+    k[:, :, 0] = 0
+    k[:, :, 0, 0] = code
+    v = torch.randn(c.codes[1].shape, generator=g) * 60 + 60
+    v[:, :, 0] = 0
+    c.codes = [k.clamp(-448, 448).to(E4), v.clamp(-448, 448).to(E4)]
+    c.scales = [torch.full_like(s, 2.0 ** -7) for s in c.scales]
+    return finish(c, page, seed)
+
+
+@pytest.mark.parametrize("L", [1, 4])
+def test_blocks_of_scale_zero_beside_large_scales(L):
+    """Keys whose values are nothing keep their share of the softmax, a sixth,
+    beside a value scale of 2^20: 4032 of them 10 nats below the first."""
+    c = sink_case(L, 4096, 224, "equal")
+    c.scales[1][:, :, 0] = 2.0 ** 20
+    c.scales[1][:, :, 1:] = 0
+    v = c.codes[1].float()
+    v[:, :, 0] = 100
+    c.codes[1] = v.to(E4)
+    finish(c)
+    c.check(c.run(split_kv=1, out_dtype=F32))
+
+
+@pytest.mark.parametrize("L", [1, 2, 4])
+def test_scales_of_zero_over_many_keys(L):
+    """All values nothing: out is 0 and lse finite, however many keys."""
+    c = Fp8Case(1, 8, 2, L, 1 << 17, 64, block=128, seed=L)
+    c.codes[0].view(torch.uint8).zero_()
+    c.scales[1].zero_()
+    finish(c)
+    out, lse, _ = c.run(split_kv=1)
+    assert out.abs().max().item() < 1e-20
+    want = np.log((1 << 17) - (L - 1) + np.arange(L))
+    assert np.abs(lse.double().cpu().numpy() - want).max() <= 1e-3
