@@ -558,12 +558,14 @@ int flexattn_forward_fp8_workspace_size(const fa_tensor* q, const fa_tensor* k, 
  *   Short queries (bf16 q on 16-byte boundaries, one query tile, 128-key tiles, E
  *       and Ev multiples of 16, 16-byte aligned codes and strides, pages of a
  *       multiple of 8 keys; up to 16 rows always, more while it is the faster
- *       way) run on the 8-bit decode kernel, which keeps q exactly (two e4m3
- *       terms a value); the softmax weights are rounded to two e4m3 terms, at
- *       most 2^-8 of each.  Other calls restore
- *       the visible part of the cache to q's type in the workspace (exact in
- *       bf16 for power-of-two scales, else rounded, 2^-8 of each value at
- *       most) and run flexattn_forward on it.
+ *       way) run on the 8-bit decode kernel.  It holds q as two e4m3 terms a
+ *       value (exact down to 2^-14 of the row's largest, off by 2^-22 of that
+ *       one at most below) and the softmax weights, times the value scales, as
+ *       three e5m2 terms: off by 2^-8 of each at most down to 2^-27 of the
+ *       row's largest, by 2^-35 of that largest one at most below.  Other calls
+ *       restore the visible part of the cache to q's type in the workspace
+ *       (exact in bf16 for power-of-two scales, else rounded, 2^-8 of each
+ *       value at most) and run flexattn_forward on it.
  *   Slots at or beyond kv_len[b] are not read as numbers (NaN there, in codes or
  *       scales, is harmless), nor are page ids past the last page in use; slots
  *       below it that a rule hides hold finite values (a weight of 0 times NaN

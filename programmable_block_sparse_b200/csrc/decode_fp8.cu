@@ -13,16 +13,21 @@
 //     rounding to 4 bits, and lo / 16, what is left, a multiple of its last
 //     place of at most 4 bits.  The sum is exact for values down to 2^-14 of
 //     the row's largest, and off by 2^-22 of that one at most below.
-//   * a softmax weight w is likewise hi + lo / 16, rounded: at most 2^-8 w, as
-//     a rounding to bf16, and a third of that in the mean square.
+//   * a softmax weight w needs range as well as precision: beside a key that
+//     takes nearly all of the weight (an attention sink) thousands of small
+//     ones make up the rest.  Two e4m3 terms end at 2^-20 of the largest.  So w
+//     is three e5m2 terms, a + b / 8 + c / 64, which beside e4m3 codes the
+//     products take as they are: e5m2 is the upper byte of fp16, so a term is
+//     the upper byte of what the terms before it leave, and only the last one
+//     is rounded.  2^-8 w at most down to 2^-27 of the row's largest weight
+//     (2^-11 w in the mean square), 2^-35 of that largest one below.
 //
-// hi and lo are columns of the small N side: 16 query rows make N = 32, 4 or 8
-// rows N = 16.  With s^k_j, s^v_j the scales of key j, c_j the codes, in log2
-// units:
+// The terms are columns of the small N side (Cfg).  With s^k_j, s^v_j the
+// scales of key j, c_j the codes, in log2 units:
 //   t_rj  = rule(s_r s^k_j scale (hi_r + lo_r / 16) . c^k_j)
-//   w_rj  = 2^(t_rj + log2 s^v_j - m_r + 6),  m_r the running maximum of
+//   w_rj  = 2^(t_rj + log2 s^v_j - m_r + 13),  m_r the running maximum of
 //           t + log2 s^v, moved when some key passes it by more than 2, so
-//           that w <= 2^8 stays inside e4m3
+//           that w <= 2^15 stays inside e5m2 (and fp16)
 //   O_r   = sum_j w_rj c^v_j,   l_r = sum_j w_rj / s^v_j,   out = O_r / l_r.
 // Carrying the value scale inside the weight keeps it out of the codes and
 // bounds the weights' rounding against the largest contribution to the output.
@@ -59,40 +64,60 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Start of the running maximum: finite and below any real score.
 constexpr float kNoKeyMax = -1.0e30f;
 // The maximum moves when a key passes it by more than kSlack; weights carry
-// 2^kShift, so they stay below 2^(kSlack + kShift) = 256 < 448.
+// 2^kShift, so they stay at or below 2^(kSlack + kShift) = 32768 < 57344.
 constexpr float kSlack = 2.0f;
-constexpr float kShift = 6.0f;
+constexpr float kShift = 13.0f;
 // Value scales below this one, 2^-80, count as it.  A weight's exponent carries
 // its key's value scale, so the smaller it may be, the sooner the key's share of
 // the softmax leaves fp32 beside a large scale; and the share is the weight
-// divided by the scale, 2^(8 + 80) at most, of which 2^30 keys still add up.
+// divided by the scale, 2^(15 + 80) at most, of which 2^30 keys still add up.
 constexpr float kLeastScale = 8.271806125530277e-25f;
 
 // A CTA of R = 4, 8 or 16 query rows: the softmax works on R scores a key, so
 // fewer rows are that much less work (one query of a group of 4 heads on 16
 // rows took 330 us where 4 rows take 232).  Sixteen rows go to two sets of four
 // softmax warps, 8 rows each, which share the tiles but nothing else.  CTAs of
-// up to 8 rows leave registers for three an SM, with rings of 4 tiles (192 KB
-// in flight an SM either way).
+// up to 8 rows leave registers for three an SM.  Rings of 4 tiles (192 KB in
+// flight an SM), or of 5 with 16 rows, whose two CTAs have larger operands.
+//
+// N side, in groups of 8 rows of 128 bytes (M = 128 takes N in 16s):
+//   Q: hi at row 0, lo at row R.
+//   weights, R = 4: a at 0, b at 4, c at 8, and 4 rows of zeros;
+//            R = 16: a at 0, b at 16, c at 32 (N = 48);
+//            R = 8: a, b and c are one group each, and N = 24 is none, so two
+//            products, (a, b) and (b, c): the second b's columns are not read.
 template <int R>
 struct Cfg {
-  static constexpr int kSets = R == 16 ? 2 : 1;          // sets of softmax warps
-  static constexpr int kOwn = R / kSets;                 // rows of a set
+  static constexpr int kSets = R == 16 ? 2 : 1;           // sets of softmax warps
+  static constexpr int kOwn = R / kSets;                  // rows of a set
   static constexpr int kThreads = 64 + 128 * kSets;
-  static constexpr int kCols = 2 * R < 16 ? 16 : 2 * R;  // N: hi at 0, lo at R (M = 128 takes N in 16s)
+  static constexpr int kQCols = 2 * R < 16 ? 16 : 2 * R;  // N of K Q^T
+  static constexpr int kWCols = R == 16 ? 48 : 16;        // N of V^T W^T
+  static constexpr int kWParts = R == 8 ? 2 : 1;          // its products
   static constexpr int kCtas = R <= 8 ? 3 : 2;
-  static constexpr int kRing = R <= 8 ? 4 : 6;           // K or V tiles of 16 KB in flight
-  static constexpr int kTmemCols = R <= 8 ? 64 : 128;    // two S^T buffers, then O^T
-  static constexpr int kOpBytes = kCols * 128;           // Q, or one buffer of weights
-  static constexpr int kSmemBytes = kRing * kTileBytes + 3 * kOpBytes + 1024;
+  static constexpr int kRing = R <= 8 ? 4 : 5;            // K or V tiles of 16 KB in flight
+  static constexpr int kO = 2 * kQCols;                   // TMEM: two S^T buffers, then O^T
+  static constexpr int kTmemCols = R <= 8 ? 64 : 128;
+  static constexpr int kQBytes = kQCols * 128;
+  static constexpr int kWBytes = R == 4 ? 2048 : 3 * R * 128;  // one of two buffers of weights
+  static constexpr int kSmemBytes = kRing * kTileBytes + kQBytes + 2 * kWBytes + 1024;
+  static_assert(kO + kWParts * kWCols <= kTmemCols, "TMEM columns");
+  // 8-column loads that take a set's columns of O^T: where the i-th begins (the
+  // set's first row added by the caller).  Four rows lie side by side.
+  static constexpr int kOLoads = R == 4 ? 2 : 3;
+  static constexpr int o_col(int i) { return R == 4 ? 8 * i : R == 8 && i == 2 ? 24 : i * R; }
+  // Where a term's weights go: bytes from the first term's, and the row that
+  // the byte's swizzle goes by (4 rows: b shares a's group).
+  static constexpr int w_bytes(int term) { return R == 4 ? (term == 2 ? 1024 : 0) : term * R * 128; }
+  static constexpr int w_row(int term) { return R == 4 && term == 1 ? 4 : 0; }
 };
 
-// kind::f8f6f4 instruction descriptor: e4m3 A and B, fp32 accumulator.
-constexpr uint32_t idesc_e4m3(int M, int N, int a_mn_major) {
-  return (1u << 4) | (static_cast<uint32_t>(a_mn_major) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
-         (static_cast<uint32_t>(M >> 4) << 24);
+// kind::f8f6f4 instruction descriptor: e4m3 A, e4m3 or e5m2 B, fp32 accumulator.
+constexpr uint32_t idesc_f8(int M, int N, int a_mn_major, int b_e5m2) {
+  return (1u << 4) | (static_cast<uint32_t>(b_e5m2) << 10) | (static_cast<uint32_t>(a_mn_major) << 15) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::
@@ -109,6 +134,25 @@ __device__ __forceinline__ void split_e4m3(float v0, float v1, uint32_t& hi, uin
   const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3);
   const float2 h = __half22float2(__half2(r));
   lo = __nv_cvt_float2_to_fp8x2(make_float2((v0 - h.x) * 16.0f, (v1 - h.y) * 16.0f), __NV_SATFINITE, __NV_E4M3);
+}
+// Two weights 0 <= v <= 2^15 as three e5m2 terms, v = a + b / 8 + c / 64: the
+// bytes 1 (v0) and 3 (v1) of each word.  The first two are cut off, so that the
+// next takes up what they leave, exactly; the last is rounded.  Few bits are left
+// by then, so ties are common: `half` sends them up (0x80 in either half) or down
+// (0x7f), by the parity of the key.  NaN stays in a.
+__device__ __forceinline__ void split_e5m2(float v0, float v1, uint32_t half, uint32_t (&term)[3]) {
+  auto bits = [](__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); };
+  auto cut = [&](__half2 x) {  // the upper byte of each half
+    const uint32_t u = bits(x) & 0xff00ff00u;
+    return *reinterpret_cast<const __half2*>(&u);
+  };
+  const __half2 eight = __float2half2_rn(8.0f);
+  const __half2 h = __floats2half2_rn(v0, v1);
+  const __half2 r = __hmul2(__hsub2(h, cut(h)), eight);
+  const __half2 q = __hmul2(__hsub2(r, cut(r)), eight);
+  term[0] = bits(h);
+  term[1] = bits(r);
+  term[2] = bits(q) + half;
 }
 
 template <int kRing>
@@ -160,6 +204,13 @@ __device__ __forceinline__ void tmem_rows(uint32_t taddr, uint32_t (&r)[2 * N]) 
 #pragma unroll
   for (int c = 0; c < 2 * N; ++c) asm volatile("" : "+r"(r[c]));  // no use is scheduled before the wait
 }
+// Likewise 8 columns of O^T.
+__device__ __forceinline__ void tmem_out(uint32_t taddr, uint32_t (&o)[8]) {
+  tmem_ld8(taddr, o);
+  tmem_wait_ld();
+#pragma unroll
+  for (int c = 0; c < 8; ++c) asm volatile("" : "+r"(o[c]));
+}
 
 // The sequence of the given rank by length of its list of tiles, longest first
 // (ties by index), for up to 32 sequences with lists of their own; else the
@@ -196,7 +247,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
                       const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, int box,
                       float* ws_o, float* ws_lse, float* ws_max) {
   using C = Cfg<R>;
-  constexpr int kRing = C::kRing, kCols = C::kCols;
+  constexpr int kRing = C::kRing;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars<kRing> bars;
   __shared__ float s_red[2][4][R];
@@ -206,7 +257,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sKV = smem;
   uint8_t* sQ = smem + kRing * kTileBytes;
-  uint8_t* sP = sQ + C::kOpBytes;
+  uint8_t* sP = sQ + C::kQBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // grid (KV head x row chunk, split, rank): the longest sequences start first
   const int split = blockIdx.y;
@@ -368,10 +419,10 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
       *reinterpret_cast<uint4*>(sQ + place(r)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       *reinterpret_cast<uint4*>(sQ + place(r + R)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
-    if (R == 4 && r >= 8)  // columns that the weights leave unused, in either buffer too
+    if (R == 4 && r >= 8)  // rows that Q leaves unused, and the weights (from 12 on) in either buffer
 #pragma unroll
       for (int buf = 0; buf < 3; ++buf)
-        *reinterpret_cast<uint4*>(sQ + buf * C::kOpBytes + place(r)) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(sQ + buf * C::kQBytes + place(r)) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
   }
   tc_fence_before();
@@ -398,8 +449,8 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA
     if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_e4m3(kKeys, kCols, 0);
-      constexpr uint32_t idesc_o = idesc_e4m3(kKeys, kCols, 1);
+      constexpr uint32_t idesc_s = idesc_f8(kKeys, C::kQCols, 0, 0);
+      constexpr uint32_t idesc_o = idesc_f8(kKeys, C::kWCols, 1, 1);
       const uint64_t dk0 = umma_desc_sw128(smem_u32(sKV), 16, 1024);
       // V^T: M runs along a row of V, one 128-byte block wide; 8 keys a group
       const uint64_t dv0 = umma_desc_sw128(smem_u32(sKV), kTileBytes, 1024);
@@ -410,8 +461,8 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
         const int e = (2 * j) % kRing, sb = j & 1;
         tc_fence_after();
         for (int kk = 0; kk < ksteps; ++kk)
-          umma_e4m3(tbase + kCols * sb, dk0 + ((e * kTileBytes + kk * 32) >> 4), dq0 + ((kk * 32) >> 4), idesc_s,
-                    kk > 0 ? 1u : 0u);
+          umma_f8(tbase + C::kQCols * sb, dk0 + ((e * kTileBytes + kk * 32) >> 4), dq0 + ((kk * 32) >> 4), idesc_s,
+                  kk > 0 ? 1u : 0u);
         umma_commit(&bars.s_full[sb]);
         umma_commit(&bars.empty[e]);
       };
@@ -419,17 +470,20 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
         const int e = (2 * j + 1) % kRing, pb = j & 1;
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 32; ++kk)
-          umma_e4m3(tbase + 2 * kCols, dv0 + ((e * kTileBytes + kk * 32 * 128) >> 4),
-                    dp0 + ((pb * C::kOpBytes + kk * 32) >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+        for (int part = 0; part < C::kWParts; ++part)  // from the second, one group of 8 rows further on
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 32; ++kk)
+            umma_f8(tbase + C::kO + part * C::kWCols, dv0 + ((e * kTileBytes + kk * 32 * 128) >> 4),
+                    dp0 + ((pb * C::kWBytes + part * 1024 + kk * 32) >> 4), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
         umma_commit(&bars.p_free[pb]);
         umma_commit(&bars.empty[e]);
       };
       // Whichever product is ready first, but QK of tile j only after PV of
       // tile j - 2: then the commit that hands over S_j (it covers everything
       // issued before) also says that the weights' buffer of tile j - 2 is free.
-      // Tile jq's K entry last held K of tile jq - kRing / 2, whose QK was issued
-      // before, and likewise for V: a tested barrier is never two phases behind.
+      // What an entry held before (kRing loads ago: K or V of tile jq - 3 at the
+      // latest, or K of tile jp - 2) went into a product that was issued before:
+      // a tested barrier is never two phases behind.
       int jq = 0, jp = 0;
       long long idle_from = clock64();
       while (jp < nsub) {
@@ -487,12 +541,12 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
       sl2[i] = make_float2(s_slope[r] * kLog2e, s_slope[r + 1] * kLog2e);
       sq2[i] = make_float2(-sl2[i].x * static_cast<float>(s_qpos[r]), -sl2[i].y * static_cast<float>(s_qpos[r + 1]));
     }
-    // where this key's weights go, by row of an 8-row group (row 4 of 4 rows is
-    // the first lo row)
+    // where the first term of this key's weights goes, by row of an 8-row group
     uint32_t wx[8];
 #pragma unroll
     for (int r = 0; r < 8; ++r)
       wx[r] = smem_u32(sP) + (row0 >> 3) * 1024 + r * 128 + (((kk >> 4) ^ r) << 4) + (kk & 15);
+    const uint32_t half = (kk & 1) ? 0x00800080u : 0x007f007fu;
     // What the next tiles need comes ahead, a stage an iteration, since each
     // load depends on the one before: tile index, page, scales.  A loaded value
     // is first touched (scaled, clamped) an iteration later: touched at once,
@@ -548,7 +602,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
       if (ok) {
         uint32_t sr[2 * N];
         tc_fence_after();
-        tmem_rows<N, R>(tbase + lane_base + kCols * sb + row0, sr);
+        tmem_rows<N, R>(tbase + lane_base + C::kQCols * sb + row0, sr);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.s_free[sb]);
@@ -660,14 +714,15 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
                                                     a.wait_cycles));
           if (alive) {
             tc_fence_after();
-            const uint32_t ot = tbase + lane_base + 2 * kCols + row0;
-            uint32_t o[2 * N];
-            tmem_rows<N, R>(ot, o);
+            const uint32_t ot = tbase + lane_base + C::kO + row0;
 #pragma unroll
-            for (int r = 0; r < 2 * N; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r % N]);
+            for (int i = 0; i < C::kOLoads; ++i) {  // one load at a time: all of them would cost spills
+              uint32_t o[8];
+              tmem_out(ot + C::o_col(i), o);
 #pragma unroll
-            for (int c = 0; c < 2 * N; c += 8)
-              tmem_st8(ot + (c < N ? c : c - N + R), *reinterpret_cast<uint32_t(*)[8]>(o + c));
+              for (int c = 0; c < 8; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[c % N]);
+              tmem_st8(ot + C::o_col(i), o);
+            }
             tmem_wait_st();
           }
         }
@@ -684,19 +739,18 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
         }
       }
       if (alive) {
-        // 4 rows: hi and lo share an 8-row group; else lo is R rows further on
-        constexpr int kLoBytes = R == 4 ? 0 : R * 128, kLoRow = R == 4 ? 4 : 0;
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
           const float2 d = add2(t[i], nms[i]);
           const float2 w = make_float2(ex2_approx(d.x), ex2_approx(d.y));
           l_part[i] = fma2(w, splat2(ivs), l_part[i]);
-          uint32_t hi, lo;
-          split_e4m3(w.x, w.y, hi, lo);
-          put_byte(wx[2 * i] + sb * C::kOpBytes, hi);
-          put_byte(wx[2 * i + 1] + sb * C::kOpBytes, hi >> 8);
-          put_byte(wx[2 * i + kLoRow] + sb * C::kOpBytes + kLoBytes, lo);
-          put_byte(wx[2 * i + 1 + kLoRow] + sb * C::kOpBytes + kLoBytes, lo >> 8);
+          uint32_t term[3];
+          split_e5m2(w.x, w.y, half, term);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            put_byte(wx[2 * i + C::w_row(k)] + sb * C::kWBytes + C::w_bytes(k), term[k] >> 8);
+            put_byte(wx[2 * i + 1 + C::w_row(k)] + sb * C::kWBytes + C::w_bytes(k), term[k] >> 24);
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -717,10 +771,14 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
     fin = named_bar_and(bar, 128, fin && !*abort);
     if (fin) {
       tc_fence_after();
-      uint32_t o[2 * N];
+      uint32_t o[8 * C::kOLoads];  // the terms a, b, c of the set's rows
 #pragma unroll
-      for (int r = 0; r < 2 * N; ++r) o[r] = 0u;
-      if (nsub > 0) tmem_rows<N, R>(tbase + lane_base + 2 * kCols + row0, o);
+      for (int c = 0; c < 8 * C::kOLoads; ++c) o[c] = 0u;
+      if (nsub > 0) {
+#pragma unroll
+        for (int i = 0; i < C::kOLoads; ++i)
+          tmem_out(tbase + lane_base + C::kO + row0 + C::o_col(i), *reinterpret_cast<uint32_t(*)[8]>(o + 8 * i));
+      }
       float lp[N];
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) {
@@ -765,7 +823,8 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
 #pragma unroll
       for (int r = 0; r < N; ++r) {
         const int64_t off = s_off[row0 + r];
-        const float val = fmaf(__uint_as_float(o[N + r]), 0.0625f, __uint_as_float(o[r])) * s_inv[row0 + r];
+        const float low = fmaf(__uint_as_float(o[2 * N + r]), 0.125f, __uint_as_float(o[N + r]));
+        const float val = fmaf(low, 0.125f, __uint_as_float(o[r])) * s_inv[row0 + r];
         if (off >= 0 && ev < a.Ev) {
           if (half_out)
             static_cast<__nv_bfloat16*>(a.out)[off + ev] = __float2bfloat16_rn(val);

@@ -59,6 +59,38 @@ def sink_case(L, S, code, tail, page=0, E=128, B=1, seed=0):
     return finish(c, page, seed)
 
 
+@pytest.mark.parametrize("split_kv", [1, 0])
+@pytest.mark.parametrize("page", [0, 64])
+@pytest.mark.parametrize("L", [1, 2, 4, 20])  # 4, 8, 16 rows a group of heads, five chunks of 16
+@pytest.mark.parametrize("code", [224, 288, 320, 352])  # 9.9, 12.7, 14.1 and 15.6 nats
+def test_many_keys_far_below_a_sink(code, L, page, split_kv):
+    c = sink_case(L, 8192, code, "normal", page)
+    c.check(c.run(split_kv=split_kv, out_dtype=F32))
+
+
+@pytest.mark.parametrize("L,S", [(1, 65536), (4, 32768)])
+@pytest.mark.parametrize("code", [192, 256, 288])
+def test_equal_keys_far_below_a_sink(code, L, S):
+    """Equal weights are rounded alike, so their errors add up."""
+    c = sink_case(L, S, code, "equal", E=64)  # 12, 16 and 18 nats
+    c.check(c.run(split_kv=1, out_dtype=F32))
+
+
+@pytest.mark.parametrize("log2", [10, 16, -16])
+@pytest.mark.parametrize("L", [1, 4])
+def test_one_block_of_values_far_from_the_others(L, log2):
+    """A block whose value scale is far from the others', its values in one channel."""
+    c = Fp8Case(2, 8, 2, L, 4096, 128, block=64, kv_len=[4096, 3000], seed=L, tail_nan=False)
+    v = c.codes[1].float()
+    v[:, :, 320:384] = 0
+    v[:, :, 320:384, 3] = 100
+    c.codes[1] = v.to(E4)
+    c.scales[1][:, :, 5] = 2.0 ** (log2 - 7)
+    finish(c)
+    for split in (1, 0):
+        c.check(c.run(split_kv=split, out_dtype=F32))
+
+
 @pytest.mark.parametrize("L", [1, 4])
 def test_blocks_of_scale_zero_beside_large_scales(L):
     """Keys whose values are nothing keep their share of the softmax, a sixth,
