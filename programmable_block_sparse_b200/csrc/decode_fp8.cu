@@ -529,7 +529,10 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
     // of a key is 2^(t + log2 s^v + nms)
     float2 nms[N / 2];
     float tm[N];
-    float2 l_part[N / 2], unit[N / 2], sl2[N / 2], sq2[N / 2];  // distance bias in log2 units: slope, slope * q
+    // Distance bias in log2 units: slope times distance.  Positions are counted
+    // from the sequence's end, where they are small for the keys that matter:
+    // the distance is exact within 2^24 of it, whatever the length.
+    float2 l_part[N / 2], unit[N / 2], sl2[N / 2], before[N / 2];  // before: the query's own, negated
 #pragma unroll
     for (int r = 0; r < N; ++r) tm[r] = -INFINITY;
 #pragma unroll
@@ -539,7 +542,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
       l_part[i] = make_float2(0.0f, 0.0f);
       unit[i] = make_float2(s_unit[r] * c_in, s_unit[r + 1] * c_in);
       sl2[i] = make_float2(s_slope[r] * kLog2e, s_slope[r + 1] * kLog2e);
-      sq2[i] = make_float2(-sl2[i].x * static_cast<float>(s_qpos[r]), -sl2[i].y * static_cast<float>(s_qpos[r + 1]));
+      before[i] = make_float2(static_cast<float>(S_b - s_qpos[r]), static_cast<float>(S_b - s_qpos[r + 1]));
     }
     // where the first term of this key's weights goes, by row of an 8-row group
     uint32_t wx[8];
@@ -607,7 +610,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.s_free[sb]);
         const float2 kfac = splat2(ks), lv2 = splat2(lv);
-        const float kvf = static_cast<float>(kv);
+        const float at = static_cast<float>(kv - S_b);
         const int pk = has_pos ? pos_at(a.score, b, kv, a.S) : kv;
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
@@ -617,7 +620,7 @@ __global__ void __launch_bounds__(Cfg<R>::kThreads, Cfg<R>::kCtas)
           if constexpr (SCORE == FA_SCORE_NONE)
             t[i] = fma2(x, f, lv2);
           else if constexpr (SCORE == FA_SCORE_ALIBI)
-            t[i] = add2(fma2(x, f, fma2(sl2[i], splat2(kvf), sq2[i])), lv2);
+            t[i] = fma2(x, f, fma2(sl2[i], add2(splat2(at), before[i]), lv2));
           else
             t[i] = mul2(x, f);
         }

@@ -116,3 +116,18 @@ def test_scales_of_zero_over_many_keys(L):
     assert out.abs().max().item() < 1e-20
     want = np.log((1 << 17) - (L - 1) + np.arange(L))
     assert np.abs(lse.double().cpu().numpy() - want).max() <= 1e-3
+
+
+@pytest.mark.parametrize("L", [1, 2, 4])
+def test_distance_bias_at_far_positions(L):
+    """lse and max_scores of a distance bias over 2^19 keys: the bias is taken
+    from the distance, so that the size of the positions does not matter."""
+    S = 1 << 19
+    c = Fp8Case(1, 8, 1, L, S, 16, block=64, score={"kind": "alibi"}, seed=L)
+    out, lse, mx = c.run()
+    q, (k, v) = c.q.double().numpy(), c.vals
+    near = 1 << 15  # slopes of 2^-8 and more: e^-128 beyond
+    sub = Fp8Case.__new__(Fp8Case)
+    sub.__dict__.update(c.__dict__)
+    sub.S, sub.vals = near, [x[:, :, -near:] for x in c.vals]
+    sub.check((out, lse, mx))
