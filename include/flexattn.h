@@ -573,7 +573,8 @@ int flexattn_forward_fp8_workspace_size(const fa_tensor* q, const fa_tensor* k, 
  *       and a key adds nothing to out and lse once its softmax weight times
  *       value scale is below 2^-130 of the row's largest such product.  A query
  *       row with an infinity or NaN gives NaN, in its own row only.
- *   split_kv: as in flexattn_forward, for the decode kernel.
+ *   split_kv: as in flexattn_forward; n > 1 takes the decode kernel for every
+ *       call that meets its requirements, whatever the number of rows.
  * Errors: those of flexattn_forward. */
 int flexattn_forward_fp8(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, const fa_kv_quant* quant,
                          const fa_tensor* out, float* lse, float scale, int32_t enable_gqa,

@@ -705,8 +705,9 @@ int prepare_fp8(const fa_tensor* q, const fa_tensor* k, const fa_tensor* v, cons
   if (paged)
     while (opt->page_size % c->box) c->box /= 2;
   plan_decode_fp8(a, split_kv, sm_count(), &c->plan);
+  // more than one split is a request for the decode kernel, as in flexattn_forward
   c->decode = q->dtype == FA_DTYPE_BF16 && bm->Mb == 1 && bm->BN == 128 && c->box >= 8 && aligned16(q) &&
-              codes_aligned16(k) && codes_aligned16(v) && prefer_decode(a, c->plan);
+              codes_aligned16(k) && codes_aligned16(v) && (split_kv > 1 || prefer_decode(a, c->plan));
   if (c->decode) {
     c->bytes = c->plan.workspace_bytes;
     return FA_OK;

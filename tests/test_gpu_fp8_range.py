@@ -131,3 +131,11 @@ def test_distance_bias_at_far_positions(L):
     sub.__dict__.update(c.__dict__)
     sub.S, sub.vals = near, [x[:, :, -near:] for x in c.vals]
     sub.check((out, lse, mx))
+
+
+@pytest.mark.parametrize("split_kv", [2, 5])
+def test_explicit_splits_of_more_rows(split_kv):
+    """More than one split is a request for the decode kernel, at every batch."""
+    for B, L in ((1, 48), (8, 48), (8, 100)):
+        c = Fp8Case(B, 16, 4, L, 640, 64, block=64, page=64, kv_len=[640 - 9 * b for b in range(B)], seed=L + B)
+        c.check(c.run(split_kv=split_kv))
