@@ -179,7 +179,8 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, const RowsIn& i
           const float fresh = pow2_scale(__uint_as_float(s_amax[par][blk]));
           const bool had = bs < sp.start;
           const float old = had ? *sc : 0.0f, now = had ? fmaxf(old, fresh) : fresh;
-          s_inv[par][blk] = now > 0.0f ? 1.0f / now : 0.0f;
+          // scale 0: nothing but zeros, infinities (+-448, not 0 * inf) and NaN
+          s_inv[par][blk] = now > 0.0f ? 1.0f / now : 1.0f;
           s_old[par][blk] = now > old ? old : -1.0f;  // -1: older codes stay as they are
           if (!had || now != old) *sc = now;
         } else {
