@@ -944,7 +944,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
 
 // Codes times scales as bf16 or fp32, 16 codes a thread, for the slots below
 // the sequence's end; the slots up to a tile past it become 0 (kernels load
-// whole tiles), the rest is not written.
+// whole tiles), and so do the values up to the last tile that the lists name
+// (lists may be older than the lengths; hidden keys are dropped by selection,
+// but their values are multiplied by 0).  The rest is not written.
 template <bool kVec>
 __global__ void __launch_bounds__(256) restore_kernel(const __grid_constant__ FwdArgs a, const QuantArgs qa,
                                                       const __grid_constant__ RestoreArgs k,
@@ -1012,6 +1014,26 @@ __global__ void __launch_bounds__(256) restore_kernel(const __grid_constant__ Fw
             static_cast<__nv_bfloat16*>(r.out)[off + e] = __float2bfloat16_rn(x[e]);
         }
     }
+  }
+  // One CTA a head and sequence looks where the lists end.
+  if (!is_v || blockIdx.x != 0 || end == a.S) return;
+  __shared__ int s_named;
+  if (threadIdx.x == 0) s_named = 0;
+  __syncthreads();
+  const int64_t rows = static_cast<int64_t>(a.bm.H) * a.bm.Mb, row0 = a.bm.B > 1 ? b * rows : 0;
+  for (int64_t row = row0 + threadIdx.x; row < row0 + rows; row += 256) {
+    const int full = __ldg(a.bm.full_kv_num_blocks + row), part = __ldg(a.bm.kv_num_blocks + row);
+    if (full > 0) atomicMax(&s_named, __ldg(a.bm.full_kv_indices + row * a.bm.Nb + full - 1) + 1);
+    if (part > 0) atomicMax(&s_named, __ldg(a.bm.kv_indices + row * a.bm.Nb + part - 1) + 1);
+  }
+  __syncthreads();
+  const int64_t last = min(static_cast<int64_t>(s_named) * a.bm.BN, static_cast<int64_t>(a.S));
+  const int64_t at = (static_cast<int64_t>(b) * a.Hkv + hk) * a.S;
+  for (int64_t i = (at + end) * r.D + threadIdx.x; i < (at + last) * r.D; i += 256) {
+    if (r.f32)
+      static_cast<float*>(r.out)[i] = 0.0f;
+    else
+      static_cast<uint16_t*>(r.out)[i] = 0;
   }
 }
 

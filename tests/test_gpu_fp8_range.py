@@ -139,3 +139,22 @@ def test_explicit_splits_of_more_rows(split_kv):
     for B, L in ((1, 48), (8, 48), (8, 100)):
         c = Fp8Case(B, 16, 4, L, 640, 64, block=64, page=64, kv_len=[640 - 9 * b for b in range(B)], seed=L + B)
         c.check(c.run(split_kv=split_kv))
+
+
+@pytest.mark.parametrize("L,qtype,E,BN", [(5, F32, 64, 128), (40, BF, 40, 128), (300, BF, 128, 128), (300, F32, 24, 100),
+                                          (3, BF, 64, 64)])
+@pytest.mark.parametrize("page", [0, 20])
+def test_lists_that_reach_past_the_end(L, qtype, E, BN, page):
+    """Lists made for the whole capacity and used at shorter lengths, over a
+    workspace of NaN: what lies past kv_len is not read as a number."""
+    import programmable_block_sparse_b200 as fa
+    S = 1000
+    c = Fp8Case(2, 4, 2, L, S, E, block=4 if page else 16, kv_len=[S, S], qtype=qtype, seed=E, tail_nan=False,
+                mask={"kind": "none"})
+    bm = c.block_mask(128, BN)
+    short = Fp8Case(2, 4, 2, L, S, E, block=4 if page else 16, page=page, kv_len=[410, 33], qtype=qtype, seed=E,
+                    mask={"kind": "none"})
+    n = fa.flexattn_forward_fp8_workspace_size(short.q.cuda(), short.dev[0], short.dev[1], bm, short.quant,
+                                               paged=short.paged)
+    ws = torch.full((max(n, 1),), 255, dtype=torch.uint8, device="cuda")
+    short.check(short.run(bm, workspace=ws), restored=True)
