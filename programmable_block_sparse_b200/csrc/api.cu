@@ -668,9 +668,10 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 // round of heads, one an SM.  Measured (us, decode / restored): 2 sequences of
 // 8k keys, 32 heads on 8: L = 64 130 / 174, L = 96 183 / 174; 8 of 4k, 16 on 4:
 // L = 32 84 / 103, L = 48 114 / 105; 1 of 32k: L = 128 405 / 543.  Head dims
-// without a tensor-core prefill stay on the decode kernel.
+// and query tiles without a tensor-core prefill stay on the decode kernel (8 of
+// 4k, 16 on 4, L = 48 in tiles of 64 rows: 115, the general kernel behind 30750).
 bool prefer_decode(const FwdArgs& a, const Fp8Plan& plan) {
-  if (a.E != a.Ev || (a.E != 64 && a.E != 128)) return true;
+  if (a.E != a.Ev || (a.E != 64 && a.E != 128) || a.bm.BM != 128) return true;
   const int64_t sms = sm_count(), rounds = (static_cast<int64_t>(a.B) * a.Hq + sms - 1) / sms;
   return static_cast<int64_t>(a.B) * a.Hkv * plan.row_chunks <= 2 * sms * rounds;
 }

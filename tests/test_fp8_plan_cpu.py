@@ -35,3 +35,12 @@ def test_explicit_splits_take_the_decode_kernel(lib, B, L):
     """Scratch for the splits' partial results, at every batch and up to a tile of rows."""
     for split in (2, 4):
         assert workspace(lib, B, 16, 4, L, 4096, 64, split) == B * 16 * L * split * (64 + 2) * 4
+
+
+@pytest.mark.parametrize("L,BM", [(48, 48), (48, 64), (100, 100), (33, 33)])
+def test_query_tiles_without_a_tensor_core_prefill_stay_on_the_decode_kernel(lib, L, BM):
+    """Where 128-row tiles go to the prefill over the restored cache, smaller
+    ones would only find the general kernel there."""
+    restored = 2 * 64 * 4 * 4096 * 64 * 2
+    assert workspace(lib, 64, 16, 4, L, 4096, 64) == restored
+    assert workspace(lib, 64, 16, 4, L, 4096, 64, BM=BM) < restored

@@ -158,3 +158,9 @@ def test_lists_that_reach_past_the_end(L, qtype, E, BN, page):
                                                paged=short.paged)
     ws = torch.full((max(n, 1),), 255, dtype=torch.uint8, device="cuda")
     short.check(short.run(bm, workspace=ws), restored=True)
+
+
+@pytest.mark.parametrize("L,BM", [(48, 48), (100, 112)])
+def test_smaller_query_tiles_of_many_rows(L, BM):
+    c = Fp8Case(8, 16, 4, L, 640, 64, block=64, page=64, kv_len=[640 - 9 * b for b in range(8)], seed=L)
+    c.check(c.run(c.block_mask(BM)))
