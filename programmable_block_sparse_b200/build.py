@@ -4,7 +4,10 @@ Every ``csrc/*.cu`` is compiled to an object under ``_build/`` at the repo
 root and linked into ``programmable_block_sparse_b200/libflexattn_b200.so``.
 Objects are rebuilt when their source, or any header under ``csrc/`` or
 ``include/``, is newer.  ``csrc/binding.cpp`` is compiled with g++ against
-torch's headers into ``_binding.so`` beside the library.  Usage: ``python -m programmable_block_sparse_b200.build``.
+torch's headers into ``_binding.so`` beside the library, again whenever torch or
+the interpreter is another one.  Where that cannot be done (no headers), the
+library is built all the same, and only the calls that go through the binding
+raise.  Usage: ``python -m programmable_block_sparse_b200.build``.
 """
 
 from __future__ import annotations
@@ -25,6 +28,7 @@ LIB_NAME = "libflexattn_b200.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
+BINDING_STAMP = os.path.join(BUILD_DIR, "binding.stamp")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH_FLAGS + [
@@ -54,6 +58,25 @@ def _compile(nvcc, src, obj, verbose):
     if r.returncode != 0:
         raise RuntimeError(f"nvcc failed for {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
     return r.stderr if verbose else ""
+
+
+def _binding_key():
+    """What the binding's ABI depends on beside its sources: torch and the interpreter."""
+    from importlib.metadata import PackageNotFoundError, version
+    try:
+        torch_version = version("torch")
+    except PackageNotFoundError:
+        torch_version = "none"
+    return f"torch {torch_version}, {sys.implementation.cache_tag}\n"
+
+
+def _binding_is_current():
+    """Newer than its sources, and built against this torch and interpreter."""
+    newest = max(os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.join(INCLUDE, "flexattn.h")))
+    if not os.path.exists(BINDING_PATH) or os.path.getmtime(BINDING_PATH) < newest or not os.path.exists(BINDING_STAMP):
+        return False
+    with open(BINDING_STAMP) as f:
+        return f.read() == _binding_key()
 
 
 def _build_binding():
@@ -99,14 +122,23 @@ def build(force=False, verbose=False, jobs=None):
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB_PATH)
-    newest = max(os.path.getmtime(BINDING_SRC), os.path.getmtime(os.path.join(INCLUDE, "flexattn.h")))
-    if force or not os.path.exists(BINDING_PATH) or os.path.getmtime(BINDING_PATH) < newest:
-        _build_binding()
     if verbose:
         for log in logs:
             sys.stderr.write(log)
+    if force or not _binding_is_current():
+        for path in (BINDING_PATH, BINDING_STAMP):  # never one of another ABI
+            if os.path.exists(path):
+                os.remove(path)
+        try:
+            _build_binding()
+        except (ImportError, OSError, RuntimeError) as e:
+            sys.stderr.write(f"the compiled binding was not built; the calls that need it will raise: {e}\n")
+        else:
+            with open(BINDING_STAMP, "w") as f:
+                f.write(_binding_key())
     return LIB_PATH
 
 
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    sys.exit(0 if os.path.exists(BINDING_PATH) else 1)
