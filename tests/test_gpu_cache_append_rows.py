@@ -1,12 +1,13 @@
-"""Appends of blocks without a finite value."""
+"""Appends of fp32 rows, and of blocks without a finite value, vs the fp64 plain
+form (tolerances: test_gpu_cache_append.py)."""
 
 import numpy as np
 import pytest
 import torch
 
 import oracle.cache_ops as co
-from test_gpu_cache_append import Setup, status
-from test_gpu_qk_prep import BF, F32, np64, randn
+from test_gpu_cache_append import Setup, run_and_check, status
+from test_gpu_qk_prep import BF, F32, half_step, inv_freq, np64, pair_size, randn
 
 pytestmark = pytest.mark.gpu
 E4 = torch.float8_e4m3fn
@@ -16,6 +17,40 @@ E4 = torch.float8_e4m3fn
 def _lib():
     from programmable_block_sparse_b200 import build
     build.build()
+
+
+def fp32_setup(*args, **kw):
+    s = Setup(*args, **kw)
+    s.k, s.v = (randn(i, *t.shape, dtype=F32).cuda() for i, t in ((31, s.k), (32, s.v)))
+    return s
+
+
+@pytest.mark.parametrize("pool,block", [(BF, 0), (F32, 0), (E4, 16), (E4, 64), (E4, 128)],
+                         ids=["bf16", "fp32", "e4m3_16", "e4m3_64", "e4m3_128"])
+@pytest.mark.parametrize("E,Ev,rot,inter", [(128, 128, 128, False), (64, 64, 32, True), (80, 128, 40, False),
+                                            (128, 64, 0, False), (13, 7, 6, False)])
+@pytest.mark.parametrize("N,start,count", [(1, [0, 5, 127], None), (37, [60, 0, 9], [37, 0, 30])])
+def test_fp32_rows(pool, block, E, Ev, rot, inter, N, start, count):
+    page = max(block, 16)
+    s = fp32_setup(3, 2, N, E, Ev, pool, page, -(-170 // page), block=block, seed=E + N)
+    rope = {"inv_freq": inv_freq(rot).cuda(), "interleaved": inter} if rot else None
+    run_and_check(s, start, count, k_norm={"weight": (1 + randn(9, E, dtype=F32)).cuda()}, rope=rope)
+
+
+@pytest.mark.parametrize("D", [64, 128, 20])
+def test_fp32_queries_in_the_same_launch(D):
+    import programmable_block_sparse_b200 as fa
+    N, start = 21, [9, 0]
+    s = fp32_setup(2, 2, N, D, D, E4, 32, 2, block=32, seed=D)
+    q = randn(11, 2, N, 6, D, dtype=F32).cuda().transpose(1, 2)
+    w, f = (1 + randn(12, D)).cuda(), inv_freq(D).cuda()
+    pos = np.array(start)[:, None] + np.arange(N)
+    ref = co.norm_rope(np64(q), pos, np64(f), norm=True, weight=np64(w))
+    size = pair_size(co.norm_rope(np64(q), norm=True, weight=np64(w)), D, False)
+    for out in (None, torch.empty(q.shape, dtype=BF, device="cuda")):
+        got = fa.flexattn_cache_append(s.k, s.v, s.spec(start), rope={"inv_freq": f}, q=q, q_norm={"weight": w}, q_out=out)
+        assert got.dtype == (F32 if out is None else BF)
+        assert np.all(np.abs(np64(got) - ref) <= 2.0 ** -20 * size + half_step(got.dtype, ref)) and status() == 0
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "fp32"])

@@ -160,6 +160,20 @@ def test_lists_that_reach_past_the_end(L, qtype, E, BN, page):
     short.check(short.run(bm, workspace=ws), restored=True)
 
 
+@pytest.mark.parametrize("L", [1, 4])
+def test_wait_budget_does_run_out(L):
+    """A budget of one cycle gives up in every part of the kernel (one and two
+    sets of softmax warps), and the next call is as good as ever."""
+    import programmable_block_sparse_b200 as fa
+    c = Fp8Case(2, 8, 2, L, 4096, 128, block=64, kv_len=[4096, 4000], seed=1)
+    bm = c.block_mask()
+    fa.flexattn_forward_fp8(c.q.cuda(), c.dev[0], c.dev[1], bm, c.quant, mask_mod=c.dev_mask, enable_gqa=True,
+                            wait_cycles=1)
+    torch.cuda.synchronize()
+    assert fa.flexattn_poll_device_status() == 13
+    c.check(c.run(bm))
+
+
 @pytest.mark.parametrize("L,BM", [(48, 48), (100, 112)])
 def test_smaller_query_tiles_of_many_rows(L, BM):
     c = Fp8Case(8, 16, 4, L, 640, 64, block=64, page=64, kv_len=[640 - 9 * b for b in range(8)], seed=L)
