@@ -444,8 +444,9 @@ typedef struct fa_rope {
  *   q_norm, k_norm: NULL for no norm.  rope: NULL for no rotation.  At least
  *       one of the three is given.
  * An output may be its own input (same base, strides and type); other overlaps
- * are not supported.  The arithmetic is fp32; the result is rounded once, to
- * the output's type.
+ * are not supported.  The arithmetic is fp32, squares included (rows with
+ * magnitudes above 2^60, or with eps = 0 below 2^-60 throughout, leave its
+ * range); the result is rounded once, to the output's type.
  * Errors: FA_ERR_NULL, FA_ERR_SHAPE, FA_ERR_BATCH, FA_ERR_DTYPE,
  * FA_ERR_HEADDIM, FA_ERR_ALIGN, FA_ERR_PARAM, FA_ERR_CUDA. */
 int flexattn_qk_norm_rope(const fa_tensor* q, const fa_tensor* k, const fa_tensor* q_out, const fa_tensor* k_out,
@@ -565,7 +566,9 @@ int flexattn_forward_fp8_workspace_size(const fa_tensor* q, const fa_tensor* k, 
  *       row's largest, by 2^-35 of that largest one at most below.  Other calls
  *       restore the visible part of the cache to q's type in the workspace
  *       (exact in bf16 for power-of-two scales, else rounded, 2^-8 of each
- *       value at most) and run flexattn_forward on it.
+ *       value at most) and run flexattn_forward on it; that takes
+ *       B * Hkv * S * (E + Ev) elements of q's type, S the capacity (for pages,
+ *       pages_per_seq * page_size) and not the lengths.
  *   Slots at or beyond kv_len[b] are not read as numbers (NaN there, in codes or
  *       scales, is harmless), nor are page ids past the last page in use; slots
  *       below it that a rule hides hold finite values (a weight of 0 times NaN

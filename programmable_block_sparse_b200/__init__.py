@@ -460,6 +460,8 @@ def flexattn_backward(q, k, v, out, dout, lse, block_mask, q_side=None, score_mo
 # These calls are made once a layer and token, and some of their kernels take
 # less time than a Python function that packs structs: csrc/binding.cpp does the
 # marshalling (and the checks of tensors whose extent the library cannot know).
+# Outputs and workspaces that it allocates belong to the call's stream: the
+# current one, or the one given as ``stream``.
 _BINDING = None
 
 

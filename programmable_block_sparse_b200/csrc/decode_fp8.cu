@@ -41,9 +41,10 @@
 //               is ready first.
 //   warps 2-    softmax (warp % 4 is the TMEM lane quadrant), epilogue.
 // Measured: 32 sequences of 4k..32k keys, 32 heads on 8, head dim 128: one query
-// 223 us for 1.44 GB of codes and scales (6.47 TB/s, the copy rate), four
-// queries 294 us, where the softmax of 16 rows a key is the bound; one sequence
-// of 32k keys 17.7 us, of which about 7 are a CTA's start, one tile and its end.
+// 171 us for 1.10 GB of codes and scales (6.42 TB/s, the copy rate), two
+// queries (8 rows) 184 us, four 230 us, where the softmax of 16 rows a key is the
+// bound; one sequence of 32k keys 18.6 us, of which about 7 are a CTA's start,
+// one tile and its end.
 #include <cuda_fp8.h>
 #include <math.h>
 

@@ -255,9 +255,10 @@ __device__ __forceinline__ Row<P> product(const Row<P>& x, const Row<P>& y) {
 // fp64 (pos is up to 2^31 and inv_freq a full fp32 value: in fp32 the angle of
 // a position past 10^5 would be off by a hundredth of a radian).  The fraction
 // left is rounded to fp32 for sincospif, and what that rounding drops (2^-25
-// turns at most) turns the result by its own small angle, so that the two are
-// good to their last place: keys that are rounded to e4m3 afterwards land on
-// another code than the exact ones where the fp32 error crosses a tie.
+// turns at most) turns the result by its own small angle, which leaves the error
+// of sincospif and of one fp32 operation: keys that are rounded to e4m3
+// afterwards land on another code than the exact ones where the fp32 error
+// crosses a tie.
 // Not inlined: short calls wait for instructions to arrive more than for
 // anything else.
 static __device__ __noinline__ float2 angle(int pos, float inv_freq) {
